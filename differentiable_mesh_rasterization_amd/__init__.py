@@ -11,8 +11,11 @@ libdmr.so is missing, every call raises.
     dmr_blend_fwd / dmr_blend_bwd                 the second stage
     dmr_project_fwd / dmr_project_bwd             the upstream projection
     rasterize_points_fwd / rasterize_points_bwd   point clouds
+    dmr_grouped_linear_fwd / _bwd                 linear layers, one weight per mesh (or other group)
+    dmr_orthogonalize                             orthogonalised updates of their weights
     rasterize_meshes, project_meshes,
-    rasterize_points                              autograd-aware conveniences
+    rasterize_points, grouped_linear              autograd-aware conveniences
+    orthogonalize                                 dmr_orthogonalize with its buffers allocated
 """
 
 from __future__ import annotations
@@ -39,9 +42,13 @@ EXPORTED = [
     "dmr_kernel_name", "dmr_set_kernel_timing", "dmr_set_kernel_timing_mask", "dmr_kernel_timing",
     "dmr_reset_kernel_timing", "dmr_blend_fwd", "dmr_blend_bwd", "dmr_project_fwd", "dmr_project_bwd",
     "rasterize_points_fwd", "rasterize_points_bwd", "dmr_points_workspace_min_size", "dmr_points_workspace_size_hint",
-    "rasterize_meshes_fwd_noalloc",
+    "rasterize_meshes_fwd_noalloc", "dmr_grouped_linear_fwd", "dmr_grouped_linear_bwd", "dmr_grouped_linear_workspace_size",
+    "dmr_orthogonalize", "dmr_orthogonalize_workspace_size",
 ]
 DMR_NOALLOC_SCRATCH_BYTES = 128 << 20
+DMR_MAX_LINEAR_WIDTH = 1 << 20
+DMR_MAX_ORTHOGONALIZE_STEPS = 64
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # dmr_dtype
 
 
 class DmrError(RuntimeError):
@@ -123,6 +130,16 @@ def lib(path: Optional[str] = None):
     L.dmr_points_workspace_min_size.argtypes = [I64, I64, I32, I32]
     L.dmr_points_workspace_size_hint.restype = SZ
     L.dmr_points_workspace_size_hint.argtypes = [I64, I64, I32, I32, I32, ctypes.c_float]
+    L.dmr_grouped_linear_fwd.restype = ctypes.c_int
+    L.dmr_grouped_linear_fwd.argtypes = [P, I64, I32, P, I64, P, P, I32, ctypes.c_int, P, P]
+    L.dmr_grouped_linear_bwd.restype = ctypes.c_int
+    L.dmr_grouped_linear_bwd.argtypes = [P, I64, I32, P, I64, P, I32, ctypes.c_int, P, P, P, P, P, SZ, P]
+    L.dmr_grouped_linear_workspace_size.restype = SZ
+    L.dmr_grouped_linear_workspace_size.argtypes = [I64, I64, I32, I32, ctypes.c_int]
+    L.dmr_orthogonalize.restype = ctypes.c_int
+    L.dmr_orthogonalize.argtypes = [P, I64, I32, I32, ctypes.c_int, I32, ctypes.c_float, P, P, SZ, P]
+    L.dmr_orthogonalize_workspace_size.restype = SZ
+    L.dmr_orthogonalize_workspace_size.argtypes = [I64, I32, I32, ctypes.c_int]
     if path is None:
         _lib = L
     return L
@@ -412,6 +429,83 @@ def rasterize_points_bwd(points: torch.Tensor, cloud_offsets: torch.Tensor, H: i
         raise DmrError("rasterize_points_bwd", rc)
 
 
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _grouped_inputs(x, row_offsets, weight):
+    dev, dt = x.device, x.dtype
+    if x.dim() != 2 or weight.dim() != 3:
+        raise ValueError("x must be [R, in_features] and weight [N, out_features, in_features]")
+    R, cin = x.shape
+    N, cout, _ = weight.shape
+    _check(x, "x", dt, dev)
+    _check(row_offsets, "row_offsets", torch.int64, dev, (N + 1,))
+    _check(weight, "weight", dt, dev, (N, cout, cin))
+    return dev, dt, R, cin, N, cout, _dtype(x, "x")
+
+
+def dmr_grouped_linear_fwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor,
+                           bias: Optional[torch.Tensor], y: torch.Tensor) -> None:
+    """C-ABI layer with one weight per group of rows, on preallocated device
+    tensors (include/dmr.h): y [R, out] from x [R, in], row_offsets [N + 1]
+    int64, weight [N, out, in] and bias [N, out] or None."""
+    dev, dt, R, cin, N, cout, code = _grouped_inputs(x, row_offsets, weight)
+    _check(bias, "bias", dt, dev, (N, cout), optional=True)
+    _check(y, "y", dt, dev, (R, cout))
+    rc = lib().dmr_grouped_linear_fwd(_ptr(x), R, cin, _ptr(row_offsets), N, _ptr(weight), _ptr(bias), cout, code,
+                                      _ptr(y), _stream_handle(dev))
+    if rc != 0:
+        raise DmrError("dmr_grouped_linear_fwd", rc)
+
+
+def dmr_grouped_linear_workspace_size(R: int, N: int, in_features: int, out_features: int, dtype: torch.dtype) -> int:
+    return int(lib().dmr_grouped_linear_workspace_size(R, N, in_features, out_features, DTYPES.get(dtype, -1)))
+
+
+def dmr_grouped_linear_bwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor,
+                           grad_x: Optional[torch.Tensor], grad_weight: Optional[torch.Tensor],
+                           grad_bias: Optional[torch.Tensor], workspace: Optional[torch.Tensor] = None) -> None:
+    """C-ABI backward of the layer (include/dmr.h); each of the three
+    gradients may be None. grad_weight and grad_bias need a workspace of
+    dmr_grouped_linear_workspace_size() bytes."""
+    dev, dt, R, cin, N, cout, code = _grouped_inputs(x, row_offsets, weight)
+    _check(grad_y, "grad_y", dt, dev, (R, cout))
+    _check(grad_x, "grad_x", dt, dev, (R, cin), optional=True)
+    _check(grad_weight, "grad_weight", dt, dev, (N, cout, cin), optional=True)
+    _check(grad_bias, "grad_bias", dt, dev, (N, cout), optional=True)
+    _check(workspace, "workspace", torch.uint8, dev, optional=grad_weight is None and grad_bias is None)
+    rc = lib().dmr_grouped_linear_bwd(_ptr(x), R, cin, _ptr(row_offsets), N, _ptr(weight), cout, code, _ptr(grad_y),
+                                      _ptr(grad_x), _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace),
+                                      0 if workspace is None else workspace.numel(), _stream_handle(dev))
+    if rc != 0:
+        raise DmrError("dmr_grouped_linear_bwd", rc)
+
+
+def dmr_orthogonalize_workspace_size(B: int, m: int, n: int, dtype: torch.dtype) -> int:
+    return int(lib().dmr_orthogonalize_workspace_size(B, m, n, DTYPES.get(dtype, -1)))
+
+
+def dmr_orthogonalize(update: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, steps: int = 5,
+                      eps: float = 1e-7) -> None:
+    """C-ABI orthogonalised update on preallocated device tensors
+    (include/dmr.h): update and out [B, m, n]."""
+    dev, dt = update.device, update.dtype
+    if update.dim() != 3:
+        raise ValueError("update must be [B, m, n]")
+    B, m, n = update.shape
+    _check(update, "update", dt, dev)
+    _check(out, "out", dt, dev, (B, m, n))
+    _check(workspace, "workspace", torch.uint8, dev)
+    rc = lib().dmr_orthogonalize(_ptr(update), B, m, n, _dtype(update, "update"), int(steps), float(eps), _ptr(out),
+                                 _ptr(workspace), workspace.numel(), _stream_handle(dev))
+    if rc != 0:
+        raise DmrError("dmr_orthogonalize", rc)
+
+
 # ----------------------------------------------------------------------------
 # convenience: allocation + autograd
 # ----------------------------------------------------------------------------
@@ -560,6 +654,58 @@ def rasterize_points(points: torch.Tensor, cloud_offsets: torch.Tensor, image_si
     dists), zbuf and dists differentiable with respect to points."""
     H, W = image_size
     return _RasterizePoints.apply(points, cloud_offsets, int(H), int(W), int(points_per_pixel), float(radius))
+
+
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, row_offsets, weight, bias):
+        y = torch.empty((x.shape[0], weight.shape[1]), dtype=x.dtype, device=x.device)
+        dmr_grouped_linear_fwd(x, row_offsets, weight, bias, y)
+        ctx.save_for_backward(x, row_offsets, weight)
+        return y
+
+    @staticmethod
+    def backward(ctx, g):
+        x, row_offsets, weight = ctx.saved_tensors
+        N, cout, cin = weight.shape
+        need_x, _, need_w, need_b = ctx.needs_input_grad
+        gx = torch.empty_like(x) if need_x else None
+        gw = torch.empty_like(weight) if need_w else None
+        gb = torch.empty((N, cout), dtype=weight.dtype, device=weight.device) if need_b else None
+        ws = None
+        if need_w or need_b:
+            ws = torch.empty(dmr_grouped_linear_workspace_size(x.shape[0], N, cin, cout, x.dtype), dtype=torch.uint8,
+                             device=x.device)
+        dmr_grouped_linear_bwd(x, row_offsets, weight, g.contiguous(), gx, gw, gb, ws)
+        return gx, None, gw, gb
+
+
+def grouped_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y_r = W_n x_r + b_n for the rows r of every group n (a mesh's
+    vertices, an image's pixels): x [R, in], row_offsets [N + 1] int64,
+    weight [N, out, in], bias [N, out], all of one type (float32, float16 or
+    bfloat16). Differentiable with respect to x, weight and bias."""
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
+        return _GroupedLinear.apply(x, row_offsets, weight, bias)
+    y = torch.empty((x.shape[0], weight.shape[1]), dtype=x.dtype, device=x.device)
+    dmr_grouped_linear_fwd(x, row_offsets, weight, bias, y)
+    return y
+
+
+def orthogonalize(update: torch.Tensor, steps: int = 5, eps: float = 1e-7) -> torch.Tensor:
+    """The nearest thing to an orthogonal matrix in the direction of each
+    matrix of `update` [B, m, n] (or [m, n]), by `steps` Newton-Schulz
+    products: what an optimiser applies in place of a weight's momentum. Not
+    differentiable."""
+    u = update.detach()
+    u = u if u.dim() == 3 else u.unsqueeze(0)
+    out = torch.empty_like(u)
+    if u.dim() != 3:
+        raise ValueError("update must be [B, m, n] or [m, n]")
+    ws = torch.empty(dmr_orthogonalize_workspace_size(*u.shape, u.dtype), dtype=torch.uint8, device=u.device)
+    dmr_orthogonalize(u, out, ws, steps, eps)
+    return out.view(update.shape)
 
 
 # ----------------------------------------------------------------------------

@@ -38,6 +38,7 @@ std::atomic<uint32_t> g_timing_mask{0};
 const char* const kKernelNames[kKernelCount] = {
     "zero_fwd", "face_setup_count", "bin_scan", "bin_fill", "bin_sort", "fine_raster", "zero_grad", "backward_slots",
     "blend_fwd", "blend_bwd", "project_fwd", "project_bwd", "point_setup", "point_raster", "point_bwd",
+    "grouped_linear_fwd", "grouped_linear_bwd", "orthogonalize",
 };
 
 hipEvent_t take_event() {
@@ -462,6 +463,103 @@ dmr_status rasterize_points_bwd(const float* points, int64_t P, const int64_t* c
     a.points = points; a.P = P; a.N = N; a.H = H; a.W = W; a.K = K;
     a.idx = idx; a.gz = grad_zbuf; a.gd = grad_dists; a.grad_points = grad_points; a.stream = stream;
     return launch_points_backward(a) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+namespace {
+
+dmr_status check_grouped(int64_t R, int32_t cin, int64_t N, int32_t cout, dmr_dtype dtype, const int64_t* off) {
+    if (R < 0 || N < 0 || cin < 1 || cout < 1) return DMR_ERROR_INVALID_VALUE;
+    if (dtype != DMR_FLOAT32 && dtype != DMR_FLOAT16 && dtype != DMR_BFLOAT16) return DMR_ERROR_INVALID_VALUE;
+    if (cin > DMR_MAX_LINEAR_WIDTH || cout > DMR_MAX_LINEAR_WIDTH) return DMR_ERROR_UNSUPPORTED;
+    // tiles are counted in 32 bits (at least 16 rows a tile, and one for each group)
+    const int64_t columns = (int64_t)(cin > cout ? cin : cout) / 16 + 1;
+    const int64_t weight_tiles = ((int64_t)cin / 64 + 1) * ((int64_t)cout / 64 + 1);
+    const int64_t most = (int64_t)INT32_MAX - 8;
+    if (R > INT64_MAX / ((int64_t)DMR_MAX_LINEAR_WIDTH * 4)) return DMR_ERROR_UNSUPPORTED;
+    if (N > most / 64 || N > most / columns || N > most / weight_tiles) return DMR_ERROR_UNSUPPORTED;
+    if (R / 16 + N > most / columns || R / 512 + N > most / weight_tiles) return DMR_ERROR_UNSUPPORTED;
+    if (N > 0 && off == nullptr) return DMR_ERROR_INVALID_VALUE;
+    if (R > 0 && N == 0) return DMR_ERROR_INVALID_VALUE;
+    return DMR_SUCCESS;
+}
+
+}  // namespace
+
+dmr_status dmr_grouped_linear_fwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                  const void* weight, const void* bias, int32_t out_features, dmr_dtype dtype, void* y,
+                                  hipStream_t stream) {
+    dmr_status st = check_grouped(R, in_features, N, out_features, dtype, row_offsets);
+    if (st != DMR_SUCCESS) return st;
+    if (R == 0) return DMR_SUCCESS;
+    if (!x || !weight || !y) return DMR_ERROR_INVALID_VALUE;
+    GroupedLinearArgs a{};
+    a.x = x; a.R = R; a.cin = in_features; a.off = row_offsets; a.N = N; a.weight = weight; a.bias = bias;
+    a.cout = out_features; a.dtype = dtype; a.y = y; a.stream = stream;
+    return launch_grouped_linear_forward(a) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype) {
+    static const int64_t none = 0;
+    if (check_grouped(R, in_features, N, out_features, dtype, &none) != DMR_SUCCESS) return 0;
+    const int64_t values = (int64_t)in_features * out_features + out_features;
+    return align_up((size_t)(grouped_pieces(R, N, in_features, out_features).slots * values) * sizeof(float) + 256, 256);
+}
+
+dmr_status dmr_grouped_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                  const void* weight, int32_t out_features, dmr_dtype dtype, const void* grad_y,
+                                  void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+    dmr_status st = check_grouped(R, in_features, N, out_features, dtype, row_offsets);
+    if (st != DMR_SUCCESS) return st;
+    const bool sums = grad_weight || grad_bias;
+    if (R > 0 && !grad_y) return DMR_ERROR_INVALID_VALUE;
+    if (R > 0 && ((grad_x && !weight) || (sums && !x))) return DMR_ERROR_INVALID_VALUE;
+    if (N == 0 || !(grad_x || sums)) return DMR_SUCCESS;
+    if (sums) {
+        if (workspace == nullptr ||
+            workspace_bytes < dmr_grouped_linear_workspace_size(R, N, in_features, out_features, dtype))
+            return DMR_ERROR_WORKSPACE_TOO_SMALL;
+        if (!ws_aligned(workspace)) return DMR_ERROR_INVALID_VALUE;
+    }
+    GroupedLinearArgs a{};
+    a.x = x; a.R = R; a.cin = in_features; a.off = row_offsets; a.N = N; a.weight = weight; a.cout = out_features;
+    a.dtype = dtype; a.grad_y = grad_y; a.grad_x = grad_x; a.grad_weight = grad_weight; a.grad_bias = grad_bias;
+    a.workspace = static_cast<float*>(workspace); a.stream = stream;
+    return launch_grouped_linear_backward(a) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+namespace {
+
+dmr_status check_orthogonalize(int64_t B, int32_t m, int32_t n, dmr_dtype dtype) {
+    if (B < 0 || m < 1 || n < 1) return DMR_ERROR_INVALID_VALUE;
+    if (dtype != DMR_FLOAT32 && dtype != DMR_FLOAT16 && dtype != DMR_BFLOAT16) return DMR_ERROR_INVALID_VALUE;
+    if (m > DMR_MAX_LINEAR_WIDTH || n > DMR_MAX_LINEAR_WIDTH) return DMR_ERROR_UNSUPPORTED;
+    if (B > 0 && orthogonalize_workspace(B, m, n, dtype) == 0) return DMR_ERROR_UNSUPPORTED;
+    return DMR_SUCCESS;
+}
+
+}  // namespace
+
+size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dtype dtype) {
+    if (check_orthogonalize(B, m, n, dtype) != DMR_SUCCESS) return 0;
+    return B > 0 ? orthogonalize_workspace(B, m, n, dtype) : 256;
+}
+
+dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n, dmr_dtype dtype, int32_t steps, float eps,
+                             void* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    dmr_status st = check_orthogonalize(B, m, n, dtype);
+    if (st != DMR_SUCCESS) return st;
+    if (steps < 1 || !isfinite(eps) || !(eps > 0.0f)) return DMR_ERROR_INVALID_VALUE;
+    if (steps > DMR_MAX_ORTHOGONALIZE_STEPS) return DMR_ERROR_UNSUPPORTED;
+    if (B == 0) return DMR_SUCCESS;
+    if (!update || !out) return DMR_ERROR_INVALID_VALUE;
+    if (workspace == nullptr || workspace_bytes < orthogonalize_workspace(B, m, n, dtype))
+        return DMR_ERROR_WORKSPACE_TOO_SMALL;
+    if (!ws_aligned(workspace)) return DMR_ERROR_INVALID_VALUE;
+    OrthogonalizeArgs a{};
+    a.update = update; a.B = B; a.m = m; a.n = n; a.dtype = dtype; a.steps = steps; a.eps = eps; a.out = out;
+    a.workspace = static_cast<char*>(workspace); a.stream = stream;
+    return launch_orthogonalize(a) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
 }
 
 dmr_status dmr_workspace_stats(const void* workspace, dmr_stats* out, hipStream_t stream) {

@@ -345,6 +345,9 @@ enum KernelId : int32_t {
     kKPointSetup,
     kKPointRaster,
     kKPointBwd,
+    kKGroupedLinearFwd,
+    kKGroupedLinearBwd,
+    kKOrthogonalize,
     kKernelCount
 };
 
@@ -422,6 +425,36 @@ hipError_t launch_point_setup(const FwdArgs& a, PointRec* recs, FaceBin* fbin, i
 hipError_t launch_points_forward(const FwdArgs& a);
 hipError_t launch_points_backward(const PointBwdArgs& a);
 hipError_t launch_project_backward(const ProjectArgs& a);
+
+struct GroupedLinearArgs {
+    const void* x; int64_t R; int32_t cin;
+    const int64_t* off; int64_t N;
+    const void* weight; const void* bias; int32_t cout;
+    dmr_dtype dtype;
+    void* y;                                                           // forward
+    const void* grad_y; void* grad_x; void* grad_weight; void* grad_bias;   // backward
+    float* workspace;
+    hipStream_t stream;
+};
+// How the backward pass cuts long groups' rows: rows of a piece, and the
+// float32 partial results that the workspace holds.
+struct GroupedPieces {
+    int rows;
+    int64_t slots;
+};
+GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout);
+hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a);
+hipError_t launch_grouped_linear_backward(const GroupedLinearArgs& a);
+
+struct OrthogonalizeArgs {
+    const void* update; int64_t B; int32_t m, n;
+    dmr_dtype dtype;
+    int32_t steps; float eps;
+    void* out; char* workspace;
+    hipStream_t stream;
+};
+size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n, dmr_dtype dtype);   // 0: too large
+hipError_t launch_orthogonalize(const OrthogonalizeArgs& a);
 
 // Timing hooks (api.hip).
 void timing_begin(KernelId id, hipStream_t s);

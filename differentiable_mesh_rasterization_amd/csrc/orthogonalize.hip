@@ -1,0 +1,609 @@
+// Orthogonalised updates on gfx950: for every matrix U [m, n] of a batch
+//     X = U / (|U|_F + eps), then `steps` times
+//     A = X X^T,  B = b A + c A A,  X <- a X + B X
+// with X [s, l] (s = min(m, n); U is taken transposed when m > n).
+//
+// The products run on the matrix cores in float16 with float32 sums. All
+// values are bounded (the largest singular value of X stays below 1.21), so
+// powers of two keep float16 away from its limits (fixed ones, but that an
+// update whose norm is far below eps is lifted: see lift_of). Two things keep
+// the result exact to more than 11 bits:
+//   the diagonals of A and B are kept apart in float32. They are the large
+//   entries (A tends to a matrix near the identity, where a X + B X cancels:
+//   a + b + c = 0.70 out of 3.44), and with A = D + O, D diagonal,
+//       (A A)_ij = (O O)_ij + (d_i + d_j) O_ij,   i != j,
+//       (A A)_ii = (O O)_ii + d_i^2,
+//       X <- (a + B_ii) X_i + (off-diagonal B) X;
+//   X, O and the off-diagonal B are pairs of float16, high + low (22 bits).
+// With PLANES = 2 (float32 and float16 updates) a product is high high +
+// high low + low high, as exact as float32 products at three times the cost of
+// one; with PLANES = 1 (bfloat16 updates) only the high parts are multiplied,
+// and X alone carries its low part. Against the definition in 64 bits on
+// matrices of 64 to 2048 that gives 0.6 times the error of float32 products,
+// and for bfloat16 an error of about a third of its output rounding.
+#include "dmr_internal.h"
+#include "mfma_tile.h"
+
+namespace dmr {
+namespace {
+
+typedef _Float16 h16;
+typedef h16 h16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScaleX = 16384.0f, kScaleO = 16384.0f, kScaleB = 8192.0f;
+
+// ---------------------------------------------------------------------------
+// matrices that fit into one workgroup's LDS: one workgroup each, one launch
+// ---------------------------------------------------------------------------
+// Everything is float32, on the float32 matrix instructions: the whole
+// iteration of such a matrix costs less than the launches of the tiled form.
+
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallLds = 150 * 1024;
+constexpr int kSmallUpdateTiles = 10;   // 16 x 16 tiles of X a wave holds
+
+struct SmallShape {
+    int s, l, sp, lp, ldx, lda;
+    size_t bytes;
+};
+__host__ __device__ __forceinline__ SmallShape small_shape(int m, int n) {
+    SmallShape h;
+    h.s = m < n ? m : n;
+    h.l = m < n ? n : m;
+    h.sp = (h.s + 15) / 16 * 16;
+    h.lp = (h.l + 15) / 16 * 16;
+    h.ldx = h.lp + 4;   // rows 16 bytes past a multiple of 64: fragment reads spread over the banks
+    h.lda = h.sp + 4;
+    h.bytes = ((size_t)h.sp * h.ldx + (size_t)h.sp * h.lda) * sizeof(float);
+    return h;
+}
+
+bool is_small(int m, int n) {
+    if ((int64_t)m * n > 40000) return false;
+    const SmallShape h = small_shape(m, n);
+    return h.sp <= 64 && h.bytes <= (size_t)kSmallLds &&
+           (h.sp / 16) * (h.lp / 16) <= kSmallUpdateTiles * kSmallWaves;
+}
+
+template <class T>
+__global__ __launch_bounds__(kSmallThreads) void orthogonalize_small(const T* __restrict__ update, int m, int n, int steps,
+                                                                     float eps, T* __restrict__ out) {
+    extern __shared__ __align__(16) float lds[];
+    __shared__ double part[kSmallWaves];
+    const SmallShape h = small_shape(m, n);
+    float* x = lds;
+    float* a = lds + h.sp * h.ldx;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, q = lane >> 4, r = lane & 15;
+    const bool turned = m > n;
+    const int64_t base = (int64_t)blockIdx.x * m * n;
+    for (int i = tid; i < h.sp * h.ldx; i += kSmallThreads) x[i] = 0.0f;
+    __syncthreads();
+    double sum = 0.0;
+    for (int i = tid; i < m * n; i += kSmallThreads) {
+        const float v = (float)update[base + i];
+        sum += (double)v * (double)v;
+        x[turned ? (i % n) * h.ldx + i / n : (i / n) * h.ldx + i % n] = v;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+    if (lane == 0) part[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; ++w) sum += part[w];
+    const float norm = (float)sqrt(sum);
+    const float inv = __builtin_isfinite(norm) ? 1.0f / (norm + eps) : __builtin_nanf("");
+    for (int i = tid; i < h.sp * h.ldx; i += kSmallThreads) x[i] *= inv;
+    __syncthreads();
+
+    const int st = h.sp / 16, lt = h.lp / 16, tri = st * (st + 1) / 2;
+    // this wave's tile of the lower triangle of A and B
+    int ti = 0;
+    while ((ti + 1) * (ti + 2) / 2 <= wave) ++ti;
+    const int tj = wave - ti * (ti + 1) / 2;
+    const bool gram = wave < tri;
+    for (int step = 0; step < steps; ++step) {
+        f32x4 acc;
+        for (int poly = 0; poly < 2; ++poly) {
+            const float* from = poly ? a : x;
+            const int ld = poly ? h.lda : h.ldx, K = poly ? h.sp : h.lp;
+            if (gram) {
+                acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                const float* pj = from + (tj * 16 + r) * ld + 4 * q;
+                const float* pi = from + (ti * 16 + r) * ld + 4 * q;
+                for (int k = 0; k < K; k += 16)
+                    acc = mma<float>(*reinterpret_cast<const u32x4*>(pj + k), *reinterpret_cast<const u32x4*>(pi + k), acc);
+                if (poly)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] = kB * a[(ti * 16 + r) * h.lda + tj * 16 + 4 * q + i] + kC * acc[i];
+            }
+            __syncthreads();   // poly: all of A has been read
+            if (gram) {
+                // this lane: row ti 16 + r, columns tj 16 + 4 q + i, and the mirrored entries
+                *reinterpret_cast<f32x4*>(a + (ti * 16 + r) * h.lda + tj * 16 + 4 * q) = acc;
+                if (ti != tj)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[(tj * 16 + 4 * q + i) * h.lda + ti * 16 + r] = acc[i];
+            }
+            __syncthreads();
+        }
+        f32x4 next[kSmallUpdateTiles];
+#pragma unroll
+        for (int u = 0; u < kSmallUpdateTiles; ++u) {
+            const int tile = wave + u * kSmallWaves;
+            if (tile >= st * lt) continue;
+            const int xi = tile % st, xj = tile / st;
+            f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < h.sp; k += 16) {
+                u32x4 p;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    p[j] = __builtin_bit_cast(uint32_t, x[(k + 4 * q + j) * h.ldx + xj * 16 + r]);
+                c = mma<float>(p, *reinterpret_cast<const u32x4*>(a + (xi * 16 + r) * h.lda + k + 4 * q), c);
+            }
+            const f32x4 old = *reinterpret_cast<const f32x4*>(x + (xi * 16 + r) * h.ldx + xj * 16 + 4 * q);
+            next[u] = kA * old + c;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kSmallUpdateTiles; ++u) {
+            const int tile = wave + u * kSmallWaves;
+            if (tile >= st * lt) continue;
+            *reinterpret_cast<f32x4*>(x + ((tile % st) * 16 + r) * h.ldx + (tile / st) * 16 + 4 * q) = next[u];
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < m * n; i += kSmallThreads)
+        out[base + i] = (T)x[turned ? (i % n) * h.ldx + i / n : (i / n) * h.ldx + i % n];
+}
+
+// ---------------------------------------------------------------------------
+// the tiled form
+// ---------------------------------------------------------------------------
+
+// Sides are padded to multiples of kPad with zeros, which the iteration
+// keeps; the planes below are [sp, lp] or [sp, sp].
+constexpr int kPad = 64;
+constexpr int kNormBlocks = 64;
+
+struct Layout {
+    int s, l, sp, lp;
+    int64_t xs, as;          // values of a plane of X, of A
+    int64_t xhi[2], xlo[2], ohi, olo, bhi, blo, diag, bdiag, norm, lift;   // byte offsets, each for the whole batch
+    size_t bytes;
+};
+
+Layout layout(int64_t B, int m, int n, bool two) {
+    Layout w{};
+    w.s = m < n ? m : n;
+    w.l = m < n ? n : m;
+    w.sp = (w.s + kPad - 1) / kPad * kPad;
+    w.lp = (w.l + kPad - 1) / kPad * kPad;
+    w.xs = (int64_t)w.sp * w.lp;
+    w.as = (int64_t)w.sp * w.sp;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    for (int k = 0; k < 2; ++k) {
+        w.xhi[k] = take(B * w.xs * 2);
+        w.xlo[k] = take(B * w.xs * 2);
+    }
+    w.ohi = take(B * w.as * 2);
+    w.olo = two ? take(B * w.as * 2) : w.ohi;
+    w.bhi = take(B * w.as * 2);
+    w.blo = two ? take(B * w.as * 2) : w.bhi;
+    w.diag = take(B * w.sp * 4);
+    w.bdiag = take(B * w.sp * 4);
+    w.norm = take(B * kNormBlocks * 8);
+    w.lift = take(B * 4);
+    w.bytes = (size_t)at;
+    return w;
+}
+
+__device__ __forceinline__ void split(float v, h16& hi, h16& lo) {
+    hi = (h16)v;
+    lo = (h16)(v - (float)hi);
+}
+
+// X_0 has the norm t = |U| / (|U| + eps), which is tiny when |U| is far below
+// eps, and a step multiplies it by less than 4: X is held times 2^e as well,
+// with the largest e that keeps 2^e 4^steps t below 1 (or 1), so that its
+// float16 pairs do not lose it below their range. A then counts for nothing.
+__device__ __forceinline__ float lift_of(float norm, float eps, int steps) {
+    const float t = norm / (norm + eps);
+    if (!(t > 0.0f)) return 1.0f;
+    int e = 0;
+    (void)__builtin_frexpf(t, &e);   // t < 2^e
+    e = -e - 2 * steps;
+    return e > 0 ? __builtin_ldexpf(1.0f, e < 88 ? e : 88) : 1.0f;
+}
+
+// Sum of squares of a slice of each matrix (float64: no overflow, and the
+// scale is exact).
+template <class T>
+__global__ __launch_bounds__(256) void orthogonalize_norm(const T* __restrict__ update, int64_t size, double* __restrict__ norm) {
+    __shared__ double part[4];
+    const int64_t at = (int64_t)(blockIdx.x / kNormBlocks) * size;
+    double sum = 0.0;
+    for (int64_t i = (int64_t)(blockIdx.x % kNormBlocks) * 256 + threadIdx.x; i < size; i += kNormBlocks * 256) {
+        const double v = (double)(float)update[at + i];
+        sum += v * v;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) norm[blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// X_0 as float16 pairs, padded; a 64 x 64 tile a workgroup, through LDS when
+// the update is taken transposed.
+template <class T>
+__global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__ update, int m, int n, float eps,
+                                                           int steps, const double* __restrict__ norm, int sp, int lp,
+                                                           h16* __restrict__ xhi, h16* __restrict__ xlo,
+                                                           float* __restrict__ lift) {
+    __shared__ float tile[64][65];
+    __shared__ float s_inv;
+    const int tiles_l = lp / 64, tiles = tiles_l * (sp / 64);
+    const int64_t b = blockIdx.x / tiles;
+    const int i0 = (int)(blockIdx.x % tiles) / tiles_l * 64, j0 = (int)(blockIdx.x % tiles) % tiles_l * 64;
+    const int tid = threadIdx.x;
+    if (tid < 64) {
+        double sum = norm[b * kNormBlocks + tid];
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+        const float f = (float)sqrt(sum);
+        if (tid == 0) {
+            const float up = lift_of(f, eps, steps);
+            s_inv = __builtin_isfinite(f) ? kScaleX * up / (f + eps) : __builtin_nanf("");
+            if (blockIdx.x % tiles == 0) lift[b] = up;
+        }
+    }
+    const bool turned = m > n;
+    const T* u = update + b * (int64_t)m * n;
+    // rows of U along tid / 64, columns along tid % 64
+    const int r0 = turned ? j0 : i0, c0 = turned ? i0 : j0;
+    for (int r = tid >> 6; r < 64; r += 4) {
+        const int row = r0 + r, col = c0 + (tid & 63);
+        const float v = row < m && col < n ? (float)u[(int64_t)row * n + col] : 0.0f;
+        if (turned) tile[tid & 63][r] = v;
+        else tile[r][tid & 63] = v;
+    }
+    __syncthreads();
+    const float inv = s_inv;
+    for (int r = tid >> 6; r < 64; r += 4) {
+        h16 hi, lo;
+        split(tile[r][tid & 63] * inv, hi, lo);
+        const int64_t at = ((int64_t)b * sp + i0 + r) * lp + j0 + (tid & 63);
+        xhi[at] = hi;
+        xlo[at] = lo;
+    }
+}
+
+// C[m][n] = sum_k Q[m][k] P[n][k] of float16 planes; PLANES = 2 adds the
+// cross products of high and low parts.
+template <int BN_, int BM_, int WN, int WM, bool PK, int PLANES>
+struct PlanesProduct {
+    static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64;
+    static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
+    using P = OperandTile<h16, BN, PK, THREADS>;
+    using Q = OperandTile<h16, BM, true, THREADS>;
+    static constexpr int kStage = (P::kBytes + Q::kBytes) * PLANES;
+    static constexpr int kLdsBytes = 2 * kStage;
+    f32x4 acc[NT][MT];
+
+    // blocks of n are paired: a lane holds eight consecutive n of each pair
+    static __device__ __forceinline__ int n_of(int tid, int a) {
+        return ((tid >> 6) % WN) * NT * 16 + (a >> 1) * 32 + 8 * ((tid & 63) >> 4) + 4 * (a & 1);
+    }
+    static __device__ __forceinline__ int m_of(int tid, int b) {
+        return ((tid >> 6) / WN) * MT * 16 + b * 16 + (tid & 15);
+    }
+
+    static __device__ __forceinline__ void stage(char* lds, const h16* phi, const h16* plo, int ldp, int rows_n,
+                                                 const h16* qhi, const h16* qlo, int ldq, int rows_m, int k0, int K, int tid) {
+        P::template stage<true>(lds, phi, ldp, rows_n, k0, K, tid);
+        Q::template stage<true>(lds + P::kBytes * PLANES, qhi, ldq, rows_m, k0, K, tid);
+        if constexpr (PLANES == 2) {
+            P::template stage<true>(lds + P::kBytes, plo, ldp, rows_n, k0, K, tid);
+            Q::template stage<true>(lds + P::kBytes * 2 + Q::kBytes, qlo, ldq, rows_m, k0, K, tid);
+        }
+    }
+
+    __device__ __forceinline__ void multiply(const char* lds, int tid) {
+        const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            u32x4 p[PLANES][NT], q[PLANES][MT];
+#pragma unroll
+            for (int s = 0; s < PLANES; ++s) {
+#pragma unroll
+                for (int a = 0; a < NT; ++a)
+                    p[s][a] = P::fragment(lds + s * P::kBytes, kk, wn * NT * 16 + (a >> 1) * 32 + 4 * (a & 1), 8, lane);
+#pragma unroll
+                for (int b = 0; b < MT; ++b)
+                    q[s][b] = Q::fragment(lds + P::kBytes * PLANES + s * Q::kBytes, kk, (wm * MT + b) * 16, 4, lane);
+            }
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int b = 0; b < MT; ++b) {
+                    if constexpr (PLANES == 2) {
+                        acc[a][b] = mma<h16>(p[0][a], q[1][b], acc[a][b]);
+                        acc[a][b] = mma<h16>(p[1][a], q[0][b], acc[a][b]);
+                    }
+                    acc[a][b] = mma<h16>(p[0][a], q[0][b], acc[a][b]);
+                }
+        }
+    }
+
+    __device__ __forceinline__ void run(char* lds, const h16* phi, const h16* plo, int ldp, int rows_n, const h16* qhi,
+                                        const h16* qlo, int ldq, int rows_m, int K, int tid) {
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int b = 0; b < MT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        stage(lds, phi, plo, ldp, rows_n, qhi, qlo, ldq, rows_m, 0, K, tid);
+        staged_barrier();
+        int cur = 0;
+        for (int k0 = 0; k0 < K; k0 += P::BK) {
+            if (k0 + P::BK < K)
+                stage(lds + (cur ^ 1) * kStage, phi, plo, ldp, rows_n, qhi, qlo, ldq, rows_m, k0 + P::BK, K, tid);
+            multiply(lds + cur * kStage, tid);
+            staged_barrier();
+            cur ^= 1;
+        }
+    }
+};
+
+// Tile (ti, tj), ti >= tj, of the lower triangle.
+__device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
+    ti = (int)((__builtin_sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
+    while ((ti + 1) * (ti + 2) / 2 <= id) ++ti;
+    while (ti * (ti + 1) / 2 > id) --ti;
+    tj = id - ti * (ti + 1) / 2;
+}
+
+struct Square {   // the planes of one [sp, sp] matrix and its diagonal
+    h16 *hi, *lo;
+    float* diag;
+};
+
+// Off-diagonal pairs and the diagonal of a symmetric matrix, from the tiles
+// of its lower triangle: POLY = false: A = X X^T; true: B = b A + c A A.
+template <int BT, int WN, int WM, int PLANES, bool POLY>
+__global__ __launch_bounds__(WN * WM * 64) void orthogonalize_square(const h16* __restrict__ hi, const h16* __restrict__ lo,
+                                                                     int sp, int K, const float* __restrict__ lift,
+                                                                     const float* __restrict__ diag,
+                                                                     h16* __restrict__ out_hi, h16* __restrict__ out_lo,
+                                                                     float* __restrict__ out_diag, int tiles) {
+    using Tile = PlanesProduct<BT, BT, WN, WM, true, PLANES>;
+    __shared__ alignas(16) char lds[Tile::kLdsBytes];
+    int ti, tj;
+    const int64_t b = blockIdx.x / tiles;
+    triangle_tile((int)(blockIdx.x % tiles), ti, tj);
+    const int tid = threadIdx.x, m0 = ti * BT, n0 = tj * BT;
+    const int64_t at = b * (int64_t)sp * K, out_at = b * (int64_t)sp * sp;
+    Tile t;
+    t.run(lds, hi + at + (int64_t)n0 * K, lo + at + (int64_t)n0 * K, K, sp - n0, hi + at + (int64_t)m0 * K,
+          lo + at + (int64_t)m0 * K, K, sp - m0, K, tid);
+    out_hi += out_at;
+    out_lo += out_at;
+    out_diag += b * sp;
+    float back = 1.0f;   // undoes the lift of both factors of X X^T
+    if constexpr (POLY) diag += b * sp;
+    else back = 1.0f / (lift[b] * lift[b]);
+#pragma unroll
+    for (int a = 0; a < Tile::NT; a += 2) {
+        const int n = n0 + Tile::n_of(tid, a);
+        if (n >= sp) continue;
+#pragma unroll
+        for (int c = 0; c < Tile::MT; ++c) {
+            const int m = m0 + Tile::m_of(tid, c);
+            if (m >= sp) continue;
+            f16x8 vhi, vlo, ohi, olo;
+            float dm = 0.0f;
+            if constexpr (POLY) {
+                ohi = *reinterpret_cast<const f16x8*>(hi + at + (int64_t)m * K + n);
+                if constexpr (PLANES == 2) olo = *reinterpret_cast<const f16x8*>(lo + at + (int64_t)m * K + n);
+                dm = diag[m];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = t.acc[a + (i >> 2)][c][i & 3];
+                float off;   // the off-diagonal value, scaled
+                if constexpr (POLY) {
+                    float o = (float)ohi[i];
+                    if constexpr (PLANES == 2) o += (float)olo[i];
+                    const float dn = diag[n + i];
+                    // v = kScaleO^2 (O O)_mn, o = kScaleO O_mn
+                    off = (kC * kScaleB / (kScaleO * kScaleO)) * v + (kScaleB / kScaleO) * (kB + kC * (dm + dn)) * o;
+                    if (m == n + i) out_diag[m] = kC * (v * (1.0f / (kScaleO * kScaleO)) + dm * dm) + kB * dm;
+                } else {
+                    off = v * (kScaleO / (kScaleX * kScaleX)) * back;
+                    if (m == n + i) out_diag[m] = v * (1.0f / (kScaleX * kScaleX)) * back;
+                }
+                h16 h, l;
+                split(m == n + i ? 0.0f : off, h, l);
+                vhi[i] = h;
+                vlo[i] = l;
+                if (ti != tj) {
+                    out_hi[(int64_t)(n + i) * sp + m] = h;
+                    if constexpr (PLANES == 2) out_lo[(int64_t)(n + i) * sp + m] = l;
+                }
+            }
+            *reinterpret_cast<f16x8*>(out_hi + (int64_t)m * sp + n) = vhi;
+            if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(out_lo + (int64_t)m * sp + n) = vlo;
+        }
+    }
+}
+
+// X <- (a + B_ii) X_i + (off-diagonal B) X; the last step writes the result
+// in its own type and orientation.
+template <int BN, int BM, int WN, int WM, int PLANES>
+__global__ __launch_bounds__(WN * WM * 64) void orthogonalize_update(
+    const h16* __restrict__ bhi, const h16* __restrict__ blo, const float* __restrict__ bdiag, const h16* __restrict__ xhi,
+    const h16* __restrict__ xlo, int sp, int lp, h16* __restrict__ yhi, h16* __restrict__ ylo, int tiles_n, int tiles) {
+    using Tile = PlanesProduct<BN, BM, WN, WM, false, PLANES>;
+    __shared__ alignas(16) char lds[Tile::kLdsBytes];
+    const int64_t b = blockIdx.x / tiles;
+    const int tile = (int)(blockIdx.x % tiles);
+    const int m0 = tile / tiles_n * BM, n0 = tile % tiles_n * BN;
+    const int tid = threadIdx.x;
+    const int64_t xat = b * (int64_t)sp * lp, bat = b * (int64_t)sp * sp + (int64_t)m0 * sp;
+    Tile t;
+    t.run(lds, xhi + xat + n0, xlo + xat + n0, lp, lp - n0, bhi + bat, blo + bat, sp, sp - m0, sp, tid);
+    bdiag += b * sp;
+#pragma unroll
+    for (int a = 0; a < Tile::NT; a += 2) {
+        const int n = n0 + Tile::n_of(tid, a);
+        if (n >= lp) continue;
+#pragma unroll
+        for (int c = 0; c < Tile::MT; ++c) {
+            const int m = m0 + Tile::m_of(tid, c);
+            if (m >= sp) continue;
+            const int64_t at = xat + (int64_t)m * lp + n;
+            const f16x8 ohi = *reinterpret_cast<const f16x8*>(xhi + at), olo = *reinterpret_cast<const f16x8*>(xlo + at);
+            const float scale = kA + bdiag[m];
+            f16x8 vhi, vlo;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h16 h, l;
+                split(scale * ((float)ohi[i] + (float)olo[i]) + t.acc[a + (i >> 2)][c][i & 3] * (1.0f / kScaleB), h, l);
+                vhi[i] = h;
+                vlo[i] = l;
+            }
+            *reinterpret_cast<f16x8*>(yhi + at) = vhi;
+            *reinterpret_cast<f16x8*>(ylo + at) = vlo;
+        }
+    }
+}
+
+// The result in its own type and orientation, a 64 x 64 tile a workgroup.
+template <class T>
+__global__ __launch_bounds__(256) void orthogonalize_end(const h16* __restrict__ xhi, const h16* __restrict__ xlo, int sp,
+                                                         int lp, const float* __restrict__ lift, T* __restrict__ out, int m,
+                                                         int n) {
+    __shared__ float tile[64][65];
+    const int tiles_l = lp / 64, tiles = tiles_l * (sp / 64);
+    const int64_t b = blockIdx.x / tiles;
+    const int i0 = (int)(blockIdx.x % tiles) / tiles_l * 64, j0 = (int)(blockIdx.x % tiles) % tiles_l * 64;
+    const int tid = threadIdx.x;
+    const float back = 1.0f / (kScaleX * lift[b]);
+    for (int r = tid >> 6; r < 64; r += 4) {
+        const int64_t at = ((int64_t)b * sp + i0 + r) * lp + j0 + (tid & 63);
+        tile[r][tid & 63] = ((float)xhi[at] + (float)xlo[at]) * back;
+    }
+    __syncthreads();
+    const bool turned = m > n;
+    const int r0 = turned ? j0 : i0, c0 = turned ? i0 : j0;
+    for (int r = tid >> 6; r < 64; r += 4) {
+        const int row = r0 + r, col = c0 + (tid & 63);
+        if (row < m && col < n) out[(b * m + row) * n + col] = (T)(turned ? tile[tid & 63][r] : tile[r][tid & 63]);
+    }
+}
+
+template <class Kernel>
+hipError_t allow_lds(Kernel kernel, int bytes) {
+    return bytes <= 65536 ? hipSuccess
+                          : hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int BT, int WN, int WM, int PLANES, bool POLY>
+hipError_t launch_square(int64_t B, const h16* hi, const h16* lo, int sp, int K, const float* lift, const float* diag, h16* out_hi, h16* out_lo,
+                         float* out_diag, hipStream_t stream) {
+    const int t = (sp + BT - 1) / BT, tiles = t * (t + 1) / 2;
+    orthogonalize_square<BT, WN, WM, PLANES, POLY><<<(unsigned)(B * tiles), WN * WM * 64, 0, stream>>>(
+        hi, lo, sp, K, lift, diag, out_hi, out_lo, out_diag, tiles);
+    return hipGetLastError();
+}
+
+template <int BT, int WN, int WM, int PLANES>
+hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w, int& cur) {
+    auto half = [&](int64_t o) { return reinterpret_cast<h16*>(a.workspace + o); };
+    auto real = [&](int64_t o) { return reinterpret_cast<float*>(a.workspace + o); };
+    hipError_t err = hipSuccess;
+    const int tiles_n = (w.lp + BT - 1) / BT, tiles = tiles_n * ((w.sp + BT - 1) / BT);
+    for (int k = 0; k < a.steps && err == hipSuccess; ++k) {
+        err = launch_square<BT, WN, WM, PLANES, false>(a.B, half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, real(w.lift), nullptr,
+                                                       half(w.ohi), half(w.olo), real(w.diag), a.stream);
+        if (err != hipSuccess) break;
+        err = launch_square<BT, WN, WM, PLANES, true>(a.B, half(w.ohi), half(w.olo), w.sp, w.sp, nullptr, real(w.diag), half(w.bhi),
+                                                      half(w.blo), real(w.bdiag), a.stream);
+        if (err != hipSuccess) break;
+        orthogonalize_update<BT, BT, WN, WM, PLANES><<<(unsigned)(a.B * tiles), WN * WM * 64, 0, a.stream>>>(
+            half(w.bhi), half(w.blo), real(w.bdiag), half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, half(w.xhi[cur ^ 1]),
+            half(w.xlo[cur ^ 1]), tiles_n, tiles);
+        err = hipGetLastError();
+        cur ^= 1;
+    }
+    return err;
+}
+
+template <class T, int PLANES>
+hipError_t launch_tiled(const OrthogonalizeArgs& a) {
+    const Layout w = layout(a.B, a.m, a.n, PLANES == 2);
+    const T* u = static_cast<const T*>(a.update);
+    h16* x0 = reinterpret_cast<h16*>(a.workspace + w.xhi[0]);
+    h16* x1 = reinterpret_cast<h16*>(a.workspace + w.xlo[0]);
+    double* norm = reinterpret_cast<double*>(a.workspace + w.norm);
+    float* lift = reinterpret_cast<float*>(a.workspace + w.lift);
+    const unsigned tiles64 = (unsigned)(a.B * (w.sp / 64) * (w.lp / 64));
+    orthogonalize_norm<T><<<(unsigned)(a.B * kNormBlocks), 256, 0, a.stream>>>(u, (int64_t)a.m * a.n, norm);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    orthogonalize_begin<T><<<tiles64, 256, 0, a.stream>>>(u, a.m, a.n, a.eps, a.steps, norm, w.sp, w.lp, x0, x1, lift);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    int cur = 0;
+    const int64_t t128 = (w.sp + 127) / 128;
+    if (a.B * t128 * (t128 + 1) / 2 >= 128) err = launch_steps<128, 2, 4, PLANES>(a, w, cur);
+    else err = launch_steps<64, 2, 2, PLANES>(a, w, cur);
+    if (err != hipSuccess) return err;
+    orthogonalize_end<T><<<tiles64, 256, 0, a.stream>>>(reinterpret_cast<h16*>(a.workspace + w.xhi[cur]),
+                                                        reinterpret_cast<h16*>(a.workspace + w.xlo[cur]), w.sp, w.lp,
+                                                        lift, static_cast<T*>(a.out), a.m, a.n);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_small(const OrthogonalizeArgs& a) {
+    const SmallShape h = small_shape(a.m, a.n);
+    const hipError_t err = allow_lds(orthogonalize_small<T>, (int)h.bytes);
+    if (err != hipSuccess) return err;
+    orthogonalize_small<T><<<(unsigned)a.B, kSmallThreads, h.bytes, a.stream>>>(
+        static_cast<const T*>(a.update), a.m, a.n, a.steps, a.eps, static_cast<T*>(a.out));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n, dmr_dtype dtype) {
+    if (is_small(m, n)) return B <= INT32_MAX ? 256 : 0;
+    const Layout one = layout(1, m, n, true);
+    // one workgroup for every 64 x 64 tile, 31 bits of them; plane sizes in 63 bits
+    const int64_t tiles = (one.xs / 4096 > kNormBlocks ? one.xs / 4096 : kNormBlocks);
+    if (tiles > INT32_MAX || B > INT32_MAX / tiles) return 0;
+    return layout(B, m, n, dtype != DMR_BFLOAT16).bytes;
+}
+
+hipError_t launch_orthogonalize(const OrthogonalizeArgs& a) {
+    timing_begin(kKOrthogonalize, a.stream);
+    const bool small = is_small(a.m, a.n);
+    hipError_t err = hipErrorInvalidValue;
+    switch (a.dtype) {
+        case DMR_FLOAT32: err = small ? launch_small<float>(a) : launch_tiled<float, 2>(a); break;
+        case DMR_FLOAT16: err = small ? launch_small<_Float16>(a) : launch_tiled<_Float16, 2>(a); break;
+        case DMR_BFLOAT16: err = small ? launch_small<__bf16>(a) : launch_tiled<__bf16, 1>(a); break;
+    }
+    timing_end(kKOrthogonalize, a.stream);
+    return err;
+}
+
+}  // namespace dmr

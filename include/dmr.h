@@ -7,8 +7,10 @@
  * rasterize_meshes_bwd) and their workspace helpers; the second stage that
  * fuses each pixel's K faces (dmr_blend_fwd / dmr_blend_bwd); point clouds
  * (rasterize_points_fwd / rasterize_points_bwd); the upstream projection
- * from world space (dmr_project_fwd / dmr_project_bwd); status strings and
- * optional per-kernel timing.
+ * from world space (dmr_project_fwd / dmr_project_bwd); linear layers with
+ * one weight per mesh (dmr_grouped_linear_fwd / dmr_grouped_linear_bwd) and
+ * the orthogonalised update of such weights (dmr_orthogonalize); status
+ * strings and optional per-kernel timing.
  *
  * The main operation is the face-selection stage of the two-stage rasterizer of
  * "Accelerating 3D Deep Learning with PyTorch3D": for every pixel, select the
@@ -328,6 +330,82 @@ size_t dmr_workspace_min_size(int64_t N, int64_t F, int32_t H, int32_t W);
  * per-bin face lists from F, the image size and blur_radius. 0 on invalid
  * arguments. */
 size_t dmr_workspace_size_hint(int64_t N, int64_t F, int32_t H, int32_t W, int32_t K, float blur_radius);
+
+/*
+ * Linear layers of a packed batch, one weight per group: the decoders and
+ * shading layers that a model of each mesh (or material, or view) learns
+ * from the rasterizer's gradients. Rows of all groups are packed one after
+ * another, as vertices are for dmr_project_fwd, and for the rows r of group n
+ *     y_r = W_n x_r + b_n.
+ *
+ *   x          [R, in_features]; y [R, out_features], overwritten.
+ *   row_offsets [N+1] int64: group n owns rows [off[n], off[n+1]) (off[0] =
+ *              0, non-decreasing, off[N] = R; other offsets give unspecified,
+ *              memory-safe results). Empty groups and groups of one row are
+ *              allowed; N >= 1 when R > 0.
+ *   weight     [N, out_features, in_features]; bias [N, out_features] or NULL.
+ *   dtype      of x, weight, bias, y and all gradients. Sums are float32
+ *              (float32 products too), rounded once.
+ * A row depends on no other row; infinities and NaN propagate as in the
+ * formula. Arrays with 16-byte aligned start and widths that are multiples
+ * of 16 bytes take wide loads; others are as exact, and slower.
+ * Errors: negative sizes, widths below 1, missing pointers, an unknown dtype
+ * or N == 0 with R > 0: DMR_ERROR_INVALID_VALUE; widths above
+ * DMR_MAX_LINEAR_WIDTH or more output tiles than a launch can hold:
+ * DMR_ERROR_UNSUPPORTED. R == 0 launches nothing.
+ */
+typedef enum dmr_dtype {
+    DMR_FLOAT32 = 0,
+    DMR_FLOAT16 = 1,
+    DMR_BFLOAT16 = 2
+} dmr_dtype;
+#define DMR_MAX_LINEAR_WIDTH (1 << 20)
+dmr_status dmr_grouped_linear_fwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                  const void* weight, const void* bias, int32_t out_features, dmr_dtype dtype, void* y,
+                                  hipStream_t stream);
+
+/* Backward of dmr_grouped_linear_fwd for the same inputs, from grad_y
+ * [R, out_features]; each result is overwritten and may be NULL:
+ *     grad_x_r = W_n^T g_r,  grad_weight_n = sum_r g_r x_r^T,
+ *     grad_bias_n = sum_r g_r   (zero for an empty group).
+ * weight is read only for grad_x, x only for grad_weight and grad_bias.
+ * Long sums over rows are cut into pieces that `workspace` holds (16-byte
+ * aligned, of dmr_grouped_linear_workspace_size() bytes; not used without
+ * grad_weight and grad_bias) and added in a fixed order: results are the
+ * same on every run. */
+dmr_status dmr_grouped_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                  const void* weight, int32_t out_features, dmr_dtype dtype, const void* grad_y,
+                                  void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+/* Workspace of dmr_grouped_linear_bwd in bytes; 0 on invalid arguments. */
+size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype);
+
+/*
+ * Orthogonalised updates of B weight matrices (an optimiser's step for the
+ * layers above): with U a matrix [m, n] of the batch,
+ *     X_0 = U / (|U|_F + eps),  X_{k+1} = a X_k + (b A_k + c A_k A_k) X_k,
+ *     A_k = X_k X_k^T (of the shorter side; X_k^T X_k gives the same),
+ *     (a, b, c) = (3.4445, -4.7750, 2.0315),
+ * `steps` times: the singular vectors of U with singular values pushed
+ * towards 1 (within about 0.7 to 1.2 after five steps).
+ *
+ *   update, out [B, m, n] of dtype; out is overwritten and may not alias.
+ *   steps      1..DMR_MAX_ORTHOGONALIZE_STEPS; eps finite and > 0.
+ *   workspace  16-byte aligned, of dmr_orthogonalize_workspace_size() bytes.
+ * float32 and float16 are computed to float32 accuracy; for bfloat16 the
+ * factors of the products are rounded to 11 bits, which its own rounding
+ * hides (sums and X stay in more). A matrix of zeros gives zeros; one with
+ * an infinity or NaN gives NaN throughout, and leaves the others as they are.
+ * Errors: negative sizes, sides below 1, missing pointers, an unknown dtype,
+ * steps below 1, eps not > 0 and finite: DMR_ERROR_INVALID_VALUE; steps above
+ * the limit, sides above DMR_MAX_LINEAR_WIDTH or beyond what a launch can
+ * hold: DMR_ERROR_UNSUPPORTED. B == 0 launches nothing.
+ */
+#define DMR_MAX_ORTHOGONALIZE_STEPS 64
+dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n, dmr_dtype dtype, int32_t steps, float eps,
+                             void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* Workspace of dmr_orthogonalize in bytes; 0 on invalid arguments. */
+size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dtype dtype);
 
 /* What the last forward call on `workspace` recorded. Copies the workspace
  * header to the host and synchronises `stream`. */
