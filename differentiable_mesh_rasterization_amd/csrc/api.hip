@@ -473,8 +473,8 @@ dmr_status check_grouped(int64_t R, int32_t cin, int64_t N, int32_t cout, dmr_dt
     if (cin > DMR_MAX_LINEAR_WIDTH || cout > DMR_MAX_LINEAR_WIDTH) return DMR_ERROR_UNSUPPORTED;
     // tiles are counted in 32 bits (at least 16 rows a tile, and one for each group)
     const int64_t columns = (int64_t)(cin > cout ? cin : cout) / 16 + 1;
-    const int64_t weight_tiles = ((int64_t)cin / 64 + 1) * ((int64_t)cout / 64 + 1);
-    const int64_t most = (int64_t)INT32_MAX - 8;
+    const int64_t weight_tiles = ((int64_t)cin / 32 + 1) * ((int64_t)cout / 32 + 1);
+    const int64_t most = (int64_t)INT32_MAX - 1024;
     if (R > INT64_MAX / ((int64_t)DMR_MAX_LINEAR_WIDTH * 4)) return DMR_ERROR_UNSUPPORTED;
     if (N > most / 64 || N > most / columns || N > most / weight_tiles) return DMR_ERROR_UNSUPPORTED;
     if (R / 16 + N > most / columns || R / 512 + N > most / weight_tiles) return DMR_ERROR_UNSUPPORTED;
@@ -501,8 +501,8 @@ dmr_status dmr_grouped_linear_fwd(const void* x, int64_t R, int32_t in_features,
 size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype) {
     static const int64_t none = 0;
     if (check_grouped(R, in_features, N, out_features, dtype, &none) != DMR_SUCCESS) return 0;
-    const int64_t values = (int64_t)in_features * out_features + out_features;
-    return align_up((size_t)(grouped_pieces(R, N, in_features, out_features).slots * values) * sizeof(float) + 256, 256);
+    const int64_t slots = grouped_pieces(R, N, in_features, out_features, dtype != DMR_FLOAT32).slots;
+    return align_up((size_t)(slots * grouped_piece_values(in_features, out_features)) * sizeof(float) + 256, 256);
 }
 
 dmr_status dmr_grouped_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,

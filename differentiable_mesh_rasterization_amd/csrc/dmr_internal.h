@@ -436,13 +436,17 @@ struct GroupedLinearArgs {
     float* workspace;
     hipStream_t stream;
 };
-// How the backward pass cuts long groups' rows: rows of a piece, and the
-// float32 partial results that the workspace holds.
+// How the backward pass cuts long groups' rows: rows of a piece, the side of
+// a tile, and the float32 partial results (slots) that the workspace holds.
 struct GroupedPieces {
-    int rows;
+    int rows, side;
     int64_t slots;
 };
-GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout);
+GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half);
+// Values of a slot: the weight's, then the bias's, padded to 16 bytes.
+__host__ __device__ __forceinline__ int64_t grouped_piece_values(int32_t cin, int32_t cout) {
+    return ((int64_t)cin * cout + cout + 3) / 4 * 4;
+}
 hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a);
 hipError_t launch_grouped_linear_backward(const GroupedLinearArgs& a);
 

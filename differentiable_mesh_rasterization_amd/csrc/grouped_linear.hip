@@ -13,6 +13,8 @@
 namespace dmr {
 namespace {
 
+constexpr int kRun = 32;   // consecutive tiles that a die is given at a time
+
 // A run of rows of one group.
 struct RowTile {
     int64_t group, first;   // group < 0: no such tile
@@ -31,13 +33,26 @@ __device__ __forceinline__ void group_bounds(const int64_t* __restrict__ off, in
     }
 }
 
-__device__ __forceinline__ int64_t wave_inclusive_sum(int64_t v, int lane) {
+template <class I>
+__device__ __forceinline__ I wave_inclusive_sum(I v, int lane) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int64_t u = __shfl_up(v, d, 64);
+        const I u = __shfl_up(v, d, 64);
         if (lane >= d) v += u;
     }
     return v;
+}
+
+// Workgroup b's place in the order of the tiles. Consecutive workgroups go to
+// the 8 dies in turn; this gives each die runs of RUN consecutive tiles (what
+// its 32 compute units work on at a time), which share rows and weights in
+// its L2, and deals the runs out in turn, so that no die is left with the
+// long groups or with the places past the last tile. The grid is a multiple
+// of 8 RUN.
+template <int RUN>
+__device__ __forceinline__ int64_t tile_of_workgroup(uint32_t b) {
+    const uint32_t die = b & 7, i = b >> 3;
+    return (int64_t)((i / RUN * 8 + die) * RUN + i % RUN);
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
@@ -47,28 +62,28 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 }
 
 // Row tile t of all groups' tiles of `per` rows in order. Every wave does
-// the same work.
-__device__ __forceinline__ RowTile find_row_tile(const int64_t* __restrict__ off, int64_t N, int64_t R, int per,
-                                                 int64_t t) {
+// the same work. (Tile counts fit in 32 bits: a launch holds no more.)
+__device__ __forceinline__ RowTile find_row_tile(const int64_t* __restrict__ off, int64_t N, int64_t R, int per, int t) {
     const int lane = threadIdx.x & 63;
-    int64_t before = 0;
+    int before = 0;
     for (int64_t base = 0; base < N; base += 64) {
         int64_t lo, hi;
         group_bounds(off, N, R, base + lane, lo, hi);
-        const int64_t tiles = (hi - lo + per - 1) / per;
-        const int64_t upto = before + wave_inclusive_sum(tiles, lane);
+        const int tiles = (int)((hi - lo + per - 1) / per);
+        const int upto = before + wave_inclusive_sum(tiles, lane);
         const uint64_t hit = __ballot(upto > t);
         if (hit) {
             const int src = __builtin_ctzll(hit);
-            const int64_t first = lo + (t - (upto - tiles)) * per;
+            const int64_t first = lo + (int64_t)(t - (upto - tiles)) * per;
             const int64_t left = hi - first;
             RowTile r;
-            r.group = uniform64(base + src);
-            r.first = uniform64(__shfl(first, src, 64));
-            r.rows = __builtin_amdgcn_readfirstlane(__shfl((int)(left < per ? left : per), src, 64));
+            r.group = base + src;
+            r.first = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)first, src) |
+                                (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)((uint64_t)first >> 32), src) << 32);
+            r.rows = __builtin_amdgcn_readlane((int)(left < per ? left : per), src);
             return r;
         }
-        before = __shfl(upto, 63, 64);
+        before = __builtin_amdgcn_readlane(upto, 63);
     }
     return {-1, 0, 0};
 }
@@ -81,77 +96,120 @@ __device__ __forceinline__ void store4(T* __restrict__ row, int n, int N, f32x4 
         if (n + i < N) row[n + i] = (T)v[i];
 }
 
-template <class T, int COUNT>
-struct alignas(16) Packed {
-    T v[COUNT];
-};
+// 16 bytes of a row: 8 16-bit or 4 float32 values.
+template <class T>
+__device__ __forceinline__ u32x4 packed(f32x4 lo, f32x4 hi) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(u32x4, lo);
+    } else {
+        alignas(16) T v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = (T)lo[i];
+            v[4 + i] = (T)hi[i];
+        }
+        return *reinterpret_cast<const u32x4*>(v);
+    }
+}
 
 // Writes a workgroup's tile: rows [0, rows) of `out` (leading dimension ld),
-// columns [n0, N), plus bias[n] if given. VEC as in OperandTile::stage.
-template <class T, class Tile, bool VEC>
+// columns [n0, N), plus bias[n] if given. `wide`: `out` is 16-byte aligned and
+// ld a multiple of 16 bytes.
+template <class T, class Tile>
 __device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, int64_t ld, int rows, int n0, int N,
-                                           const T* __restrict__ bias, int tid) {
-    constexpr int STEP = Tile::PAIRED ? 2 : 1;
+                                           const T* __restrict__ bias, bool wide, int tid) {
+    constexpr int STEP = Tile::PAIRED ? 2 : 1;              // blocks of n in a lane's 16 bytes
+    constexpr bool CHUNKS = Tile::PAIRED || sizeof(T) == 4;   // a lane holds 16 bytes of a row
+    f32x4 add[Tile::NT];
 #pragma unroll
-    for (int a = 0; a < Tile::NT; a += STEP) {
-        const int n = n0 + Tile::n_of(tid, a);
-        f32x4 add[STEP];
+    for (int a = 0; a < Tile::NT; ++a)
 #pragma unroll
-        for (int s = 0; s < STEP; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = n + 4 * s + i;   // past the end: any value, not stored
-                add[s][i] = bias ? (float)bias[at < N ? at : N - 1] : 0.0f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int at = n0 + Tile::n_of(tid, a) + i;   // past the end: any value, not stored
+            add[a][i] = bias ? (float)bias[at < N ? at : N - 1] : 0.0f;
+        }
+    if (CHUNKS && wide) {
+        // 32-bit offsets from the tile's corner; stores past the buffer's
+        // range are dropped
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(out + n0, 0, kBufferRange, 0x00020000);
+        const uint32_t line = (uint32_t)(ld * sizeof(T));
+        const int left = N - n0;
 #pragma unroll
         for (int b = 0; b < Tile::MT; ++b) {
             const int m = Tile::m_of(tid, b);
-            if (m >= rows) continue;
-            T* row = out + (int64_t)m * ld;
-            if constexpr (VEC && (Tile::PAIRED || sizeof(T) == 4)) {
-                if (n < N) {
-                    Packed<T, 4 * STEP> w;
 #pragma unroll
-                    for (int s = 0; s < STEP; ++s)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w.v[4 * s + i] = (T)(t.acc[a + s][b][i] + add[s][i]);
-                    *reinterpret_cast<Packed<T, 4 * STEP>*>(row + n) = w;
+            for (int a = 0; a < Tile::NT; a += 2 * STEP) {
+                const u32x4 c0 = packed<T>(t.acc[a][b] + add[a], t.acc[a + STEP - 1][b] + add[a + STEP - 1]);
+                const int na = Tile::n_of(tid, a);
+                if constexpr (Tile::NT % (2 * STEP) == 0) {
+                    const u32x4 c1 = packed<T>(t.acc[a + STEP][b] + add[a + STEP],
+                                               t.acc[a + 2 * STEP - 1][b] + add[a + 2 * STEP - 1]);
+                    const int nb = Tile::n_of(tid, a + STEP);
+                    store_row_pairs(c0, c1, tid, [&](bool odd, int chunk, u32x4 v) {
+                        const int row = (m & ~1) | (odd ? 1 : 0), n = chunk ? nb : na;
+                        const uint32_t off = (uint32_t)row * line + (uint32_t)n * (uint32_t)sizeof(T);
+                        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, row < rows && n < left ? off : kNowhere, 0, 0);
+                    });
+                } else {
+                    const uint32_t off = (uint32_t)m * line + (uint32_t)na * (uint32_t)sizeof(T);
+                    __builtin_amdgcn_raw_buffer_store_b128(c0, rsrc, m < rows && na < left ? off : kNowhere, 0, 0);
                 }
-            } else {
-#pragma unroll
-                for (int s = 0; s < STEP; ++s) store4<T>(row, n + 4 * s, N, t.acc[a + s][b] + add[s]);
             }
         }
+        return;
     }
+#pragma unroll
+    for (int a = 0; a < Tile::NT; ++a)
+#pragma unroll
+        for (int b = 0; b < Tile::MT; ++b) {
+            const int m = Tile::m_of(tid, b);
+            if (m < rows) store4<T>(out + (int64_t)m * ld, n0 + Tile::n_of(tid, a), N, t.acc[a][b] + add[a]);
+        }
 }
 
 // y = x W^T + b (WK: the weight's contiguous direction is summed over) or
 // grad_x = g W (!WK), row tile by row tile. `n_out` is the width of `out`,
 // `k_in` that of `rows_in`; the weight of a group is [n_out][k_in] if WK and
 // [k_in][n_out] if not.
-template <class T, int BN, int BM, int WN, int WM, bool WK, bool VEC>
-__global__ __launch_bounds__(WN * WM * 64) void grouped_rows(const T* __restrict__ rows_in, int64_t R, int k_in,
-                                                             const int64_t* __restrict__ off, int64_t N,
-                                                             const T* __restrict__ weight, int n_out,
-                                                             const T* __restrict__ bias, T* __restrict__ out,
-                                                             int64_t tiles, int n_tiles) {
-    using Tile = TileProduct<T, BN, BM, WN, WM, WK, true>;
+template <class T, class Tile, bool WK, bool VEC>
+__global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restrict__ rows_in, int64_t R, int k_in,
+                                                              const int64_t* __restrict__ off, int64_t N,
+                                                              const T* __restrict__ weight, int n_out,
+                                                              const T* __restrict__ bias, T* __restrict__ out, bool wide,
+                                                              int64_t tiles, int n_tiles, uint32_t places) {
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
-    // consecutive workgroups go to the 8 dies in turn: each die takes a run
-    // of consecutive tiles, which share rows and weights in its L2
-    const int64_t per = (tiles + 7) / 8;
-    const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (id >= tiles) return;
-    const RowTile at = find_row_tile(off, N, R, BM, id / n_tiles);
-    if (at.group < 0) return;
-    const int n0 = (int)(id % n_tiles) * BN;
     const int tid = threadIdx.x;
-    const T* w = weight + at.group * (int64_t)n_out * k_in + (WK ? (int64_t)n0 * k_in : (int64_t)n0);
-    Tile t;
-    t.template run<VEC, false>(lds, w, WK ? k_in : n_out, n_out - n0, rows_in + at.first * (int64_t)k_in, k_in, at.rows,
-                               k_in, tid, false);
-    store_tile<T, Tile, VEC>(t, out + at.first * (int64_t)n_out, n_out, at.rows, n0, n_out,
-                             bias ? bias + at.group * (int64_t)n_out : nullptr, tid);
+    const auto find = [&](uint32_t place) {
+        const int64_t id = tile_of_workgroup<kRun>(place);
+        if (id >= tiles) return RowTile{-1, 0, 0};
+        return find_row_tile(off, N, R, Tile::BM, (int)(id / n_tiles));
+    };
+    const auto column = [&](uint32_t place) { return (int)(tile_of_workgroup<kRun>(place) % n_tiles) * Tile::BN; };
+    const auto weights = [&](const RowTile& at, int n0) {
+        const T* w = weight + at.group * (int64_t)n_out * k_in + (WK ? (int64_t)n0 * k_in : (int64_t)n0);
+        return typename Tile::Source{w, nullptr, WK ? k_in : n_out, n_out - n0};
+    };
+    const auto rows_of = [&](const RowTile& at) {
+        return typename Tile::Source{rows_in + at.first * (int64_t)k_in, nullptr, k_in, at.rows};
+    };
+    // A workgroup that takes several tiles finds the next one while a tile is
+    // multiplied and issues its first loads before it stores.
+    uint32_t place = blockIdx.x;
+    RowTile at = find(place);
+    int n0 = column(place);
+    if (at.group >= 0) Tile::template begin<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
+    while (at.group >= 0) {
+        place += gridDim.x;
+        const RowTile next = place < places ? find(place) : RowTile{-1, 0, 0};
+        const int next_n0 = column(place);
+        Tile t;
+        t.template finish<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
+        if (next.group >= 0) Tile::template begin<VEC>(lds, weights(next, next_n0), rows_of(next), k_in, tid);
+        store_tile<T, Tile>(t, out + at.first * (int64_t)n_out, n_out, at.rows, n0, n_out,
+                            bias ? bias + at.group * (int64_t)n_out : nullptr, wide, tid);
+        at = next;
+        n0 = next_n0;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -187,7 +245,7 @@ __device__ __forceinline__ Piece find_piece(const int64_t* __restrict__ off, int
             const int64_t first = lo + k * per;
             const int64_t left = hi - first;
             Piece r;
-            r.group = uniform64(base + src);
+            r.group = base + src;
             r.first = uniform64(__shfl(first, src, 64));
             r.rows = __builtin_amdgcn_readfirstlane(__shfl((int)(left < per ? left : per), src, 64));
             r.slot = uniform64(__shfl(pieces > 1 ? slots_upto - slots + k : (int64_t)-1, src, 64));
@@ -199,34 +257,32 @@ __device__ __forceinline__ Piece find_piece(const int64_t* __restrict__ off, int
     return {-1, 0, 0, -1};
 }
 
-template <class T, int BN, int BM, int WN, int WM, bool VEC>
-__global__ __launch_bounds__(WN * WM * 64) void grouped_weight_grad(
+template <class T, class Tile, bool VEC>
+__global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
     const T* __restrict__ x, const T* __restrict__ g, int64_t R, int cin, int cout, const int64_t* __restrict__ off,
-    int64_t N, int per, T* __restrict__ grad_weight, T* __restrict__ grad_bias, float* __restrict__ slots,
+    int64_t N, int per, T* __restrict__ grad_weight, T* __restrict__ grad_bias, bool wide, float* __restrict__ slots,
     int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
-    using Tile = TileProduct<T, BN, BM, WN, WM, false, false>;
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
-    const int64_t each = (items + 7) / 8;
-    const int64_t id = (int64_t)(blockIdx.x & 7) * each + (blockIdx.x >> 3);
+    const int64_t id = tile_of_workgroup<kRun>(blockIdx.x);
     if (id >= items) return;
     const int tiles = n_tiles * m_tiles;
     const Piece at = find_piece(off, N, R, per, id / tiles);
     if (at.group < 0 || at.slot >= slot_count) return;
     const int tile = (int)(id % tiles);
-    const int n0 = (tile % n_tiles) * BN, m0 = (tile / n_tiles) * BM;
+    const int n0 = (tile % n_tiles) * Tile::BN, m0 = (tile / n_tiles) * Tile::BM;
     const int tid = threadIdx.x;
     const bool sums = n0 == 0 && grad_bias != nullptr;
     if (!grad_weight && !sums) return;
     Tile t;
-    t.template run<VEC, true>(lds, x + at.first * cin + n0, cin, cin - n0, g + at.first * cout + m0, cout, cout - m0,
-                              at.rows, tid, sums);
-    const int rows = cout - m0 < BM ? cout - m0 : BM;
+    t.template run<VEC>(lds, {x + at.first * cin + n0, nullptr, cin, cin - n0},
+                        {g + at.first * cout + m0, nullptr, cout, cout - m0}, at.rows, tid, sums);
+    const int rows = cout - m0 < Tile::BM ? cout - m0 : Tile::BM;
     const int lane = tid & 63;
-    const bool first_n = (tid >> 6) % WN == 0 && lane < 16;   // one lane per m holds the row's sum
+    const bool first_n = Tile::n_of(tid, 0) == 0 && lane < 16;   // one lane per m holds the row's sum
     if (at.slot < 0) {
         if (grad_weight)
-            store_tile<T, Tile, VEC>(t, grad_weight + (at.group * cout + m0) * (int64_t)cin, cin, rows, n0, cin,
-                                     (const T*)nullptr, tid);
+            store_tile<T, Tile>(t, grad_weight + (at.group * cout + m0) * (int64_t)cin, cin, rows, n0, cin,
+                                (const T*)nullptr, wide, tid);
         if (sums && first_n)
 #pragma unroll
             for (int b = 0; b < Tile::MT; ++b) {
@@ -235,14 +291,18 @@ __global__ __launch_bounds__(WN * WM * 64) void grouped_weight_grad(
             }
         return;
     }
-    float* slot = slots + at.slot * ((int64_t)cout * cin + cout);
+    float* slot = slots + at.slot * grouped_piece_values(cin, cout);
     if (grad_weight) {
+        const bool whole = cin % 4 == 0;
 #pragma unroll
         for (int a = 0; a < Tile::NT; ++a)
 #pragma unroll
             for (int b = 0; b < Tile::MT; ++b) {
-                const int m = Tile::m_of(tid, b);
-                if (m < rows) store4<float>(slot + (int64_t)(m0 + m) * cin, n0 + Tile::n_of(tid, a), cin, t.acc[a][b]);
+                const int m = Tile::m_of(tid, b), n = n0 + Tile::n_of(tid, a);
+                if (m >= rows) continue;
+                float* row = slot + (int64_t)(m0 + m) * cin;
+                if (!whole) store4<float>(row, n, cin, t.acc[a][b]);
+                else if (n < cin) *reinterpret_cast<f32x4*>(row + n) = t.acc[a][b];
             }
     }
     if (sums && first_n)
@@ -253,11 +313,15 @@ __global__ __launch_bounds__(WN * WM * 64) void grouped_weight_grad(
         }
 }
 
-// Adds the pieces of the groups that have more than one, in order.
+// Adds the pieces of the groups that have more than one, in order, eight
+// loads in flight a lane. A workgroup takes 1024 values of a group.
+constexpr int kAddValues = 1024;
+
 template <class T>
 __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restrict__ off, int64_t N, int64_t R, int per,
-                                                          int64_t values, int64_t weights, const float* __restrict__ slots,
-                                                          int64_t slot_count, unsigned blocks, T* __restrict__ grad_weight,
+                                                          int64_t values, int64_t width, int64_t weights,
+                                                          const float* __restrict__ slots, int64_t slot_count,
+                                                          unsigned blocks, T* __restrict__ grad_weight,
                                                           T* __restrict__ grad_bias) {
     const int lane = threadIdx.x & 63;
     const int64_t group = blockIdx.x / blocks;
@@ -271,15 +335,27 @@ __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restr
         if (group < base + 64) mine = __shfl(pieces, (int)(group - base), 64);
     }
     if (mine <= 1 || slot + mine > slot_count) return;
-    const int64_t width = values;   // weights, then the bias
-    for (int64_t i = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x; i < width; i += (int64_t)blocks * 256) {
-        const bool is_weight = i < weights;
-        if (is_weight ? grad_weight == nullptr : grad_bias == nullptr) continue;
-        const float* from = slots + slot * width + i;
-        float s = from[0];
-        for (int64_t k = 1; k < mine; ++k) s += from[k * width];
-        if (is_weight) grad_weight[group * weights + i] = (T)s;
-        else grad_bias[group * (width - weights) + i - weights] = (T)s;
+    const int64_t i0 = ((int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x) * 4;   // slots are padded to whole vectors
+    if (i0 >= values) return;
+    const float* from = slots + slot * width + i0;
+    f32x4 s = *reinterpret_cast<const f32x4*>(from);
+    int64_t k = 1;
+    for (; k + 8 <= mine; k += 8) {
+        f32x4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x4*>(from + (k + j) * width);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    for (; k < mine; ++k) s += *reinterpret_cast<const f32x4*>(from + k * width);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t i = i0 + j;
+        if (i < weights) {
+            if (grad_weight) grad_weight[group * weights + i] = (T)s[j];
+        } else if (i < values && grad_bias) {
+            grad_bias[group * (values - weights) + i - weights] = (T)s[j];
+        }
     }
 }
 
@@ -294,78 +370,107 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // The most row tiles of `per` rows that R rows in N groups can make.
 int64_t most_row_tiles(int64_t R, int64_t N, int per) { return R / per + (N < R ? N : R); }
 
-template <class T, int BN, int BM, int WN, int WM, bool WK>
-hipError_t launch_rows_tile(const GroupedLinearArgs& a, const T* in, int k_in, const T* bias, T* out, int n_out, bool vec) {
-    const int n_tiles = ceil_div(n_out, BN);
-    const int64_t tiles = most_row_tiles(a.R, a.N, BM) * n_tiles;
-    const int64_t grid = (tiles + 7) / 8 * 8;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
+// Workgroups for `tiles` tiles; 0 if a launch cannot hold them.
+unsigned run_grid(int64_t tiles) {
+    const int64_t grid = (tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun);
+    return grid > INT32_MAX ? 0u : (unsigned)grid;
+}
+
+template <class T, class Tile, bool WK>
+hipError_t launch_rows_tile(const GroupedLinearArgs& a, const T* in, int k_in, const T* bias, T* out, int n_out, bool vec,
+                            bool wide) {
+    const int n_tiles = ceil_div(n_out, Tile::BN);
+    const int64_t tiles = most_row_tiles(a.R, a.N, Tile::BM) * n_tiles;
+    const unsigned places = run_grid(tiles);
+    if (places == 0) return hipErrorInvalidValue;
+    // as many workgroups as the device holds at a time (a multiple of 8 kRun)
+    constexpr unsigned kHeld = 256 * (160 * 1024 / Tile::kLdsBytes);
+    const unsigned grid = places > kHeld ? kHeld : places;
     const T* w = static_cast<const T*>(a.weight);
     if (vec)
-        grouped_rows<T, BN, BM, WN, WM, WK, true><<<(unsigned)grid, WN * WM * 64, 0, a.stream>>>(
-            in, a.R, k_in, a.off, a.N, w, n_out, bias, out, tiles, n_tiles);
-    else
-        grouped_rows<T, BN, BM, WN, WM, WK, false><<<(unsigned)grid, WN * WM * 64, 0, a.stream>>>(
-            in, a.R, k_in, a.off, a.N, w, n_out, bias, out, tiles, n_tiles);
+        grouped_rows<T, Tile, WK, true><<<grid, Tile::THREADS, 0, a.stream>>>(in, a.R, k_in, a.off, a.N, w, n_out, bias, out,
+                                                                              wide, tiles, n_tiles, places);
+    else if constexpr (Tile::BN < 256)   // the largest tiles have no form for unaligned arrays
+        grouped_rows<T, Tile, WK, false><<<grid, Tile::THREADS, 0, a.stream>>>(in, a.R, k_in, a.off, a.N, w, n_out, bias, out,
+                                                                               wide, tiles, n_tiles, places);
     return hipGetLastError();
 }
 
 template <class T, bool WK>
-hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const T* bias, T* out, int n_out, bool vec) {
-    if (a.R <= 16 * a.N) return launch_rows_tile<T, 64, 16, 4, 1, WK>(a, in, k_in, bias, out, n_out, vec);
-    if (n_out <= 16) return launch_rows_tile<T, 16, 256, 1, 4, WK>(a, in, k_in, bias, out, n_out, vec);
-    if (n_out <= 64) return launch_rows_tile<T, 64, 128, 1, 4, WK>(a, in, k_in, bias, out, n_out, vec);
-    return launch_rows_tile<T, 128, 128, 2, 2, WK>(a, in, k_in, bias, out, n_out, vec);
+hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const T* bias, T* out, int n_out, bool vec,
+                       bool wide) {
+    if (a.R <= 16 * a.N)
+        return launch_rows_tile<T, TileProduct<T, 64, 16, 4, 1, WK, true, 4, 4>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+    if (n_out <= 16)
+        return launch_rows_tile<T, TileProduct<T, 16, 256, 1, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+    if (n_out <= 64)
+        return launch_rows_tile<T, TileProduct<T, 64, 128, 1, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+    if constexpr (sizeof(T) == 2)
+        if (vec && n_out > 128 && a.R >= 512 * a.N)
+            return launch_rows_tile<T, TileProduct<T, 256, 256, 4, 2, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
+                                                                                           wide);
+    return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 2, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
 }
 
-template <class T, int BN, int BM, int WN, int WM>
-hipError_t launch_weight_tile(const GroupedLinearArgs& a, int per, int64_t slot_count, bool vec) {
-    const int n_tiles = ceil_div(a.cin, BN), m_tiles = ceil_div(a.cout, BM);
-    const int64_t items = (a.R / per + a.N) * n_tiles * m_tiles;
-    const int64_t grid = (items + 7) / 8 * 8;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
+template <class T, class Tile>
+hipError_t launch_weight_tile(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide) {
+    const int n_tiles = ceil_div(a.cin, Tile::BN), m_tiles = ceil_div(a.cout, Tile::BM);
+    const int64_t items = (a.R / p.rows + a.N) * n_tiles * m_tiles;
+    const unsigned grid = run_grid(items);
+    if (grid == 0) return hipErrorInvalidValue;
     const T *x = static_cast<const T*>(a.x), *g = static_cast<const T*>(a.grad_y);
     T *gw = static_cast<T*>(a.grad_weight), *gb = static_cast<T*>(a.grad_bias);
     if (vec)
-        grouped_weight_grad<T, BN, BM, WN, WM, true><<<(unsigned)grid, WN * WM * 64, 0, a.stream>>>(
-            x, g, a.R, a.cin, a.cout, a.off, a.N, per, gw, gb, a.workspace, slot_count, items, n_tiles, m_tiles);
-    else
-        grouped_weight_grad<T, BN, BM, WN, WM, false><<<(unsigned)grid, WN * WM * 64, 0, a.stream>>>(
-            x, g, a.R, a.cin, a.cout, a.off, a.N, per, gw, gb, a.workspace, slot_count, items, n_tiles, m_tiles);
+        grouped_weight_grad<T, Tile, true><<<grid, Tile::THREADS, 0, a.stream>>>(
+            x, g, a.R, a.cin, a.cout, a.off, a.N, p.rows, gw, gb, wide, a.workspace, p.slots, items, n_tiles, m_tiles);
+    else if constexpr (Tile::BN < 256)
+        grouped_weight_grad<T, Tile, false><<<grid, Tile::THREADS, 0, a.stream>>>(
+            x, g, a.R, a.cin, a.cout, a.off, a.N, p.rows, gw, gb, wide, a.workspace, p.slots, items, n_tiles, m_tiles);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
     const T* bias = static_cast<const T*>(a.bias);
-    const bool widths = a.cin % (16 / sizeof(T)) == 0 && a.cout % (16 / sizeof(T)) == 0;
+    const bool in16 = a.cin % (16 / sizeof(T)) == 0, out16 = a.cout % (16 / sizeof(T)) == 0;   // rows of whole 16 bytes
     if (!backward) {
-        const bool vec = widths && aligned16(a.x) && aligned16(a.weight) && aligned16(a.y);
         if (a.R == 0) return hipSuccess;
         timing_begin(kKGroupedLinearFwd, a.stream);
-        const hipError_t err = launch_rows<T, true>(a, static_cast<const T*>(a.x), a.cin, bias, static_cast<T*>(a.y), a.cout, vec);
+        const hipError_t err = launch_rows<T, true>(a, static_cast<const T*>(a.x), a.cin, bias, static_cast<T*>(a.y), a.cout,
+                                                    in16 && aligned16(a.x) && aligned16(a.weight), out16 && aligned16(a.y));
         timing_end(kKGroupedLinearFwd, a.stream);
         return err;
     }
     timing_begin(kKGroupedLinearBwd, a.stream);
     hipError_t err = hipSuccess;
-    if (a.grad_x && a.R > 0) {
-        const bool vec = widths && aligned16(a.grad_y) && aligned16(a.weight) && aligned16(a.grad_x);
+    if (a.grad_x && a.R > 0)
         err = launch_rows<T, false>(a, static_cast<const T*>(a.grad_y), a.cout, (const T*)nullptr, static_cast<T*>(a.grad_x),
-                                    a.cin, vec);
-    }
+                                    a.cin, in16 && out16 && aligned16(a.grad_y) && aligned16(a.weight),
+                                    in16 && aligned16(a.grad_x));
     if (err == hipSuccess && (a.grad_weight || a.grad_bias) && a.N > 0) {
-        const bool vec = widths && aligned16(a.x) && aligned16(a.grad_y) && aligned16(a.grad_weight);
-        const GroupedPieces p = grouped_pieces(a.R, a.N, a.cin, a.cout);
-        if (a.cin <= 64 && a.cout <= 64) err = launch_weight_tile<T, 64, 64, 2, 2>(a, p.rows, p.slots, vec);
-        else err = launch_weight_tile<T, 128, 128, 2, 2>(a, p.rows, p.slots, vec);
+        const bool vec = in16 && out16 && aligned16(a.x) && aligned16(a.grad_y);
+        const bool wide = in16 && aligned16(a.grad_weight);
+        const GroupedPieces p = grouped_pieces(a.R, a.N, a.cin, a.cout, sizeof(T) == 2);
+        bool done = false;
+        if constexpr (sizeof(T) == 2)
+            if (p.side == 256 && vec) {
+                err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, 2, 1, true>>(a, p, vec, wide);
+                done = true;
+            }
+        if (!done)
+            err = p.side == 64
+                      ? launch_weight_tile<T, TileProduct<T, 64, 64, 2, 2, false, false, 2, 2, 1, true>>(a, p, vec, wide)
+                      : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, 2, 1, true>>(a, p, vec, wide);
         if (err == hipSuccess && p.slots > 0) {
             const int64_t weights = (int64_t)a.cin * a.cout, values = weights + a.cout;
-            const unsigned blocks = (unsigned)(values < 64 * 256 ? (values + 255) / 256 : 64);
-            grouped_add_pieces<T><<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
-                a.off, a.N, a.R, p.rows, values, weights, a.workspace, p.slots, blocks, static_cast<T*>(a.grad_weight),
-                static_cast<T*>(a.grad_bias));
-            err = hipGetLastError();
+            const int64_t blocks = (values + kAddValues - 1) / kAddValues;
+            if (blocks * a.N > INT32_MAX) err = hipErrorInvalidValue;
+            else {
+                grouped_add_pieces<T><<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
+                    a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), weights, a.workspace, p.slots,
+                    (unsigned)blocks, static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
+                err = hipGetLastError();
+            }
         }
     }
     timing_end(kKGroupedLinearBwd, a.stream);
@@ -383,18 +488,19 @@ hipError_t launch_typed(const GroupedLinearArgs& a, bool backward) {
 
 }  // namespace
 
-// Rows of a piece of the weight gradient, and the slots that the pieces of
-// groups longer than one piece can take: a group of r > rows has at most
-// 2 r / rows of them.
-GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout) {
-    const bool small = cin <= 64 && cout <= 64;
-    const int64_t side = small ? 64 : 128;
+// The tile side, the rows of a piece of the weight gradient, and the slots
+// that the pieces of groups longer than one piece can take: a group of
+// r > rows has at most 2 floor(r / rows) of them.
+GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half) {
+    const int64_t side = cin <= 64 && cout <= 64 ? 64 : !half || cin <= 128 || cout <= 128 || R < 512 * N ? 128 : 256;
     const int64_t tiles = ((cin + side - 1) / side) * ((cout + side - 1) / side);
-    const int64_t want = tiles >= 512 ? 1 : 512 / tiles;   // pieces that fill the device
-    int64_t rows = (R + want - 1) / want;
+    // pieces short enough that the longest is a fraction of a compute unit's
+    // share of the work
+    const int64_t want = (side == 256 ? 512 : 1024) / tiles;
+    int64_t rows = want > 0 ? (R + want - 1) / want : R;
     rows = (rows + 127) / 128 * 128;
     rows = rows < 512 ? 512 : rows > 8192 ? 8192 : rows;
-    return {(int)rows, R > rows ? 2 * (R / rows) : 0};
+    return {(int)rows, (int)side, R > rows ? 2 * (R / rows) : 0};
 }
 
 hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a) { return launch_typed(a, false); }

@@ -1,22 +1,25 @@
 // Matrix-core tiles shared by the layers and the optimiser's products.
 //
 // A workgroup computes a BM x BN tile of C[m][n] = sum_k Q[m][k] P[n][k] in
-// float32 accumulators. Both operands are staged in LDS one K step of 128
-// bytes at a time (BK = 64 16-bit or 32 float32 elements), double buffered:
-// the loads of step t + 1 go straight from memory into LDS while the waves
-// multiply step t.
+// float32 accumulators. Both operands are staged in LDS 128 bytes of k (whole
+// cache lines of a row) at a time, in rings of SP and SQ stages. A step is two
+// slices
+// of 64 bytes of k: while the matrix cores work on one slice's fragments, the
+// next slice's are read from LDS into a second set of registers. In the middle
+// of a step its last fragments have been read, so its stage is free there:
+// that is where the one barrier of a step stands, and where the loads, which
+// go straight from memory into LDS, are issued SP and SQ steps ahead.
 //
 // P is the first operand of the matrix instruction and n its row index, so
 // that a lane's four accumulators are four consecutive n of one row m of C:
 // C is stored n-contiguous, 16 bytes a lane.
 //
-// An operand is K-major (row r at base + r ld, k contiguous) or row-major in
-// the other sense, "M-major" (k at base + k ld, rows contiguous), as memory
-// has it; the transpose of 16-bit M-major tiles happens on the way from LDS
-// to registers (ds_read_b64_tr_b16: 16 lanes read a 4 x 16 block and get its
-// columns). Which k a lane holds does not matter as long as both operands
-// agree, so float32 operands take four consecutive k of a lane for four
-// successive instructions.
+// An operand is K-major (row r at base + r ld, k contiguous) or M-major (k at
+// base + k ld, rows contiguous), as memory has it; 16-bit M-major tiles are
+// transposed on the way from LDS to registers (ds_read_b64_tr_b16: 16 lanes
+// read a 4 x 16 block and get its columns). Which k a lane holds does not
+// matter as long as both operands agree, so float32 operands take four
+// consecutive k of a lane for four successive instructions.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -31,10 +34,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-#define DMR_LDS __attribute__((address_space(3)))
-
-// Bytes of k in a staged step.
+// Bytes of k in a step.
 constexpr int kStepBytes = 128;
+
+#define DMR_LDS __attribute__((address_space(3)))
 
 // An offset past every buffer descriptor's range: loads from it give zero.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
@@ -69,31 +72,28 @@ __device__ __forceinline__ f32x4 mma<float>(u32x4 p, u32x4 q, f32x4 c) {
     return c;
 }
 
-// Every wave's loads into LDS have arrived. (A barrier alone does not wait
-// for loads from memory.)
-__device__ __forceinline__ void staged_barrier() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-}
-
 // One operand's staged step: ROWS rows of 128 bytes of k.
 //
 // LDS holds it in 16-byte chunks in the order memory has it (the loads write
-// LDS linearly, lane after lane), with the chunks of a row exchanged by a
+// LDS linearly, lane after lane), with the chunks of a line exchanged by a
 // swizzle so that the 16 lanes of a fragment read hit different banks.
 template <class T, int ROWS, bool KMAJOR, int THREADS>
 struct OperandTile {
-    static constexpr int kElems = 16 / (int)sizeof(T);          // elements of a chunk
-    static constexpr int BK = kStepBytes / (int)sizeof(T);
-    static constexpr int kBytes = ROWS * kStepBytes;
+    static constexpr int KB = kStepBytes;
+    static constexpr int kElems = 16 / (int)sizeof(T);   // elements of a chunk
+    static constexpr int BK = KB / (int)sizeof(T);
+    static constexpr int kBytes = ROWS * KB;
     static constexpr int kChunks = kBytes / 16;
-    // chunks of one line: 8 of k of a row, or the rows of one k
-    static constexpr int kLine = KMAJOR ? 8 : ROWS / kElems;
+    static constexpr int kLoads = (kChunks + THREADS - 1) / THREADS;   // of a thread, at most
+    static constexpr int kLoadsLeast = kChunks / THREADS;              // of a wave, at least
+    // chunks of a line: a row's k, or the rows of one k
+    static constexpr int kLine = KMAJOR ? KB / 16 : ROWS / kElems;
 
     static __device__ __forceinline__ int swizzle(int line) {
         if constexpr (KMAJOR) {
-            // rows differing in bits 0..3, or in bits 0, 1, 3 and 4, land on 16 different 16-byte slots of 256
-            return ((line >> 1) & 1) | ((((line >> 2) ^ (line >> 4)) & 1) << 1) | (((line >> 3) & 1) << 2);
+            // rows differing in bits 0..3, or in bits 0, 1, 3 and 4, land on
+            // 16 different 16-byte slots of 256
+            return ((line >> 1) & 1) | (((line >> 2) ^ (line >> 4)) & 1) << 1 | ((line >> 3) & 1) << 2;
         } else if constexpr (sizeof(T) == 2) {
             return kLine >= 16 ? (line & 3) << 2 : kLine == 8 ? (line & 2) << 1 : 0;
         } else {
@@ -101,31 +101,52 @@ struct OperandTile {
         }
     }
 
+    // Where a thread's chunks are, from row 0 and the step's first k: byte
+    // offsets, past the buffer's range for rows that do not exist.
+    struct Offsets {
+        uint32_t at[kLoads];
+    };
+    static __device__ __forceinline__ Offsets offsets(int64_t ld, int rows, int tid) {
+        Offsets o;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = i * THREADS + tid;
+            const int line = c / kLine, chunk = (c % kLine) ^ swizzle(line);
+            const int row = KMAJOR ? line : chunk * kElems;
+            o.at[i] = row < rows ? (uint32_t)line * (uint32_t)(ld * sizeof(T)) + (uint32_t)chunk * 16u : kNowhere;
+        }
+        return o;
+    }
+
     // Stages k in [k0, k0 + BK) of rows [0, ROWS): zero where the row is not
     // below `rows` or k not below K. `base` points at row 0 and k = 0.
     // VEC: base and ld are multiples of 16 bytes, and so is the extent of the
     // contiguous direction, so that a chunk is inside or outside as a whole.
     template <bool VEC>
-    static __device__ __forceinline__ void stage(char* lds, const T* base, int64_t ld, int rows, int k0, int K, int tid) {
+    static __device__ __forceinline__ void stage(char* lds, const T* base, int64_t ld, int rows, const Offsets& o, int k0,
+                                                 int K, int tid) {
         const T* at = KMAJOR ? base + k0 : base + (int64_t)k0 * ld;
         const int kleft = K - k0;
         if constexpr (VEC) {
             const __amdgpu_buffer_rsrc_t rsrc =
                 __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, kBufferRange, 0x00020000);
             const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+            const bool whole = kleft >= BK;
 #pragma unroll
-            for (int i = 0; i * THREADS < kChunks; ++i) {
+            for (int i = 0; i < kLoads; ++i) {
                 if (kChunks % THREADS != 0 && i * THREADS + wave * 64 >= kChunks) break;
-                const int c = i * THREADS + tid;
-                const int line = c / kLine, chunk = (c % kLine) ^ swizzle(line);
-                const int row = KMAJOR ? line : chunk * kElems, k = KMAJOR ? chunk * kElems : line;
-                const uint32_t off = (uint32_t)line * (uint32_t)(ld * sizeof(T)) + (uint32_t)chunk * 16u;
+                uint32_t off = o.at[i];
+                if (!whole) {
+                    const int c = i * THREADS + tid, line = c / kLine;
+                    const int k = KMAJOR ? ((c % kLine) ^ swizzle(line)) * kElems : line;
+                    if (k >= kleft) off = kNowhere;
+                }
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (DMR_LDS void*)(lds + (i * THREADS + wave * 64) * 16), 16,
-                                                         row < rows && k < kleft ? off : kNowhere, 0, 0, 0);
+                                                         off, 0, 0, 0);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i * THREADS < kChunks; ++i) {
+            for (int i = 0; i < kLoads; ++i) {
                 const int c = i * THREADS + tid;
                 if (kChunks % THREADS != 0 && c >= kChunks) break;
                 const int line = c / kLine, chunk = (c % kLine) ^ swizzle(line);
@@ -142,14 +163,14 @@ struct OperandTile {
         }
     }
 
-    // The fragment of 16 rows for k slice `kk` (64 bytes of k): lane l holds
-    // row row_of(l & 15) and the slice's 16-byte part l >> 4 of k. The rows
-    // are given as row_of(4 a + i) = first + stride a + i.
+    // The fragment of 16 rows for the slice `kk` (64 bytes) of k: lane l
+    // holds row row_of(l & 15) and the slice's 16-byte part l >> 4 of k. The
+    // rows are given as row_of(4 a + i) = first + stride a + i.
     static __device__ __forceinline__ u32x4 fragment(const char* lds, int kk, int first, int stride, int lane) {
         const int q = lane >> 4, r = lane & 15;
         if constexpr (KMAJOR) {
             const int row = first + stride * (r >> 2) + (r & 3);
-            return *reinterpret_cast<const u32x4*>(lds + row * kStepBytes + (((kk * 4 + q) ^ swizzle(row)) << 4));
+            return *reinterpret_cast<const u32x4*>(lds + row * KB + (((kk * 4 + q) ^ swizzle(row)) << 4));
         } else if constexpr (sizeof(T) == 2) {
             s16x4 half[2];
 #pragma unroll
@@ -173,10 +194,22 @@ struct OperandTile {
     }
 };
 
+// Waits until at most N of this wave's loads into LDS are outstanding and all
+// its reads from LDS are done, then for the other waves. (A barrier alone
+// waits for neither.)
+template <int N>
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // The tile product of one workgroup: WN x WM waves, each NT x MT blocks of
-// 16 x 16. 16-bit outputs pair neighbouring blocks of n so that a lane holds
-// eight consecutive n (16 bytes).
-template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK>
+// 16 x 16. Of 16-bit types, neighbouring blocks of n are paired so that a lane
+// holds eight consecutive n. PLANES = 2: each operand is the sum of two
+// planes, and the product of the two low ones is left out. SUMS: sum over k
+// of Q[m][k] as well.
+template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int SP, int SQ, int PLANES = 1, bool SUMS = false>
 struct TileProduct {
     static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64;
     static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
@@ -184,13 +217,23 @@ struct TileProduct {
     static constexpr bool PAIRED = sizeof(T) == 2 && NT % 2 == 0;
     using P = OperandTile<T, BN, PK, THREADS>;
     using Q = OperandTile<T, BM, QK, THREADS>;
-    static constexpr int kStage = P::kBytes + Q::kBytes;
-    static constexpr int kLdsBytes = 2 * kStage;
+    static constexpr int kP = P::kBytes * PLANES, kQ = Q::kBytes * PLANES;   // bytes of a stage
+    static constexpr int kLdsBytes = SP * kP + SQ * kQ;
+    static_assert(SP >= SQ && SQ >= 1 && kLdsBytes <= 160 * 1024, "");
+
+    struct Source {   // an operand's planes, at row 0 of the tile and k = 0
+        const T *hi, *lo;
+        int64_t ld;
+        int rows;   // that exist
+    };
+    struct Fragments {
+        u32x4 p[PLANES][NT], q[PLANES][MT];
+    };
 
     f32x4 acc[NT][MT];
-    f32x4 ones[MT];   // SUMS: sum over k of Q[m][k]
+    f32x4 ones[SUMS ? MT : 1];
 
-    // First n of this lane's values of block a (pairs: of both blocks)
+    // First n of this lane's values of block a, and its row m of block b.
     static __device__ __forceinline__ int n_of(int tid, int a) {
         const int wn = (tid >> 6) % WN, q = (tid & 63) >> 4;
         return wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 8 * q + 4 * (a & 1) : a * 16 + 4 * q);
@@ -199,35 +242,76 @@ struct TileProduct {
         return ((tid >> 6) / WN) * MT * 16 + b * 16 + (tid & 15);
     }
 
-    template <bool SUMS>
-    __device__ __forceinline__ void multiply(const char* lds, int tid) {
+    template <bool VEC>
+    static __device__ __forceinline__ void stage_p(char* lds, const Source& p, const typename P::Offsets& o, int k0, int K,
+                                                   int tid) {
+        P::template stage<VEC>(lds, p.hi, p.ld, p.rows, o, k0, K, tid);
+        if constexpr (PLANES == 2) P::template stage<VEC>(lds + P::kBytes, p.lo, p.ld, p.rows, o, k0, K, tid);
+    }
+    template <bool VEC>
+    static __device__ __forceinline__ void stage_q(char* lds, const Source& q, const typename Q::Offsets& o, int k0, int K,
+                                                   int tid) {
+        Q::template stage<VEC>(lds, q.hi, q.ld, q.rows, o, k0, K, tid);
+        if constexpr (PLANES == 2) Q::template stage<VEC>(lds + Q::kBytes, q.lo, q.ld, q.rows, o, k0, K, tid);
+    }
+
+    static __device__ __forceinline__ void read(Fragments& f, const char* lds_p, const char* lds_q, int kk, int tid) {
         const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 p[NT], q[MT];
+        for (int s = 0; s < PLANES; ++s) {
 #pragma unroll
             for (int a = 0; a < NT; ++a)
-                p[a] = P::fragment(lds, kk, wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 4 * (a & 1) : a * 16), PAIRED ? 8 : 4, lane);
+                f.p[s][a] = P::fragment(lds_p + s * P::kBytes, kk,
+                                        wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 4 * (a & 1) : a * 16), PAIRED ? 8 : 4, lane);
 #pragma unroll
-            for (int b = 0; b < MT; ++b) q[b] = Q::fragment(lds + P::kBytes, kk, (wm * MT + b) * 16, 4, lane);
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-                for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(p[a], q[b], acc[a][b]);
-            if constexpr (SUMS) {
-                constexpr uint32_t w = one_bits<T>();
-                const u32x4 one = {w, w, w, w};
-#pragma unroll
-                for (int b = 0; b < MT; ++b) ones[b] = mma<T>(one, q[b], ones[b]);
-            }
+            for (int b = 0; b < MT; ++b) f.q[s][b] = Q::fragment(lds_q + s * Q::kBytes, kk, (wm * MT + b) * 16, 4, lane);
         }
     }
 
-    // acc = sum over k in [0, K). `p` points at (n = 0, k = 0) of the tile,
-    // `rows_n` rows of it exist; `q` likewise with m.
-    template <bool VEC, bool SUMS>
-    __device__ __forceinline__ void run(char* lds, const T* p, int64_t ldp, int rows_n, const T* q, int64_t ldq, int rows_m,
-                                        int K, int tid, bool sums) {
+    __device__ __forceinline__ void multiply(const Fragments& f, bool sums) {
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int b = 0; b < MT; ++b) {
+                if constexpr (PLANES == 2) {
+                    acc[a][b] = mma<T>(f.p[0][a], f.q[1][b], acc[a][b]);
+                    acc[a][b] = mma<T>(f.p[1][a], f.q[0][b], acc[a][b]);
+                }
+                acc[a][b] = mma<T>(f.p[0][a], f.q[0][b], acc[a][b]);
+            }
+        if constexpr (SUMS)
+            if (sums) {
+                constexpr uint32_t w = one_bits<T>();
+                const u32x4 one = {w, w, w, w};
+#pragma unroll
+                for (int b = 0; b < MT; ++b) ones[b] = mma<T>(one, f.q[0][b], ones[b]);
+            }
+    }
+
+    // Loads are issued as P(0) .. P(SP - SQ - 1), then Q(t), P(t + SP - SQ)
+    // for t = 0, 1, ..; a wave's loads arrive in that order.
+    static constexpr int kAhead = SP - SQ;
+
+    // Issues the loads of the first steps of a product over k in [0, K).
+    template <bool VEC>
+    static __device__ __forceinline__ void begin(char* lds, const Source& p, const Source& q, int K, int tid) {
+        const int steps = (K + BK - 1) / BK;
+        const typename P::Offsets po = P::offsets(p.ld, p.rows, tid);
+        const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t)
+            if (t < steps) stage_p<VEC>(lds + t * kP, p, po, t * BK, K, tid);
+#pragma unroll
+        for (int t = 0; t < SQ; ++t) {
+            if (t < steps) stage_q<VEC>(lds + SP * kP + t * kQ, q, qo, t * BK, K, tid);
+            if (t + kAhead < steps) stage_p<VEC>(lds + (t + kAhead) * kP, p, po, (t + kAhead) * BK, K, tid);
+        }
+    }
+
+    // acc = sum over k in [0, K), begun with the same arguments; the LDS is
+    // free for other use afterwards. SQ = 1: K is at most one step.
+    template <bool VEC>
+    __device__ __forceinline__ void finish(char* lds, const Source& p, const Source& q, int K, int tid, bool sums = false) {
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -236,22 +320,57 @@ struct TileProduct {
 #pragma unroll
             for (int b = 0; b < MT; ++b) ones[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (K <= 0) return;
-        P::template stage<VEC>(lds, p, ldp, rows_n, 0, K, tid);
-        Q::template stage<VEC>(lds + P::kBytes, q, ldq, rows_m, 0, K, tid);
-        staged_barrier();
-        int cur = 0;
-        for (int k0 = 0; k0 < K; k0 += BK) {
-            if (k0 + BK < K) {
-                char* next = lds + (cur ^ 1) * kStage;
-                P::template stage<VEC>(next, p, ldp, rows_n, k0 + BK, K, tid);
-                Q::template stage<VEC>(next + P::kBytes, q, ldq, rows_m, k0 + BK, K, tid);
-            }
-            if (SUMS && sums) multiply<true && SUMS>(lds + cur * kStage, tid);
-            else multiply<false>(lds + cur * kStage, tid);
-            staged_barrier();
-            cur ^= 1;
+        const int steps = (K + BK - 1) / BK;
+        const typename P::Offsets po = P::offsets(p.ld, p.rows, tid);
+        const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
+        char *const lds_p = lds, *const lds_q = lds + SP * kP;
+        // After Q(t): one P if P is ahead, and both of the later steps.
+        constexpr int kPLoads = VEC ? PLANES * P::kLoadsLeast : 0, kQLoads = VEC ? PLANES * Q::kLoadsLeast : 0;
+        constexpr int kBehind = kAhead > 0 ? kPLoads : 0;
+        if (SP <= steps) step_barrier<kBehind + (SQ - 1) * (kPLoads + kQLoads)>();   // step 0 is here
+        else step_barrier<0>();
+        Fragments first, second;
+        read(first, lds_p, lds_q, 0, tid);
+        int at_p = 0, at_q = 0;   // this step's stages
+        for (int t = 0; t < steps; ++t) {
+            read(second, lds_p + at_p, lds_q + at_q, 1, tid);
+            multiply(first, sums);
+            // step t is read, and the loads of step t + 1 have arrived
+            if (SQ > 1 && t - 1 + SP < steps) step_barrier<kBehind + (SQ > 1 ? SQ - 2 : 0) * (kPLoads + kQLoads)>();
+            else step_barrier<0>();
+            if (t + SQ < steps) stage_q<VEC>(lds_q + at_q, q, qo, (t + SQ) * BK, K, tid);
+            if (t + SP < steps) stage_p<VEC>(lds_p + at_p, p, po, (t + SP) * BK, K, tid);
+            at_p = at_p + kP == SP * kP ? 0 : at_p + kP;
+            at_q = at_q + kQ == SQ * kQ ? 0 : at_q + kQ;
+            if (SQ > 1) read(first, lds_p + at_p, lds_q + at_q, 0, tid);   // past the end: not used
+            multiply(second, sums);
         }
+        step_barrier<0>();
+    }
+
+    template <bool VEC>
+    __device__ __forceinline__ void run(char* lds, const Source& p, const Source& q, int K, int tid, bool sums = false) {
+        begin<VEC>(lds, p, q, K, tid);
+        finish<VEC>(lds, p, q, K, tid, sums);
     }
 };
+
+// Stores two 16-byte chunks of a row that each of a fragment's lanes holds
+// (chunk 0 and chunk 1 of its row: 64 bytes apart or more, four lanes to 64
+// bytes) as whole 128-byte pieces of a row: neighbouring lanes, of
+// neighbouring rows, exchange a chunk, and then store the even row's two and
+// the odd row's two. put(odd row?, chunk, value).
+template <class Put>
+__device__ __forceinline__ void store_row_pairs(u32x4 c0, u32x4 c1, int lane, Put&& put) {
+    const bool odd = lane & 1;
+    u32x4 got;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t send = odd ? c0[j] : c1[j];
+        got[j] = (uint32_t)__builtin_amdgcn_mov_dpp((int)send, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+    }
+    put(false, odd ? 1 : 0, odd ? got : c0);
+    put(true, odd ? 1 : 0, odd ? c1 : got);
+}
 
 }  // namespace dmr

@@ -225,13 +225,30 @@ __device__ __forceinline__ float lift_of(float norm, float eps, int steps) {
 // Sum of squares of a slice of each matrix (float64: no overflow, and the
 // scale is exact).
 template <class T>
-__global__ __launch_bounds__(256) void orthogonalize_norm(const T* __restrict__ update, int64_t size, double* __restrict__ norm) {
+__global__ __launch_bounds__(256) void orthogonalize_norm(const T* __restrict__ update, int64_t size, bool wide,
+                                                          double* __restrict__ norm) {
     __shared__ double part[4];
-    const int64_t at = (int64_t)(blockIdx.x / kNormBlocks) * size;
+    constexpr int E = 16 / (int)sizeof(T);
+    const T* u = update + (int64_t)(blockIdx.x / kNormBlocks) * size;
+    const int64_t at = (int64_t)(blockIdx.x % kNormBlocks) * 256 + threadIdx.x;
+    constexpr int64_t stride = kNormBlocks * 256;
     double sum = 0.0;
-    for (int64_t i = (int64_t)(blockIdx.x % kNormBlocks) * 256 + threadIdx.x; i < size; i += kNormBlocks * 256) {
-        const double v = (double)(float)update[at + i];
-        sum += v * v;
+    if (wide) {
+        const int64_t chunks = size / E;
+        for (int64_t i = at; i < chunks; i += 4 * stride) {
+            alignas(16) T v[4][E];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)   // past the end: the last chunk again, not added
+                *reinterpret_cast<u32x4*>(v[j]) =
+                    reinterpret_cast<const u32x4*>(u)[i + j * stride < chunks ? i + j * stride : chunks - 1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j * stride < chunks)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sum += (double)(float)v[j][e] * (double)(float)v[j][e];
+        }
+    } else {
+        for (int64_t i = at; i < size; i += stride) sum += (double)(float)u[i] * (double)(float)u[i];
     }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
@@ -285,82 +302,6 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
     }
 }
 
-// C[m][n] = sum_k Q[m][k] P[n][k] of float16 planes; PLANES = 2 adds the
-// cross products of high and low parts.
-template <int BN_, int BM_, int WN, int WM, bool PK, int PLANES>
-struct PlanesProduct {
-    static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64;
-    static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
-    using P = OperandTile<h16, BN, PK, THREADS>;
-    using Q = OperandTile<h16, BM, true, THREADS>;
-    static constexpr int kStage = (P::kBytes + Q::kBytes) * PLANES;
-    static constexpr int kLdsBytes = 2 * kStage;
-    f32x4 acc[NT][MT];
-
-    // blocks of n are paired: a lane holds eight consecutive n of each pair
-    static __device__ __forceinline__ int n_of(int tid, int a) {
-        return ((tid >> 6) % WN) * NT * 16 + (a >> 1) * 32 + 8 * ((tid & 63) >> 4) + 4 * (a & 1);
-    }
-    static __device__ __forceinline__ int m_of(int tid, int b) {
-        return ((tid >> 6) / WN) * MT * 16 + b * 16 + (tid & 15);
-    }
-
-    static __device__ __forceinline__ void stage(char* lds, const h16* phi, const h16* plo, int ldp, int rows_n,
-                                                 const h16* qhi, const h16* qlo, int ldq, int rows_m, int k0, int K, int tid) {
-        P::template stage<true>(lds, phi, ldp, rows_n, k0, K, tid);
-        Q::template stage<true>(lds + P::kBytes * PLANES, qhi, ldq, rows_m, k0, K, tid);
-        if constexpr (PLANES == 2) {
-            P::template stage<true>(lds + P::kBytes, plo, ldp, rows_n, k0, K, tid);
-            Q::template stage<true>(lds + P::kBytes * 2 + Q::kBytes, qlo, ldq, rows_m, k0, K, tid);
-        }
-    }
-
-    __device__ __forceinline__ void multiply(const char* lds, int tid) {
-        const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 p[PLANES][NT], q[PLANES][MT];
-#pragma unroll
-            for (int s = 0; s < PLANES; ++s) {
-#pragma unroll
-                for (int a = 0; a < NT; ++a)
-                    p[s][a] = P::fragment(lds + s * P::kBytes, kk, wn * NT * 16 + (a >> 1) * 32 + 4 * (a & 1), 8, lane);
-#pragma unroll
-                for (int b = 0; b < MT; ++b)
-                    q[s][b] = Q::fragment(lds + P::kBytes * PLANES + s * Q::kBytes, kk, (wm * MT + b) * 16, 4, lane);
-            }
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-                for (int b = 0; b < MT; ++b) {
-                    if constexpr (PLANES == 2) {
-                        acc[a][b] = mma<h16>(p[0][a], q[1][b], acc[a][b]);
-                        acc[a][b] = mma<h16>(p[1][a], q[0][b], acc[a][b]);
-                    }
-                    acc[a][b] = mma<h16>(p[0][a], q[0][b], acc[a][b]);
-                }
-        }
-    }
-
-    __device__ __forceinline__ void run(char* lds, const h16* phi, const h16* plo, int ldp, int rows_n, const h16* qhi,
-                                        const h16* qlo, int ldq, int rows_m, int K, int tid) {
-#pragma unroll
-        for (int a = 0; a < NT; ++a)
-#pragma unroll
-            for (int b = 0; b < MT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        stage(lds, phi, plo, ldp, rows_n, qhi, qlo, ldq, rows_m, 0, K, tid);
-        staged_barrier();
-        int cur = 0;
-        for (int k0 = 0; k0 < K; k0 += P::BK) {
-            if (k0 + P::BK < K)
-                stage(lds + (cur ^ 1) * kStage, phi, plo, ldp, rows_n, qhi, qlo, ldq, rows_m, k0 + P::BK, K, tid);
-            multiply(lds + cur * kStage, tid);
-            staged_barrier();
-            cur ^= 1;
-        }
-    }
-};
-
 // Tile (ti, tj), ti >= tj, of the lower triangle.
 __device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
     ti = (int)((__builtin_sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
@@ -369,20 +310,15 @@ __device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
     tj = id - ti * (ti + 1) / 2;
 }
 
-struct Square {   // the planes of one [sp, sp] matrix and its diagonal
-    h16 *hi, *lo;
-    float* diag;
-};
-
 // Off-diagonal pairs and the diagonal of a symmetric matrix, from the tiles
 // of its lower triangle: POLY = false: A = X X^T; true: B = b A + c A A.
-template <int BT, int WN, int WM, int PLANES, bool POLY>
-__global__ __launch_bounds__(WN * WM * 64) void orthogonalize_square(const h16* __restrict__ hi, const h16* __restrict__ lo,
+template <class Tile, int PLANES, bool POLY>
+__global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16* __restrict__ hi, const h16* __restrict__ lo,
                                                                      int sp, int K, const float* __restrict__ lift,
                                                                      const float* __restrict__ diag,
                                                                      h16* __restrict__ out_hi, h16* __restrict__ out_lo,
                                                                      float* __restrict__ out_diag, int tiles) {
-    using Tile = PlanesProduct<BT, BT, WN, WM, true, PLANES>;
+    constexpr int BT = Tile::BN;
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
     int ti, tj;
     const int64_t b = blockIdx.x / tiles;
@@ -390,8 +326,8 @@ __global__ __launch_bounds__(WN * WM * 64) void orthogonalize_square(const h16* 
     const int tid = threadIdx.x, m0 = ti * BT, n0 = tj * BT;
     const int64_t at = b * (int64_t)sp * K, out_at = b * (int64_t)sp * sp;
     Tile t;
-    t.run(lds, hi + at + (int64_t)n0 * K, lo + at + (int64_t)n0 * K, K, sp - n0, hi + at + (int64_t)m0 * K,
-          lo + at + (int64_t)m0 * K, K, sp - m0, K, tid);
+    t.template run<true>(lds, {hi + at + (int64_t)n0 * K, lo + at + (int64_t)n0 * K, K, sp - n0},
+                         {hi + at + (int64_t)m0 * K, lo + at + (int64_t)m0 * K, K, sp - m0}, K, tid);
     out_hi += out_at;
     out_lo += out_at;
     out_diag += b * sp;
@@ -443,13 +379,14 @@ __global__ __launch_bounds__(WN * WM * 64) void orthogonalize_square(const h16* 
     }
 }
 
-// X <- (a + B_ii) X_i + (off-diagonal B) X; the last step writes the result
-// in its own type and orientation.
-template <int BN, int BM, int WN, int WM, int PLANES>
-__global__ __launch_bounds__(WN * WM * 64) void orthogonalize_update(
+// X <- (a + B_ii) X_i + (off-diagonal B) X. LAST: the result goes to `out` in
+// its own type and orientation ([m, n], transposed if `turned`) instead.
+template <class T, class Tile, bool LAST>
+__global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
     const h16* __restrict__ bhi, const h16* __restrict__ blo, const float* __restrict__ bdiag, const h16* __restrict__ xhi,
-    const h16* __restrict__ xlo, int sp, int lp, h16* __restrict__ yhi, h16* __restrict__ ylo, int tiles_n, int tiles) {
-    using Tile = PlanesProduct<BN, BM, WN, WM, false, PLANES>;
+    const h16* __restrict__ xlo, int sp, int lp, h16* __restrict__ yhi, h16* __restrict__ ylo, int tiles_n, int tiles,
+    const float* __restrict__ lift, T* __restrict__ out, int s, int l, bool turned, bool wide) {
+    constexpr int BN = Tile::BN, BM = Tile::BM;
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
     const int64_t b = blockIdx.x / tiles;
     const int tile = (int)(blockIdx.x % tiles);
@@ -457,8 +394,13 @@ __global__ __launch_bounds__(WN * WM * 64) void orthogonalize_update(
     const int tid = threadIdx.x;
     const int64_t xat = b * (int64_t)sp * lp, bat = b * (int64_t)sp * sp + (int64_t)m0 * sp;
     Tile t;
-    t.run(lds, xhi + xat + n0, xlo + xat + n0, lp, lp - n0, bhi + bat, blo + bat, sp, sp - m0, sp, tid);
+    t.template run<true>(lds, {xhi + xat + n0, xlo + xat + n0, lp, lp - n0}, {bhi + bat, blo + bat, sp, sp - m0}, sp, tid);
     bdiag += b * sp;
+    float back = 1.0f;
+    if constexpr (LAST) {
+        back = 1.0f / (kScaleX * lift[b]);
+        out += b * (int64_t)s * l;
+    }
 #pragma unroll
     for (int a = 0; a < Tile::NT; a += 2) {
         const int n = n0 + Tile::n_of(tid, a);
@@ -470,41 +412,40 @@ __global__ __launch_bounds__(WN * WM * 64) void orthogonalize_update(
             const int64_t at = xat + (int64_t)m * lp + n;
             const f16x8 ohi = *reinterpret_cast<const f16x8*>(xhi + at), olo = *reinterpret_cast<const f16x8*>(xlo + at);
             const float scale = kA + bdiag[m];
-            f16x8 vhi, vlo;
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h16 h, l;
-                split(scale * ((float)ohi[i] + (float)olo[i]) + t.acc[a + (i >> 2)][c][i & 3] * (1.0f / kScaleB), h, l);
-                vhi[i] = h;
-                vlo[i] = l;
+            for (int i = 0; i < 8; ++i)
+                v[i] = scale * ((float)ohi[i] + (float)olo[i]) + t.acc[a + (i >> 2)][c][i & 3] * (1.0f / kScaleB);
+            if constexpr (!LAST) {
+                f16x8 vhi, vlo;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h16 h, w;
+                    split(v[i], h, w);
+                    vhi[i] = h;
+                    vlo[i] = w;
+                }
+                *reinterpret_cast<f16x8*>(yhi + at) = vhi;
+                *reinterpret_cast<f16x8*>(ylo + at) = vlo;
+            } else if (m < s) {
+                if (!turned && wide) {   // rows of whole 16 bytes
+                    if (n < l) {
+                        struct alignas(16) Row { T v[8]; } row;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) row.v[i] = (T)(v[i] * back);
+                        T* to = out + (int64_t)m * l + n;
+                        if (sizeof(T) == 2 || n + 4 < l) *reinterpret_cast<Row*>(to) = row;
+                        else
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) to[i] = row.v[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (n + i < l) out[turned ? (int64_t)(n + i) * s + m : (int64_t)m * l + n + i] = (T)(v[i] * back);
+                }
             }
-            *reinterpret_cast<f16x8*>(yhi + at) = vhi;
-            *reinterpret_cast<f16x8*>(ylo + at) = vlo;
         }
-    }
-}
-
-// The result in its own type and orientation, a 64 x 64 tile a workgroup.
-template <class T>
-__global__ __launch_bounds__(256) void orthogonalize_end(const h16* __restrict__ xhi, const h16* __restrict__ xlo, int sp,
-                                                         int lp, const float* __restrict__ lift, T* __restrict__ out, int m,
-                                                         int n) {
-    __shared__ float tile[64][65];
-    const int tiles_l = lp / 64, tiles = tiles_l * (sp / 64);
-    const int64_t b = blockIdx.x / tiles;
-    const int i0 = (int)(blockIdx.x % tiles) / tiles_l * 64, j0 = (int)(blockIdx.x % tiles) % tiles_l * 64;
-    const int tid = threadIdx.x;
-    const float back = 1.0f / (kScaleX * lift[b]);
-    for (int r = tid >> 6; r < 64; r += 4) {
-        const int64_t at = ((int64_t)b * sp + i0 + r) * lp + j0 + (tid & 63);
-        tile[r][tid & 63] = ((float)xhi[at] + (float)xlo[at]) * back;
-    }
-    __syncthreads();
-    const bool turned = m > n;
-    const int r0 = turned ? j0 : i0, c0 = turned ? i0 : j0;
-    for (int r = tid >> 6; r < 64; r += 4) {
-        const int row = r0 + r, col = c0 + (tid & 63);
-        if (row < m && col < n) out[(b * m + row) * n + col] = (T)(turned ? tile[tid & 63][r] : tile[r][tid & 63]);
     }
 }
 
@@ -515,31 +456,40 @@ hipError_t allow_lds(Kernel kernel, int bytes) {
                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int BT, int WN, int WM, int PLANES, bool POLY>
+template <class Tile, int PLANES, bool POLY>
 hipError_t launch_square(int64_t B, const h16* hi, const h16* lo, int sp, int K, const float* lift, const float* diag, h16* out_hi, h16* out_lo,
                          float* out_diag, hipStream_t stream) {
-    const int t = (sp + BT - 1) / BT, tiles = t * (t + 1) / 2;
-    orthogonalize_square<BT, WN, WM, PLANES, POLY><<<(unsigned)(B * tiles), WN * WM * 64, 0, stream>>>(
+    const int t = (sp + Tile::BN - 1) / Tile::BN, tiles = t * (t + 1) / 2;
+    orthogonalize_square<Tile, PLANES, POLY><<<(unsigned)(B * tiles), Tile::THREADS, 0, stream>>>(
         hi, lo, sp, K, lift, diag, out_hi, out_lo, out_diag, tiles);
     return hipGetLastError();
 }
 
-template <int BT, int WN, int WM, int PLANES>
-hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w, int& cur) {
+// Tiles of BT x BT by WN x WM waves, staged in rings of SP and SQ.
+template <class T, int BT, int WN, int WM, int SP, int SQ, int PLANES>
+hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w) {
     auto half = [&](int64_t o) { return reinterpret_cast<h16*>(a.workspace + o); };
     auto real = [&](int64_t o) { return reinterpret_cast<float*>(a.workspace + o); };
+    using Square = TileProduct<h16, BT, BT, WN, WM, true, true, SP, SQ, PLANES>;
+    using Update = TileProduct<h16, BT, BT, WN, WM, false, true, SP, SQ, PLANES>;
     hipError_t err = hipSuccess;
+    int cur = 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.n % (16 / (int)sizeof(T)) == 0;
     const int tiles_n = (w.lp + BT - 1) / BT, tiles = tiles_n * ((w.sp + BT - 1) / BT);
     for (int k = 0; k < a.steps && err == hipSuccess; ++k) {
-        err = launch_square<BT, WN, WM, PLANES, false>(a.B, half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, real(w.lift), nullptr,
+        err = launch_square<Square, PLANES, false>(a.B, half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, real(w.lift), nullptr,
                                                        half(w.ohi), half(w.olo), real(w.diag), a.stream);
         if (err != hipSuccess) break;
-        err = launch_square<BT, WN, WM, PLANES, true>(a.B, half(w.ohi), half(w.olo), w.sp, w.sp, nullptr, real(w.diag), half(w.bhi),
+        err = launch_square<Square, PLANES, true>(a.B, half(w.ohi), half(w.olo), w.sp, w.sp, nullptr, real(w.diag), half(w.bhi),
                                                       half(w.blo), real(w.bdiag), a.stream);
         if (err != hipSuccess) break;
-        orthogonalize_update<BT, BT, WN, WM, PLANES><<<(unsigned)(a.B * tiles), WN * WM * 64, 0, a.stream>>>(
-            half(w.bhi), half(w.blo), real(w.bdiag), half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, half(w.xhi[cur ^ 1]),
-            half(w.xlo[cur ^ 1]), tiles_n, tiles);
+        auto update = [&](auto kernel) {
+            kernel<<<(unsigned)(a.B * tiles), Update::THREADS, 0, a.stream>>>(
+                half(w.bhi), half(w.blo), real(w.bdiag), half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, half(w.xhi[cur ^ 1]),
+                half(w.xlo[cur ^ 1]), tiles_n, tiles, real(w.lift), static_cast<T*>(a.out), w.s, w.l, a.m > a.n, wide);
+        };
+        if (k + 1 < a.steps) update(orthogonalize_update<T, Update, false>);
+        else update(orthogonalize_update<T, Update, true>);
         err = hipGetLastError();
         cur ^= 1;
     }
@@ -555,21 +505,17 @@ hipError_t launch_tiled(const OrthogonalizeArgs& a) {
     double* norm = reinterpret_cast<double*>(a.workspace + w.norm);
     float* lift = reinterpret_cast<float*>(a.workspace + w.lift);
     const unsigned tiles64 = (unsigned)(a.B * (w.sp / 64) * (w.lp / 64));
-    orthogonalize_norm<T><<<(unsigned)(a.B * kNormBlocks), 256, 0, a.stream>>>(u, (int64_t)a.m * a.n, norm);
+    const int64_t size = (int64_t)a.m * a.n;
+    orthogonalize_norm<T><<<(unsigned)(a.B * kNormBlocks), 256, 0, a.stream>>>(
+        u, size, (reinterpret_cast<uintptr_t>(u) & 15) == 0 && size * sizeof(T) % 16 == 0, norm);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     orthogonalize_begin<T><<<tiles64, 256, 0, a.stream>>>(u, a.m, a.n, a.eps, a.steps, norm, w.sp, w.lp, x0, x1, lift);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
-    int cur = 0;
     const int64_t t128 = (w.sp + 127) / 128;
-    if (a.B * t128 * (t128 + 1) / 2 >= 128) err = launch_steps<128, 2, 4, PLANES>(a, w, cur);
-    else err = launch_steps<64, 2, 2, PLANES>(a, w, cur);
-    if (err != hipSuccess) return err;
-    orthogonalize_end<T><<<tiles64, 256, 0, a.stream>>>(reinterpret_cast<h16*>(a.workspace + w.xhi[cur]),
-                                                        reinterpret_cast<h16*>(a.workspace + w.xlo[cur]), w.sp, w.lp,
-                                                        lift, static_cast<T*>(a.out), a.m, a.n);
-    return hipGetLastError();
+    if (a.B * t128 * (t128 + 1) / 2 >= 128) return launch_steps<T, 128, 4, 4, 2, 2, PLANES>(a, w);
+    return launch_steps<T, 64, 2, 2, 4, 4, PLANES>(a, w);
 }
 
 template <class T>
