@@ -187,10 +187,10 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restric
     const auto column = [&](uint32_t place) { return (int)(tile_of_workgroup<kRun>(place) % n_tiles) * Tile::BN; };
     const auto weights = [&](const RowTile& at, int n0) {
         const T* w = weight + at.group * (int64_t)n_out * k_in + (WK ? (int64_t)n0 * k_in : (int64_t)n0);
-        return typename Tile::Source{w, nullptr, WK ? k_in : n_out, n_out - n0};
+        return typename Tile::Source{w, WK ? k_in : n_out, n_out - n0};
     };
     const auto rows_of = [&](const RowTile& at) {
-        return typename Tile::Source{rows_in + at.first * (int64_t)k_in, nullptr, k_in, at.rows};
+        return typename Tile::Source{rows_in + at.first * (int64_t)k_in, k_in, at.rows};
     };
     // A workgroup that takes several tiles finds the next one while a tile is
     // multiplied and issues its first loads before it stores.
@@ -274,8 +274,8 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
     const bool sums = n0 == 0 && grad_bias != nullptr;
     if (!grad_weight && !sums) return;
     Tile t;
-    t.template run<VEC>(lds, {x + at.first * cin + n0, nullptr, cin, cin - n0},
-                        {g + at.first * cout + m0, nullptr, cout, cout - m0}, at.rows, tid, sums);
+    t.template run<VEC>(lds, {x + at.first * cin + n0, cin, cin - n0},
+                        {g + at.first * cout + m0, cout, cout - m0}, at.rows, tid, sums);
     const int rows = cout - m0 < Tile::BM ? cout - m0 : Tile::BM;
     const int lane = tid & 63;
     const bool first_n = Tile::n_of(tid, 0) == 0 && lane < 16;   // one lane per m holds the row's sum
@@ -454,13 +454,13 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
         bool done = false;
         if constexpr (sizeof(T) == 2)
             if (p.side == 256 && vec) {
-                err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, 2, 1, true>>(a, p, vec, wide);
+                err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, 2, true>>(a, p, vec, wide);
                 done = true;
             }
         if (!done)
             err = p.side == 64
-                      ? launch_weight_tile<T, TileProduct<T, 64, 64, 2, 2, false, false, 2, 2, 1, true>>(a, p, vec, wide)
-                      : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, 2, 1, true>>(a, p, vec, wide);
+                      ? launch_weight_tile<T, TileProduct<T, 64, 64, 2, 2, false, false, 2, 2, true>>(a, p, vec, wide)
+                      : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, 2, true>>(a, p, vec, wide);
         if (err == hipSuccess && p.slots > 0) {
             const int64_t weights = (int64_t)a.cin * a.cout, values = weights + a.cout;
             const int64_t blocks = (values + kAddValues - 1) / kAddValues;

@@ -72,14 +72,13 @@ __device__ __forceinline__ f32x4 mma<float>(u32x4 p, u32x4 q, f32x4 c) {
     return c;
 }
 
-// One operand's staged step: ROWS rows of 128 bytes of k.
+// One operand's staged step: ROWS rows of KB bytes of k (K-major: 128).
 //
 // LDS holds it in 16-byte chunks in the order memory has it (the loads write
 // LDS linearly, lane after lane), with the chunks of a line exchanged by a
 // swizzle so that the 16 lanes of a fragment read hit different banks.
-template <class T, int ROWS, bool KMAJOR, int THREADS>
+template <class T, int ROWS, bool KMAJOR, int THREADS, int KB = kStepBytes>
 struct OperandTile {
-    static constexpr int KB = kStepBytes;
     static constexpr int kElems = 16 / (int)sizeof(T);   // elements of a chunk
     static constexpr int BK = KB / (int)sizeof(T);
     static constexpr int kBytes = ROWS * KB;
@@ -206,10 +205,8 @@ __device__ __forceinline__ void step_barrier() {
 
 // The tile product of one workgroup: WN x WM waves, each NT x MT blocks of
 // 16 x 16. Of 16-bit types, neighbouring blocks of n are paired so that a lane
-// holds eight consecutive n. PLANES = 2: each operand is the sum of two
-// planes, and the product of the two low ones is left out. SUMS: sum over k
-// of Q[m][k] as well.
-template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int SP, int SQ, int PLANES = 1, bool SUMS = false>
+// holds eight consecutive n. SUMS: sum over k of Q[m][k] as well.
+template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int SP, int SQ, bool SUMS = false>
 struct TileProduct {
     static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64;
     static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
@@ -217,17 +214,17 @@ struct TileProduct {
     static constexpr bool PAIRED = sizeof(T) == 2 && NT % 2 == 0;
     using P = OperandTile<T, BN, PK, THREADS>;
     using Q = OperandTile<T, BM, QK, THREADS>;
-    static constexpr int kP = P::kBytes * PLANES, kQ = Q::kBytes * PLANES;   // bytes of a stage
+    static constexpr int kP = P::kBytes, kQ = Q::kBytes;   // bytes of a stage
     static constexpr int kLdsBytes = SP * kP + SQ * kQ;
     static_assert(SP >= SQ && SQ >= 1 && kLdsBytes <= 160 * 1024, "");
 
-    struct Source {   // an operand's planes, at row 0 of the tile and k = 0
-        const T *hi, *lo;
+    struct Source {   // an operand, at row 0 of the tile and k = 0
+        const T* at;
         int64_t ld;
         int rows;   // that exist
     };
     struct Fragments {
-        u32x4 p[PLANES][NT], q[PLANES][MT];
+        u32x4 p[NT], q[MT];
     };
 
     f32x4 acc[NT][MT];
@@ -245,46 +242,34 @@ struct TileProduct {
     template <bool VEC>
     static __device__ __forceinline__ void stage_p(char* lds, const Source& p, const typename P::Offsets& o, int k0, int K,
                                                    int tid) {
-        P::template stage<VEC>(lds, p.hi, p.ld, p.rows, o, k0, K, tid);
-        if constexpr (PLANES == 2) P::template stage<VEC>(lds + P::kBytes, p.lo, p.ld, p.rows, o, k0, K, tid);
+        P::template stage<VEC>(lds, p.at, p.ld, p.rows, o, k0, K, tid);
     }
     template <bool VEC>
     static __device__ __forceinline__ void stage_q(char* lds, const Source& q, const typename Q::Offsets& o, int k0, int K,
                                                    int tid) {
-        Q::template stage<VEC>(lds, q.hi, q.ld, q.rows, o, k0, K, tid);
-        if constexpr (PLANES == 2) Q::template stage<VEC>(lds + Q::kBytes, q.lo, q.ld, q.rows, o, k0, K, tid);
+        Q::template stage<VEC>(lds, q.at, q.ld, q.rows, o, k0, K, tid);
     }
 
     static __device__ __forceinline__ void read(Fragments& f, const char* lds_p, const char* lds_q, int kk, int tid) {
         const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
 #pragma unroll
-        for (int s = 0; s < PLANES; ++s) {
+        for (int a = 0; a < NT; ++a)
+            f.p[a] = P::fragment(lds_p, kk, wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 4 * (a & 1) : a * 16), PAIRED ? 8 : 4, lane);
 #pragma unroll
-            for (int a = 0; a < NT; ++a)
-                f.p[s][a] = P::fragment(lds_p + s * P::kBytes, kk,
-                                        wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 4 * (a & 1) : a * 16), PAIRED ? 8 : 4, lane);
-#pragma unroll
-            for (int b = 0; b < MT; ++b) f.q[s][b] = Q::fragment(lds_q + s * Q::kBytes, kk, (wm * MT + b) * 16, 4, lane);
-        }
+        for (int b = 0; b < MT; ++b) f.q[b] = Q::fragment(lds_q, kk, (wm * MT + b) * 16, 4, lane);
     }
 
     __device__ __forceinline__ void multiply(const Fragments& f, bool sums) {
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
-            for (int b = 0; b < MT; ++b) {
-                if constexpr (PLANES == 2) {
-                    acc[a][b] = mma<T>(f.p[0][a], f.q[1][b], acc[a][b]);
-                    acc[a][b] = mma<T>(f.p[1][a], f.q[0][b], acc[a][b]);
-                }
-                acc[a][b] = mma<T>(f.p[0][a], f.q[0][b], acc[a][b]);
-            }
+            for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(f.p[a], f.q[b], acc[a][b]);
         if constexpr (SUMS)
             if (sums) {
                 constexpr uint32_t w = one_bits<T>();
                 const u32x4 one = {w, w, w, w};
 #pragma unroll
-                for (int b = 0; b < MT; ++b) ones[b] = mma<T>(one, f.q[0][b], ones[b]);
+                for (int b = 0; b < MT; ++b) ones[b] = mma<T>(one, f.q[b], ones[b]);
             }
     }
 
@@ -325,7 +310,7 @@ struct TileProduct {
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
         char *const lds_p = lds, *const lds_q = lds + SP * kP;
         // After Q(t): one P if P is ahead, and both of the later steps.
-        constexpr int kPLoads = VEC ? PLANES * P::kLoadsLeast : 0, kQLoads = VEC ? PLANES * Q::kLoadsLeast : 0;
+        constexpr int kPLoads = VEC ? P::kLoadsLeast : 0, kQLoads = VEC ? Q::kLoadsLeast : 0;
         constexpr int kBehind = kAhead > 0 ? kPLoads : 0;
         if (SP <= steps) step_barrier<kBehind + (SQ - 1) * (kPLoads + kQLoads)>();   // step 0 is here
         else step_barrier<0>();
@@ -352,6 +337,96 @@ struct TileProduct {
     __device__ __forceinline__ void run(char* lds, const Source& p, const Source& q, int K, int tid, bool sums = false) {
         begin<VEC>(lds, p, q, K, tid);
         finish<VEC>(lds, p, q, K, tid, sums);
+    }
+};
+
+// The same product of operands that are pairs of float16, high + low: high
+// high + high low + low high, three matrix instructions for one. In memory the
+// 32 high parts of a block of 32 values are followed by their 32 low parts,
+// so that a cache line of a row is a step of 32 k with both; row strides
+// count float16. The step is long for its bytes (1.5 times that of one plane),
+// so a plain ring of S stages feeds it: the loads of step t + S - 1 are issued
+// as step t begins.
+template <int BN_, int BM_, int WN, int WM, bool PK, int S>
+struct PairProduct {
+    typedef _Float16 T;
+    static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64;
+    static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
+    static constexpr bool PAIRED = true;
+    static_assert(NT % 2 == 0 && S >= 2, "");
+    // M-major, the 2 BN float16 of a line and 32 lines
+    using P = OperandTile<T, PK ? BN : 2 * BN, PK, THREADS, PK ? 128 : 64>;
+    using Q = OperandTile<T, BM, true, THREADS>;
+    static constexpr int kStage = P::kBytes + Q::kBytes, kLdsBytes = S * kStage;
+    static_assert(kLdsBytes <= 160 * 1024, "");
+
+    struct Source {
+        const T* at;
+        int64_t ld;
+        int rows;   // that exist (M-major: values of a line)
+    };
+
+    f32x4 acc[NT][MT];
+
+    static __device__ __forceinline__ int n_of(int tid, int a) {
+        return ((tid >> 6) % WN) * NT * 16 + (a >> 1) * 32 + 8 * ((tid & 63) >> 4) + 4 * (a & 1);
+    }
+    static __device__ __forceinline__ int m_of(int tid, int b) {
+        return ((tid >> 6) / WN) * MT * 16 + b * 16 + (tid & 15);
+    }
+
+    // acc = sum over k in [0, K), K a multiple of 32; the LDS is free for
+    // other use afterwards.
+    __device__ __forceinline__ void run(char* lds, const Source& p, const Source& q, int K, int tid) {
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int b = 0; b < MT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int steps = K / 32;
+        const int rows_p = PK ? p.rows : 2 * p.rows;
+        const typename P::Offsets po = P::offsets(p.ld, rows_p, tid);
+        const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
+        constexpr int kLoads = P::kLoadsLeast + Q::kLoadsLeast;
+        const auto stage = [&](char* to, int t) {
+            P::template stage<true>(to, p.at, p.ld, rows_p, po, t * P::BK, steps * P::BK, tid);
+            Q::template stage<true>(to + P::kBytes, q.at, q.ld, q.rows, qo, t * Q::BK, steps * Q::BK, tid);
+        };
+#pragma unroll
+        for (int t = 0; t < S - 1; ++t)
+            if (t < steps) stage(lds + t * kStage, t);
+        const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
+        int cur = 0;
+        for (int t = 0; t < steps; ++t) {
+            // step t has arrived, and step t - 1 is multiplied
+            if (t + S - 1 <= steps) step_barrier<kLoads * (S - 2)>();
+            else step_barrier<0>();
+            if (t + S - 1 < steps) stage(lds + (cur == 0 ? kLdsBytes - kStage : cur - kStage), t + S - 1);
+            const char* at = lds + cur;
+            u32x4 pf[2][NT], qf[2][MT];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    const int n = wn * NT * 16 + (a >> 1) * 32, i = 4 * (a & 1);
+                    pf[s][a] = PK ? P::fragment(at, s, n + i, 8, lane) : P::fragment(at, 0, 2 * n + 32 * s + i, 8, lane);
+                }
+#pragma unroll
+                for (int b = 0; b < MT; ++b) qf[s][b] = Q::fragment(at + P::kBytes, s, (wm * MT + b) * 16, 4, lane);
+            }
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(pf[0][a], qf[0][b], acc[a][b]);
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int b = 0; b < MT; ++b) {
+                    acc[a][b] = mma<T>(pf[0][a], qf[1][b], acc[a][b]);
+                    acc[a][b] = mma<T>(pf[1][a], qf[0][b], acc[a][b]);
+                }
+            cur = cur + kStage == kLdsBytes ? 0 : cur + kStage;
+        }
+        step_barrier<0>();
     }
 };
 

@@ -163,14 +163,16 @@ __global__ __launch_bounds__(kSmallThreads) void orthogonalize_small(const T* __
 // ---------------------------------------------------------------------------
 
 // Sides are padded to multiples of kPad with zeros, which the iteration
-// keeps; the planes below are [sp, lp] or [sp, sp].
+// keeps. X is [sp, lp], the off-diagonal A and B are [sp, sp]. With PLANES = 2
+// they are held as the pairs that PairProduct reads (32 high parts, 32 low
+// parts, ..); with PLANES = 1 the high parts are a plane for TileProduct, and
+// the low parts of X, which no product reads, another one after it.
 constexpr int kPad = 64;
 constexpr int kNormBlocks = 64;
 
 struct Layout {
     int s, l, sp, lp;
-    int64_t xs, as;          // values of a plane of X, of A
-    int64_t xhi[2], xlo[2], ohi, olo, bhi, blo, diag, bdiag, norm, lift;   // byte offsets, each for the whole batch
+    int64_t x[2], o, b, diag, bdiag, norm, lift;   // byte offsets, each for the whole batch
     size_t bytes;
 };
 
@@ -180,22 +182,16 @@ Layout layout(int64_t B, int m, int n, bool two) {
     w.l = m < n ? n : m;
     w.sp = (w.s + kPad - 1) / kPad * kPad;
     w.lp = (w.l + kPad - 1) / kPad * kPad;
-    w.xs = (int64_t)w.sp * w.lp;
-    w.as = (int64_t)w.sp * w.sp;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = at;
         at += (bytes + 255) / 256 * 256;
         return o;
     };
-    for (int k = 0; k < 2; ++k) {
-        w.xhi[k] = take(B * w.xs * 2);
-        w.xlo[k] = take(B * w.xs * 2);
-    }
-    w.ohi = take(B * w.as * 2);
-    w.olo = two ? take(B * w.as * 2) : w.ohi;
-    w.bhi = take(B * w.as * 2);
-    w.blo = two ? take(B * w.as * 2) : w.bhi;
+    const int64_t xs = B * w.sp * w.lp, as = B * w.sp * w.sp;
+    for (int k = 0; k < 2; ++k) w.x[k] = take(xs * 4);
+    w.o = take(as * (two ? 4 : 2));
+    w.b = take(as * (two ? 4 : 2));
     w.diag = take(B * w.sp * 4);
     w.bdiag = take(B * w.sp * 4);
     w.norm = take(B * kNormBlocks * 8);
@@ -204,7 +200,19 @@ Layout layout(int64_t B, int m, int n, bool two) {
     return w;
 }
 
+// Where a matrix of rows of `ld` values holds value n of row m: its high
+// part, in float16 from the matrix's start.
+template <int PLANES>
+__device__ __forceinline__ int64_t place(int64_t m, int ld, int n) {
+    return PLANES == 2 ? m * 2 * ld + (n >> 5) * 64 + (n & 31) : m * ld + n;
+}
+
+// v as a pair. v is pinned to its float32 value first: the compiler may
+// otherwise round the product or sum that gives it straight to float16 for the
+// high part, and take the low part from the float32 one, which a tie apart are
+// not the same number.
 __device__ __forceinline__ void split(float v, h16& hi, h16& lo) {
+    asm("" : "+v"(v));
     hi = (h16)v;
     lo = (h16)(v - (float)hi);
 }
@@ -258,12 +266,11 @@ __global__ __launch_bounds__(256) void orthogonalize_norm(const T* __restrict__ 
 }
 
 // X_0 as float16 pairs, padded; a 64 x 64 tile a workgroup, through LDS when
-// the update is taken transposed.
-template <class T>
+// the update is taken transposed. `low`: from a high part to its low part.
+template <class T, int PLANES>
 __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__ update, int m, int n, float eps,
                                                            int steps, const double* __restrict__ norm, int sp, int lp,
-                                                           h16* __restrict__ xhi, h16* __restrict__ xlo,
-                                                           float* __restrict__ lift) {
+                                                           h16* __restrict__ x, int64_t low, float* __restrict__ lift) {
     __shared__ float tile[64][65];
     __shared__ float s_inv;
     const int tiles_l = lp / 64, tiles = tiles_l * (sp / 64);
@@ -293,14 +300,31 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
     }
     __syncthreads();
     const float inv = s_inv;
-    for (int r = tid >> 6; r < 64; r += 4) {
-        h16 hi, lo;
-        split(tile[r][tid & 63] * inv, hi, lo);
-        const int64_t at = ((int64_t)b * sp + i0 + r) * lp + j0 + (tid & 63);
-        xhi[at] = hi;
-        xlo[at] = lo;
+    x += b * sp * (int64_t)lp * PLANES;
+    for (int r = tid >> 3; r < 64; r += 32) {   // 8 values a thread
+        const int c = (tid & 7) * 8;
+        f16x8 hi, lo;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h16 h, w;
+            split(tile[r][c + i] * inv, h, w);
+            hi[i] = h;
+            lo[i] = w;
+        }
+        h16* at = x + place<PLANES>(i0 + r, lp, j0 + c);
+        *reinterpret_cast<f16x8*>(at) = hi;
+        *reinterpret_cast<f16x8*>(at + low) = lo;
     }
 }
+
+// Workgroup b's place in the order of `count` equal tiles: consecutive
+// workgroups go to the 8 dies in turn; this gives each die one run, so that
+// its L2 holds few matrices (a whole one, of a batch of 8). The grid is
+// die_grid(count); places at or past `count` are none.
+__device__ __forceinline__ int64_t die_place(int64_t count) {
+    return (int64_t)(blockIdx.x & 7) * ((count + 7) / 8) + (blockIdx.x >> 3);
+}
+__host__ __forceinline__ unsigned die_grid(int64_t count) { return (unsigned)((count + 7) / 8 * 8); }
 
 // Tile (ti, tj), ti >= tj, of the lower triangle.
 __device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
@@ -310,45 +334,63 @@ __device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
     tj = id - ti * (ti + 1) / 2;
 }
 
+template <class Tile, int PLANES>
+__device__ __forceinline__ void run_tile(Tile& t, char* lds, const h16* p, int64_t ldp, int rows_n, const h16* q, int64_t ldq,
+                                         int rows_m, int K, int tid) {
+    if constexpr (PLANES == 2) t.run(lds, {p, ldp, rows_n}, {q, ldq, rows_m}, K, tid);
+    else t.template run<true>(lds, {p, ldp, rows_n}, {q, ldq, rows_m}, K, tid);
+}
+
 // Off-diagonal pairs and the diagonal of a symmetric matrix, from the tiles
-// of its lower triangle: POLY = false: A = X X^T; true: B = b A + c A A.
+// of its lower triangle: POLY = false: A = X X^T; true: B = b A + c A A. The
+// upper triangle is written from the same tiles, transposed in LDS by each
+// wave for itself.
 template <class Tile, int PLANES, bool POLY>
-__global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16* __restrict__ hi, const h16* __restrict__ lo,
-                                                                     int sp, int K, const float* __restrict__ lift,
-                                                                     const float* __restrict__ diag,
-                                                                     h16* __restrict__ out_hi, h16* __restrict__ out_lo,
-                                                                     float* __restrict__ out_diag, int tiles) {
+__global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16* __restrict__ in, int sp, int K,
+                                                                      const float* __restrict__ lift,
+                                                                      const float* __restrict__ diag, h16* __restrict__ out,
+                                                                      float* __restrict__ out_diag, int tiles, int64_t count) {
     constexpr int BT = Tile::BN;
-    __shared__ alignas(16) char lds[Tile::kLdsBytes];
+    // a wave's transposed pair of blocks: 32 rows n of MT 16 columns m
+    constexpr int kTurnRow = Tile::MT * 16 + 8, kTurn = 32 * kTurnRow * PLANES;
+    constexpr int kTurnBytes = kTurn * 2 * (Tile::THREADS / 64);
+    __shared__ alignas(16) char lds[Tile::kLdsBytes > kTurnBytes ? Tile::kLdsBytes : kTurnBytes];
     int ti, tj;
-    const int64_t b = blockIdx.x / tiles;
-    triangle_tile((int)(blockIdx.x % tiles), ti, tj);
-    const int tid = threadIdx.x, m0 = ti * BT, n0 = tj * BT;
-    const int64_t at = b * (int64_t)sp * K, out_at = b * (int64_t)sp * sp;
-    Tile t;
-    t.template run<true>(lds, {hi + at + (int64_t)n0 * K, lo + at + (int64_t)n0 * K, K, sp - n0},
-                         {hi + at + (int64_t)m0 * K, lo + at + (int64_t)m0 * K, K, sp - m0}, K, tid);
-    out_hi += out_at;
-    out_lo += out_at;
+    const int64_t id = die_place(count);
+    if (id >= count) return;
+    const int64_t b = id / tiles;
+    triangle_tile((int)(id % tiles), ti, tj);
+    const int tid = threadIdx.x, lane = tid & 63, m0 = ti * BT, n0 = tj * BT;
+    in += b * (int64_t)sp * K * PLANES;
+    out += b * (int64_t)sp * sp * PLANES;
     out_diag += b * sp;
     float back = 1.0f;   // undoes the lift of both factors of X X^T
     if constexpr (POLY) diag += b * sp;
     else back = 1.0f / (lift[b] * lift[b]);
+    Tile t;
+    run_tile<Tile, PLANES>(t, lds, in + (int64_t)n0 * K * PLANES, (int64_t)K * PLANES, sp - n0,
+                           in + (int64_t)m0 * K * PLANES, (int64_t)K * PLANES, sp - m0, K, tid);
+    h16* turn = reinterpret_cast<h16*>(lds) + (tid >> 6) * kTurn;
 #pragma unroll
     for (int a = 0; a < Tile::NT; a += 2) {
         const int n = n0 + Tile::n_of(tid, a);
-        if (n >= sp) continue;
 #pragma unroll
         for (int c = 0; c < Tile::MT; ++c) {
             const int m = m0 + Tile::m_of(tid, c);
-            if (m >= sp) continue;
-            f16x8 vhi, vlo, ohi, olo;
+            const bool inside = n < sp && m < sp;
+            f16x8 ohi, olo;
             float dm = 0.0f;
+            f32x4 dn[2];
             if constexpr (POLY) {
-                ohi = *reinterpret_cast<const f16x8*>(hi + at + (int64_t)m * K + n);
-                if constexpr (PLANES == 2) olo = *reinterpret_cast<const f16x8*>(lo + at + (int64_t)m * K + n);
-                dm = diag[m];
+                const int ms = m < sp ? m : sp - 1, ns = n < sp ? n : sp - 8;   // outside: any value, not stored
+                const h16* at = in + place<PLANES>(ms, sp, ns);
+                ohi = *reinterpret_cast<const f16x8*>(at);
+                if constexpr (PLANES == 2) olo = *reinterpret_cast<const f16x8*>(at + 32);
+                dm = diag[ms];
+                dn[0] = *reinterpret_cast<const f32x4*>(diag + ns);
+                dn[1] = *reinterpret_cast<const f32x4*>(diag + ns + 4);
             }
+            f16x8 vhi, vlo;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float v = t.acc[a + (i >> 2)][c][i & 3];
@@ -356,51 +398,79 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
                 if constexpr (POLY) {
                     float o = (float)ohi[i];
                     if constexpr (PLANES == 2) o += (float)olo[i];
-                    const float dn = diag[n + i];
                     // v = kScaleO^2 (O O)_mn, o = kScaleO O_mn
-                    off = (kC * kScaleB / (kScaleO * kScaleO)) * v + (kScaleB / kScaleO) * (kB + kC * (dm + dn)) * o;
-                    if (m == n + i) out_diag[m] = kC * (v * (1.0f / (kScaleO * kScaleO)) + dm * dm) + kB * dm;
+                    off = (kC * kScaleB / (kScaleO * kScaleO)) * v +
+                          (kScaleB / kScaleO) * (kB + kC * (dm + dn[i >> 2][i & 3])) * o;
+                    if (m == n + i && inside) out_diag[m] = kC * (v * (1.0f / (kScaleO * kScaleO)) + dm * dm) + kB * dm;
                 } else {
                     off = v * (kScaleO / (kScaleX * kScaleX)) * back;
-                    if (m == n + i) out_diag[m] = v * (1.0f / (kScaleX * kScaleX)) * back;
+                    if (m == n + i && inside) out_diag[m] = v * (1.0f / (kScaleX * kScaleX)) * back;
                 }
                 h16 h, l;
                 split(m == n + i ? 0.0f : off, h, l);
                 vhi[i] = h;
                 vlo[i] = l;
                 if (ti != tj) {
-                    out_hi[(int64_t)(n + i) * sp + m] = h;
-                    if constexpr (PLANES == 2) out_lo[(int64_t)(n + i) * sp + m] = l;
+                    h16* to = turn + (8 * (lane >> 4) + i) * kTurnRow + c * 16 + (lane & 15);
+                    to[0] = h;
+                    if constexpr (PLANES == 2) to[32 * kTurnRow] = l;
                 }
             }
-            *reinterpret_cast<f16x8*>(out_hi + (int64_t)m * sp + n) = vhi;
-            if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(out_lo + (int64_t)m * sp + n) = vlo;
+            if (inside) {
+                h16* to = out + place<PLANES>(m, sp, n);
+                *reinterpret_cast<f16x8*>(to) = vhi;
+                if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(to + 32) = vlo;
+            }
+        }
+        if (ti != tj) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own writes
+            constexpr int kRowChunks = Tile::MT * 2;
+            const int row0 = n0 + Tile::n_of(tid & ~63, a), col0 = m0 + Tile::m_of(tid & ~63, 0);
+#pragma unroll
+            for (int k = 0; k < 32 * kRowChunks; k += 64) {
+                const int row = (k + lane) / kRowChunks, chunk = (k + lane) % kRowChunks;
+                const int rn = row0 + row, cm = col0 + chunk * 8;
+                const h16* from = turn + row * kTurnRow + chunk * 8;
+                const f16x8 hi = *reinterpret_cast<const f16x8*>(from);
+                f16x8 lo;
+                if constexpr (PLANES == 2) lo = *reinterpret_cast<const f16x8*>(from + 32 * kTurnRow);
+                if (rn < sp && cm < sp) {
+                    h16* to = out + place<PLANES>(rn, sp, cm);
+                    *reinterpret_cast<f16x8*>(to) = hi;
+                    if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(to + 32) = lo;
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
     }
 }
 
 // X <- (a + B_ii) X_i + (off-diagonal B) X. LAST: the result goes to `out` in
 // its own type and orientation ([m, n], transposed if `turned`) instead.
-template <class T, class Tile, bool LAST>
+template <class T, class Tile, int PLANES, bool LAST>
 __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
-    const h16* __restrict__ bhi, const h16* __restrict__ blo, const float* __restrict__ bdiag, const h16* __restrict__ xhi,
-    const h16* __restrict__ xlo, int sp, int lp, h16* __restrict__ yhi, h16* __restrict__ ylo, int tiles_n, int tiles,
-    const float* __restrict__ lift, T* __restrict__ out, int s, int l, bool turned, bool wide) {
+    const h16* __restrict__ poly, const float* __restrict__ bdiag, const h16* __restrict__ x, int64_t low, int sp, int lp,
+    h16* __restrict__ y, int tiles_n, int tiles, int64_t count, const float* __restrict__ lift, T* __restrict__ out, int s, int l,
+    bool turned, bool wide) {
     constexpr int BN = Tile::BN, BM = Tile::BM;
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
-    const int64_t b = blockIdx.x / tiles;
-    const int tile = (int)(blockIdx.x % tiles);
+    const int64_t id = die_place(count);
+    if (id >= count) return;
+    const int64_t b = id / tiles;
+    const int tile = (int)(id % tiles);
     const int m0 = tile / tiles_n * BM, n0 = tile % tiles_n * BN;
     const int tid = threadIdx.x;
-    const int64_t xat = b * (int64_t)sp * lp, bat = b * (int64_t)sp * sp + (int64_t)m0 * sp;
-    Tile t;
-    t.template run<true>(lds, {xhi + xat + n0, xlo + xat + n0, lp, lp - n0}, {bhi + bat, blo + bat, sp, sp - m0}, sp, tid);
+    poly += (b * sp + m0) * (int64_t)sp * PLANES;
+    x += b * sp * (int64_t)lp * PLANES;
+    y += b * sp * (int64_t)lp * PLANES;
     bdiag += b * sp;
     float back = 1.0f;
     if constexpr (LAST) {
         back = 1.0f / (kScaleX * lift[b]);
         out += b * (int64_t)s * l;
     }
+    Tile t;
+    run_tile<Tile, PLANES>(t, lds, x + n0 * PLANES, (int64_t)lp * PLANES, lp - n0, poly, (int64_t)sp * PLANES, sp - m0, sp, tid);
 #pragma unroll
     for (int a = 0; a < Tile::NT; a += 2) {
         const int n = n0 + Tile::n_of(tid, a);
@@ -409,8 +479,8 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
         for (int c = 0; c < Tile::MT; ++c) {
             const int m = m0 + Tile::m_of(tid, c);
             if (m >= sp) continue;
-            const int64_t at = xat + (int64_t)m * lp + n;
-            const f16x8 ohi = *reinterpret_cast<const f16x8*>(xhi + at), olo = *reinterpret_cast<const f16x8*>(xlo + at);
+            const int64_t at = place<PLANES>(m, lp, n);
+            const f16x8 ohi = *reinterpret_cast<const f16x8*>(x + at), olo = *reinterpret_cast<const f16x8*>(x + at + low);
             const float scale = kA + bdiag[m];
             float v[8];
 #pragma unroll
@@ -425,8 +495,8 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
                     vhi[i] = h;
                     vlo[i] = w;
                 }
-                *reinterpret_cast<f16x8*>(yhi + at) = vhi;
-                *reinterpret_cast<f16x8*>(ylo + at) = vlo;
+                *reinterpret_cast<f16x8*>(y + at) = vhi;
+                *reinterpret_cast<f16x8*>(y + at + low) = vlo;
             } else if (m < s) {
                 if (!turned && wide) {   // rows of whole 16 bytes
                     if (n < l) {
@@ -449,6 +519,10 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
     }
 }
 
+// The tiles of X that make larger tiles worth while: about one for each of the
+// 256 compute units of the larger kind, half as many of the middle one.
+constexpr int64_t kBig = 224, kMid = 128;
+
 template <class Kernel>
 hipError_t allow_lds(Kernel kernel, int bytes) {
     return bytes <= 65536 ? hipSuccess
@@ -456,66 +530,71 @@ hipError_t allow_lds(Kernel kernel, int bytes) {
                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <class Tile, int PLANES, bool POLY>
-hipError_t launch_square(int64_t B, const h16* hi, const h16* lo, int sp, int K, const float* lift, const float* diag, h16* out_hi, h16* out_lo,
-                         float* out_diag, hipStream_t stream) {
-    const int t = (sp + Tile::BN - 1) / Tile::BN, tiles = t * (t + 1) / 2;
-    orthogonalize_square<Tile, PLANES, POLY><<<(unsigned)(B * tiles), Tile::THREADS, 0, stream>>>(
-        hi, lo, sp, K, lift, diag, out_hi, out_lo, out_diag, tiles);
-    return hipGetLastError();
-}
-
-// Tiles of BT x BT by WN x WM waves, staged in rings of SP and SQ.
-template <class T, int BT, int WN, int WM, int SP, int SQ, int PLANES>
-hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w) {
+template <class T, class Square, class Update, int PLANES>
+hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w, int64_t low) {
     auto half = [&](int64_t o) { return reinterpret_cast<h16*>(a.workspace + o); };
     auto real = [&](int64_t o) { return reinterpret_cast<float*>(a.workspace + o); };
-    using Square = TileProduct<h16, BT, BT, WN, WM, true, true, SP, SQ, PLANES>;
-    using Update = TileProduct<h16, BT, BT, WN, WM, false, true, SP, SQ, PLANES>;
-    hipError_t err = hipSuccess;
-    int cur = 0;
+    const int side = (w.sp + Square::BN - 1) / Square::BN, triangle = side * (side + 1) / 2;
+    const int tiles_n = (w.lp + Update::BN - 1) / Update::BN, tiles = tiles_n * ((w.sp + Update::BM - 1) / Update::BM);
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.n % (16 / (int)sizeof(T)) == 0;
-    const int tiles_n = (w.lp + BT - 1) / BT, tiles = tiles_n * ((w.sp + BT - 1) / BT);
-    for (int k = 0; k < a.steps && err == hipSuccess; ++k) {
-        err = launch_square<Square, PLANES, false>(a.B, half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, real(w.lift), nullptr,
-                                                       half(w.ohi), half(w.olo), real(w.diag), a.stream);
-        if (err != hipSuccess) break;
-        err = launch_square<Square, PLANES, true>(a.B, half(w.ohi), half(w.olo), w.sp, w.sp, nullptr, real(w.diag), half(w.bhi),
-                                                      half(w.blo), real(w.bdiag), a.stream);
-        if (err != hipSuccess) break;
-        auto update = [&](auto kernel) {
-            kernel<<<(unsigned)(a.B * tiles), Update::THREADS, 0, a.stream>>>(
-                half(w.bhi), half(w.blo), real(w.bdiag), half(w.xhi[cur]), half(w.xlo[cur]), w.sp, w.lp, half(w.xhi[cur ^ 1]),
-                half(w.xlo[cur ^ 1]), tiles_n, tiles, real(w.lift), static_cast<T*>(a.out), w.s, w.l, a.m > a.n, wide);
-        };
-        if (k + 1 < a.steps) update(orthogonalize_update<T, Update, false>);
-        else update(orthogonalize_update<T, Update, true>);
+    int cur = 0;
+    for (int k = 0; k < a.steps; ++k) {
+        orthogonalize_square<Square, PLANES, false><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
+            half(w.x[cur]), w.sp, w.lp, real(w.lift), nullptr, half(w.o), real(w.diag), triangle, a.B * triangle);
+        hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        orthogonalize_square<Square, PLANES, true><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
+            half(w.o), w.sp, w.sp, nullptr, real(w.diag), half(w.b), real(w.bdiag), triangle, a.B * triangle);
         err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        auto update = [&](auto kernel) {
+            kernel<<<die_grid(a.B * tiles), Update::THREADS, 0, a.stream>>>(
+                half(w.b), real(w.bdiag), half(w.x[cur]), low, w.sp, w.lp, half(w.x[cur ^ 1]), tiles_n, tiles, a.B * tiles,
+                real(w.lift),
+                static_cast<T*>(a.out), w.s, w.l, a.m > a.n, wide);
+        };
+        if (k + 1 < a.steps) update(orthogonalize_update<T, Update, PLANES, false>);
+        else update(orthogonalize_update<T, Update, PLANES, true>);
+        err = hipGetLastError();
+        if (err != hipSuccess) return err;
         cur ^= 1;
     }
-    return err;
+    return hipSuccess;
 }
 
 template <class T, int PLANES>
 hipError_t launch_tiled(const OrthogonalizeArgs& a) {
     const Layout w = layout(a.B, a.m, a.n, PLANES == 2);
     const T* u = static_cast<const T*>(a.update);
-    h16* x0 = reinterpret_cast<h16*>(a.workspace + w.xhi[0]);
-    h16* x1 = reinterpret_cast<h16*>(a.workspace + w.xlo[0]);
     double* norm = reinterpret_cast<double*>(a.workspace + w.norm);
-    float* lift = reinterpret_cast<float*>(a.workspace + w.lift);
     const unsigned tiles64 = (unsigned)(a.B * (w.sp / 64) * (w.lp / 64));
-    const int64_t size = (int64_t)a.m * a.n;
+    const int64_t size = (int64_t)a.m * a.n, low = PLANES == 2 ? 32 : a.B * w.sp * w.lp;
     orthogonalize_norm<T><<<(unsigned)(a.B * kNormBlocks), 256, 0, a.stream>>>(
         u, size, (reinterpret_cast<uintptr_t>(u) & 15) == 0 && size * sizeof(T) % 16 == 0, norm);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    orthogonalize_begin<T><<<tiles64, 256, 0, a.stream>>>(u, a.m, a.n, a.eps, a.steps, norm, w.sp, w.lp, x0, x1, lift);
+    orthogonalize_begin<T, PLANES><<<tiles64, 256, 0, a.stream>>>(
+        u, a.m, a.n, a.eps, a.steps, norm, w.sp, w.lp, reinterpret_cast<h16*>(a.workspace + w.x[0]), low,
+        reinterpret_cast<float*>(a.workspace + w.lift));
     err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const int64_t t128 = (w.sp + 127) / 128;
-    if (a.B * t128 * (t128 + 1) / 2 >= 128) return launch_steps<T, 128, 4, 4, 2, 2, PLANES>(a, w);
-    return launch_steps<T, 64, 2, 2, 4, 4, PLANES>(a, w);
+    const auto count = [&](int t) { return a.B * ((w.sp + t - 1) / t) * ((w.lp + t - 1) / t); };   // tiles of X
+    if constexpr (PLANES == 2) {
+        if (count(256) >= kBig)
+            return launch_steps<T, PairProduct<128, 128, 2, 4, true, 2>, PairProduct<256, 256, 4, 2, false, 2>, 2>(a, w, low);
+        if (count(128) >= kMid)
+            return launch_steps<T, PairProduct<128, 128, 2, 4, true, 2>, PairProduct<128, 128, 2, 4, false, 2>, 2>(a, w, low);
+        return launch_steps<T, PairProduct<64, 64, 2, 2, true, 8>, PairProduct<64, 64, 2, 2, false, 8>, 2>(a, w, low);
+    } else {
+        if (count(256) >= kBig)
+            return launch_steps<T, TileProduct<h16, 256, 256, 4, 2, true, true, 2, 2>,
+                                TileProduct<h16, 256, 256, 4, 2, false, true, 2, 2>, 1>(a, w, low);
+        if (count(128) >= kMid)
+            return launch_steps<T, TileProduct<h16, 128, 128, 4, 4, true, true, 2, 2>,
+                                TileProduct<h16, 128, 128, 4, 4, false, true, 2, 2>, 1>(a, w, low);
+        return launch_steps<T, TileProduct<h16, 64, 64, 2, 2, true, true, 4, 4>,
+                            TileProduct<h16, 64, 64, 2, 2, false, true, 4, 4>, 1>(a, w, low);
+    }
 }
 
 template <class T>
@@ -534,7 +613,8 @@ size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n, dmr_dtype dtype)
     if (is_small(m, n)) return B <= INT32_MAX ? 256 : 0;
     const Layout one = layout(1, m, n, true);
     // one workgroup for every 64 x 64 tile, 31 bits of them; plane sizes in 63 bits
-    const int64_t tiles = (one.xs / 4096 > kNormBlocks ? one.xs / 4096 : kNormBlocks);
+    const int64_t xs = (int64_t)one.sp * one.lp;
+    const int64_t tiles = (xs / 4096 > kNormBlocks ? xs / 4096 : kNormBlocks);
     if (tiles > INT32_MAX || B > INT32_MAX / tiles) return 0;
     return layout(B, m, n, dtype != DMR_BFLOAT16).bytes;
 }
