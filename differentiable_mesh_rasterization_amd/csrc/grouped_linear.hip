@@ -13,7 +13,10 @@
 namespace dmr {
 namespace {
 
-constexpr int kRun = 32;   // consecutive tiles that a die is given at a time
+// Consecutive tiles that a die is given at a time: what its 32 compute units
+// work on together; of the weight gradient's tiles, whose lengths differ,
+// fewer, so that the dies end together.
+constexpr int kRun = 32, kPieceRun = 8;
 
 // A run of rows of one group.
 struct RowTile {
@@ -215,10 +218,11 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restric
 // ---------------------------------------------------------------------------
 // gradient of the weights: a product over each group's rows
 // ---------------------------------------------------------------------------
-// A group's rows are cut into pieces of `per` rows. A group of one piece (or
-// none) is written directly; the pieces of longer groups go to the workspace
-// in float32, each to a slot of its own, and are added in order afterwards:
-// no atomics, so the result does not depend on timing.
+// A group of more than `per` rows is cut into equal pieces of at most that
+// many. A group of one piece (or none) is written directly; the pieces of
+// longer groups go to the workspace in float32, each to a slot of its own, and
+// are added in order afterwards: no atomics, so the result does not depend on
+// timing.
 
 struct Piece {
     int64_t group, first;   // group < 0: no such piece
@@ -226,33 +230,52 @@ struct Piece {
     int64_t slot;           // < 0: the group's only piece
 };
 
-__device__ __forceinline__ int64_t pieces_of(int64_t rows, int per) { return rows > per ? (rows + per - 1) / per : 1; }
+// The pieces of a group of `rows` rows, and their length (the last may be
+// shorter), a multiple of 64 rows.
+__device__ __forceinline__ int pieces_of(int64_t rows, int per, int& length) {
+    const int64_t n = rows > per ? (rows + per - 1) / per : 1;
+    length = (int)((rows + n * 64 - 1) / (n * 64) * 64);
+    return rows > per ? (int)((rows + length - 1) / length) : 1;
+}
 
-__device__ __forceinline__ Piece find_piece(const int64_t* __restrict__ off, int64_t N, int64_t R, int per, int64_t t) {
+// Piece t of all groups'. Every wave does the same work. Up to 64 groups, the
+// pieces are taken longest first, so that what the device finishes with is
+// short: lane g compares its group's piece with every other's.
+__device__ __forceinline__ Piece find_piece(const int64_t* __restrict__ off, int64_t N, int64_t R, int per, int t) {
     const int lane = threadIdx.x & 63;
-    int64_t before = 0, slots_before = 0;
+    int before = 0, slots_before = 0;
     for (int64_t base = 0; base < N; base += 64) {
         int64_t lo, hi;
         group_bounds(off, N, R, base + lane, lo, hi);
-        const int64_t pieces = base + lane < N ? pieces_of(hi - lo, per) : 0;
-        const int64_t slots = pieces > 1 ? pieces : 0;
-        const int64_t upto = before + wave_inclusive_sum(pieces, lane);
-        const int64_t slots_upto = slots_before + wave_inclusive_sum(slots, lane);
-        const uint64_t hit = __ballot(upto > t);
+        int length = 0;
+        const int pieces = base + lane < N ? pieces_of(hi - lo, per, length) : 0;
+        const int slots = pieces > 1 ? pieces : 0;
+        const int slots_upto = slots_before + wave_inclusive_sum(slots, lane);
+        int first_of;   // this group's first piece in the order
+        if (N <= 64) {
+            first_of = 0;
+            for (int g = 0; g < (int)N; ++g) {
+                const int l = __builtin_amdgcn_readlane(length, g), n = __builtin_amdgcn_readlane(pieces, g);
+                if (l > length || (l == length && g < lane)) first_of += n;
+            }
+        } else {
+            first_of = before + wave_inclusive_sum(pieces, lane) - pieces;
+        }
+        const uint64_t hit = __ballot(first_of <= t && t < first_of + pieces);
         if (hit) {
             const int src = __builtin_ctzll(hit);
-            const int64_t k = t - (upto - pieces);
-            const int64_t first = lo + k * per;
+            const int k = t - first_of;
+            const int64_t first = lo + (int64_t)k * length;
             const int64_t left = hi - first;
             Piece r;
             r.group = base + src;
             r.first = uniform64(__shfl(first, src, 64));
-            r.rows = __builtin_amdgcn_readfirstlane(__shfl((int)(left < per ? left : per), src, 64));
-            r.slot = uniform64(__shfl(pieces > 1 ? slots_upto - slots + k : (int64_t)-1, src, 64));
+            r.rows = __builtin_amdgcn_readlane((int)(left < length ? left : length), src);
+            r.slot = __builtin_amdgcn_readlane(pieces > 1 ? slots_upto - slots + k : -1, src);
             return r;
         }
-        before = __shfl(upto, 63, 64);
-        slots_before = __shfl(slots_upto, 63, 64);
+        before = __builtin_amdgcn_readlane(first_of + pieces, 63);
+        slots_before = __builtin_amdgcn_readlane(slots_upto, 63);
     }
     return {-1, 0, 0, -1};
 }
@@ -263,10 +286,10 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
     int64_t N, int per, T* __restrict__ grad_weight, T* __restrict__ grad_bias, bool wide, float* __restrict__ slots,
     int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
-    const int64_t id = tile_of_workgroup<kRun>(blockIdx.x);
+    const int64_t id = tile_of_workgroup<kPieceRun>(blockIdx.x);
     if (id >= items) return;
     const int tiles = n_tiles * m_tiles;
-    const Piece at = find_piece(off, N, R, per, id / tiles);
+    const Piece at = find_piece(off, N, R, per, (int)(id / tiles));
     if (at.group < 0 || at.slot >= slot_count) return;
     const int tile = (int)(id % tiles);
     const int n0 = (tile % n_tiles) * Tile::BN, m0 = (tile / n_tiles) * Tile::BM;
@@ -313,49 +336,76 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
         }
 }
 
-// Adds the pieces of the groups that have more than one, in order, eight
-// loads in flight a lane. A workgroup takes 1024 values of a group.
-constexpr int kAddValues = 1024;
+// Adds the pieces of the groups that have more than one, in a fixed order,
+// eight loads in flight a lane. SPLIT: a workgroup takes 256 values of a group
+// and its four waves a quarter of the pieces each (small weights, whose long
+// groups have many pieces); otherwise it takes 4096 values.
+template <bool SPLIT>
+constexpr int kAddValues = SPLIT ? 256 : 4096;
 
-template <class T>
+template <class T, bool SPLIT>
 __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restrict__ off, int64_t N, int64_t R, int per,
                                                           int64_t values, int64_t width, int64_t weights,
                                                           const float* __restrict__ slots, int64_t slot_count,
                                                           unsigned blocks, T* __restrict__ grad_weight,
                                                           T* __restrict__ grad_bias) {
-    const int lane = threadIdx.x & 63;
+    __shared__ f32x4 part[SPLIT ? 4 : 1][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t group = blockIdx.x / blocks;
-    int64_t slot = 0, mine = 0;
+    int64_t slot = 0;
+    int mine = 0;
     for (int64_t base = 0; base <= group; base += 64) {
         int64_t lo, hi;
         group_bounds(off, N, R, base + lane, lo, hi);
-        const int64_t pieces = base + lane <= group ? pieces_of(hi - lo, per) : 0;
-        const int64_t upto = wave_inclusive_sum(base + lane < group && pieces > 1 ? pieces : 0, lane);
-        slot += __shfl(upto, 63, 64);
-        if (group < base + 64) mine = __shfl(pieces, (int)(group - base), 64);
+        int length;
+        const int pieces = base + lane <= group ? pieces_of(hi - lo, per, length) : 0;
+        const int upto = wave_inclusive_sum(base + lane < group && pieces > 1 ? pieces : 0, lane);
+        slot += __builtin_amdgcn_readlane(upto, 63);
+        if (group < base + 64) mine = __builtin_amdgcn_readlane(pieces, (int)(group - base));
     }
     if (mine <= 1 || slot + mine > slot_count) return;
-    const int64_t i0 = ((int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x) * 4;   // slots are padded to whole vectors
-    if (i0 >= values) return;
-    const float* from = slots + slot * width + i0;
-    f32x4 s = *reinterpret_cast<const f32x4*>(from);
-    int64_t k = 1;
-    for (; k + 8 <= mine; k += 8) {
-        f32x4 v[8];
+    // the sum of pieces first, first + step, ..
+    const auto sum = [&](int64_t i, int first, int step) {
+        const float* from = slots + (slot + first) * width + i;   // slots are padded to whole vectors
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = first; k < mine; k += 8 * step) {
+            f32x4 v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x4*>(from + (k + j) * width);
+            for (int j = 0; j < 8; ++j) {   // past the end: this one again, not added
+                const bool in = k + j * step < mine;
+                v[j] = *reinterpret_cast<const f32x4*>(from + (in ? (int64_t)j * step * width : 0));
+            }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += v[j];
-    }
-    for (; k < mine; ++k) s += *reinterpret_cast<const f32x4*>(from + k * width);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t i = i0 + j;
-        if (i < weights) {
-            if (grad_weight) grad_weight[group * weights + i] = (T)s[j];
-        } else if (i < values && grad_bias) {
-            grad_bias[group * (values - weights) + i - weights] = (T)s[j];
+            for (int j = 0; j < 8; ++j)
+                if (k + j * step < mine) s += v[j];
+            from += (int64_t)8 * step * width;
         }
+        return s;
+    };
+    const auto write = [&](int64_t i0, f32x4 s) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = i0 + j;
+            if (i < weights) {
+                if (grad_weight) grad_weight[group * weights + i] = (T)s[j];
+            } else if (i < values && grad_bias) {
+                grad_bias[group * (values - weights) + i - weights] = (T)s[j];
+            }
+        }
+    };
+    const int64_t begin = (int64_t)(blockIdx.x % blocks) * kAddValues<SPLIT>;
+    if constexpr (SPLIT) {
+        const int64_t i = begin + lane * 4;
+        if (i < values && wave < mine) part[wave][lane] = sum(i, wave, 4);
+        __syncthreads();
+        if (wave > 0 || i >= values) return;
+        f32x4 s = part[0][lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+            if (w < mine) s += part[w][lane];
+        write(i, s);
+    } else {
+        for (int64_t i = begin + tid * 4; i < values && i < begin + kAddValues<SPLIT>; i += 1024) write(i, sum(i, 0, 1));
     }
 }
 
@@ -371,8 +421,9 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int64_t most_row_tiles(int64_t R, int64_t N, int per) { return R / per + (N < R ? N : R); }
 
 // Workgroups for `tiles` tiles; 0 if a launch cannot hold them.
+template <int RUN>
 unsigned run_grid(int64_t tiles) {
-    const int64_t grid = (tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun);
+    const int64_t grid = (tiles + 8 * RUN - 1) / (8 * RUN) * (8 * RUN);
     return grid > INT32_MAX ? 0u : (unsigned)grid;
 }
 
@@ -381,7 +432,7 @@ hipError_t launch_rows_tile(const GroupedLinearArgs& a, const T* in, int k_in, c
                             bool wide) {
     const int n_tiles = ceil_div(n_out, Tile::BN);
     const int64_t tiles = most_row_tiles(a.R, a.N, Tile::BM) * n_tiles;
-    const unsigned places = run_grid(tiles);
+    const unsigned places = run_grid<kRun>(tiles);
     if (places == 0) return hipErrorInvalidValue;
     // as many workgroups as the device holds at a time (a multiple of 8 kRun)
     constexpr unsigned kHeld = 256 * (160 * 1024 / Tile::kLdsBytes);
@@ -416,7 +467,7 @@ template <class T, class Tile>
 hipError_t launch_weight_tile(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide) {
     const int n_tiles = ceil_div(a.cin, Tile::BN), m_tiles = ceil_div(a.cout, Tile::BM);
     const int64_t items = (a.R / p.rows + a.N) * n_tiles * m_tiles;
-    const unsigned grid = run_grid(items);
+    const unsigned grid = run_grid<kPieceRun>(items);
     if (grid == 0) return hipErrorInvalidValue;
     const T *x = static_cast<const T*>(a.x), *g = static_cast<const T*>(a.grad_y);
     T *gw = static_cast<T*>(a.grad_weight), *gb = static_cast<T*>(a.grad_bias);
@@ -463,10 +514,14 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
                       : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, 2, true>>(a, p, vec, wide);
         if (err == hipSuccess && p.slots > 0) {
             const int64_t weights = (int64_t)a.cin * a.cout, values = weights + a.cout;
-            const int64_t blocks = (values + kAddValues - 1) / kAddValues;
-            if (blocks * a.N > INT32_MAX) err = hipErrorInvalidValue;
-            else {
-                grouped_add_pieces<T><<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
+            const bool split = values <= 65536;
+            const int64_t blocks = split ? (values + kAddValues<true> - 1) / kAddValues<true>
+                                         : (values + kAddValues<false> - 1) / kAddValues<false>;
+            if (blocks * a.N > INT32_MAX) {
+                err = hipErrorInvalidValue;
+            } else {
+                const auto add = split ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
+                add<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
                     a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), weights, a.workspace, p.slots,
                     (unsigned)blocks, static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
                 err = hipGetLastError();
@@ -494,9 +549,9 @@ hipError_t launch_typed(const GroupedLinearArgs& a, bool backward) {
 GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half) {
     const int64_t side = cin <= 64 && cout <= 64 ? 64 : !half || cin <= 128 || cout <= 128 || R < 512 * N ? 128 : 256;
     const int64_t tiles = ((cin + side - 1) / side) * ((cout + side - 1) / side);
-    // pieces short enough that the longest is a fraction of a compute unit's
-    // share of the work
-    const int64_t want = (side == 256 ? 512 : 1024) / tiles;
+    // a piece is at most one of the places' shares of the work: 256 compute
+    // units with one workgroup of the largest tiles, two or four of the others
+    const int64_t want = (side == 256 ? 256 : side == 128 ? 512 : 1024) / tiles;
     int64_t rows = want > 0 ? (R + want - 1) / want : R;
     rows = (rows + 127) / 128 * 128;
     rows = rows < 512 ? 512 : rows > 8192 ? 8192 : rows;
