@@ -436,16 +436,32 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
+def _alike(t: torch.Tensor, dtype, device, shape) -> bool:
+    # what _check asks, without its messages (these calls can be short)
+    return t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous()
+
+
 def _grouped_inputs(x, row_offsets, weight):
     dev, dt = x.device, x.dtype
     if x.dim() != 2 or weight.dim() != 3:
         raise ValueError("x must be [R, in_features] and weight [N, out_features, in_features]")
     R, cin = x.shape
     N, cout, _ = weight.shape
-    _check(x, "x", dt, dev)
-    _check(row_offsets, "row_offsets", torch.int64, dev, (N + 1,))
-    _check(weight, "weight", dt, dev, (N, cout, cin))
+    if not (x.is_contiguous() and _alike(weight, dt, dev, (N, cout, cin)) and _alike(row_offsets, torch.int64, dev, (N + 1,))):
+        _check(x, "x", dt, dev)
+        _check(row_offsets, "row_offsets", torch.int64, dev, (N + 1,))
+        _check(weight, "weight", dt, dev, (N, cout, cin))
     return dev, dt, R, cin, N, cout, _dtype(x, "x")
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device: torch.device) -> int:
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def dmr_grouped_linear_fwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor,
@@ -454,10 +470,15 @@ def dmr_grouped_linear_fwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: t
     tensors (include/dmr.h): y [R, out] from x [R, in], row_offsets [N + 1]
     int64, weight [N, out, in] and bias [N, out] or None."""
     dev, dt, R, cin, N, cout, code = _grouped_inputs(x, row_offsets, weight)
-    _check(bias, "bias", dt, dev, (N, cout), optional=True)
-    _check(y, "y", dt, dev, (R, cout))
-    rc = lib().dmr_grouped_linear_fwd(_ptr(x), R, cin, _ptr(row_offsets), N, _ptr(weight), _ptr(bias), cout, code,
-                                      _ptr(y), _stream_handle(dev))
+    if not (_alike(y, dt, dev, (R, cout)) and (bias is None or _alike(bias, dt, dev, (N, cout)))):
+        _check(bias, "bias", dt, dev, (N, cout), optional=True)
+        _check(y, "y", dt, dev, (R, cout))
+    _launch_grouped(x, R, cin, row_offsets, N, weight, bias, cout, code, y, dev)
+
+
+def _launch_grouped(x, R, cin, row_offsets, N, weight, bias, cout, code, y, dev):
+    rc = lib().dmr_grouped_linear_fwd(x.data_ptr(), R, cin, row_offsets.data_ptr(), N, weight.data_ptr(), _address(bias),
+                                      cout, code, y.data_ptr(), _raw_stream(dev))
     if rc != 0:
         raise DmrError("dmr_grouped_linear_fwd", rc)
 
@@ -473,14 +494,21 @@ def dmr_grouped_linear_bwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: t
     gradients may be None. grad_weight and grad_bias need a workspace of
     dmr_grouped_linear_workspace_size() bytes."""
     dev, dt, R, cin, N, cout, code = _grouped_inputs(x, row_offsets, weight)
-    _check(grad_y, "grad_y", dt, dev, (R, cout))
-    _check(grad_x, "grad_x", dt, dev, (R, cin), optional=True)
-    _check(grad_weight, "grad_weight", dt, dev, (N, cout, cin), optional=True)
-    _check(grad_bias, "grad_bias", dt, dev, (N, cout), optional=True)
-    _check(workspace, "workspace", torch.uint8, dev, optional=grad_weight is None and grad_bias is None)
-    rc = lib().dmr_grouped_linear_bwd(_ptr(x), R, cin, _ptr(row_offsets), N, _ptr(weight), cout, code, _ptr(grad_y),
-                                      _ptr(grad_x), _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(), _stream_handle(dev))
+    sums = grad_weight is not None or grad_bias is not None
+    if not (_alike(grad_y, dt, dev, (R, cout)) and (grad_x is None or _alike(grad_x, dt, dev, (R, cin)))
+            and (grad_weight is None or _alike(grad_weight, dt, dev, (N, cout, cin)))
+            and (grad_bias is None or _alike(grad_bias, dt, dev, (N, cout)))
+            and (workspace is not None or not sums)):
+        _check(grad_y, "grad_y", dt, dev, (R, cout))
+        _check(grad_x, "grad_x", dt, dev, (R, cin), optional=True)
+        _check(grad_weight, "grad_weight", dt, dev, (N, cout, cin), optional=True)
+        _check(grad_bias, "grad_bias", dt, dev, (N, cout), optional=True)
+        _check(workspace, "workspace", torch.uint8, dev, optional=not sums)
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, dev)
+    rc = lib().dmr_grouped_linear_bwd(x.data_ptr(), R, cin, row_offsets.data_ptr(), N, weight.data_ptr(), cout, code,
+                                      grad_y.data_ptr(), _address(grad_x), _address(grad_weight), _address(grad_bias),
+                                      _address(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(dev))
     if rc != 0:
         raise DmrError("dmr_grouped_linear_bwd", rc)
 
@@ -500,8 +528,8 @@ def dmr_orthogonalize(update: torch.Tensor, out: torch.Tensor, workspace: torch.
     _check(update, "update", dt, dev)
     _check(out, "out", dt, dev, (B, m, n))
     _check(workspace, "workspace", torch.uint8, dev)
-    rc = lib().dmr_orthogonalize(_ptr(update), B, m, n, _dtype(update, "update"), int(steps), float(eps), _ptr(out),
-                                 _ptr(workspace), workspace.numel(), _stream_handle(dev))
+    rc = lib().dmr_orthogonalize(update.data_ptr(), B, m, n, _dtype(update, "update"), int(steps), float(eps), out.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
     if rc != 0:
         raise DmrError("dmr_orthogonalize", rc)
 
@@ -659,6 +687,7 @@ def rasterize_points(points: torch.Tensor, cloud_offsets: torch.Tensor, image_si
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, row_offsets, weight, bias):
+        _grouped_inputs(x, row_offsets, weight)
         y = torch.empty((x.shape[0], weight.shape[1]), dtype=x.dtype, device=x.device)
         dmr_grouped_linear_fwd(x, row_offsets, weight, bias, y)
         ctx.save_for_backward(x, row_offsets, weight)
@@ -688,8 +717,11 @@ def grouped_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Ten
     bfloat16). Differentiable with respect to x, weight and bias."""
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
         return _GroupedLinear.apply(x, row_offsets, weight, bias)
-    y = torch.empty((x.shape[0], weight.shape[1]), dtype=x.dtype, device=x.device)
-    dmr_grouped_linear_fwd(x, row_offsets, weight, bias, y)
+    dev, dt, R, cin, N, cout, code = _grouped_inputs(x, row_offsets, weight)
+    if bias is not None and not _alike(bias, dt, dev, (N, cout)):
+        _check(bias, "bias", dt, dev, (N, cout))
+    y = torch.empty((R, cout), dtype=dt, device=dev)
+    _launch_grouped(x, R, cin, row_offsets, N, weight, bias, cout, code, y, dev)
     return y
 
 
@@ -699,10 +731,13 @@ def orthogonalize(update: torch.Tensor, steps: int = 5, eps: float = 1e-7) -> to
     products: what an optimiser applies in place of a weight's momentum. Not
     differentiable."""
     u = update.detach()
-    u = u if u.dim() == 3 else u.unsqueeze(0)
-    out = torch.empty_like(u)
+    if u.dim() == 2:
+        u = u.unsqueeze(0)
     if u.dim() != 3:
         raise ValueError("update must be [B, m, n] or [m, n]")
+    _dtype(u, "update")
+    _check(u, "update", u.dtype, u.device)
+    out = torch.empty_like(u)
     ws = torch.empty(dmr_orthogonalize_workspace_size(*u.shape, u.dtype), dtype=torch.uint8, device=u.device)
     dmr_orthogonalize(u, out, ws, steps, eps)
     return out.view(update.shape)

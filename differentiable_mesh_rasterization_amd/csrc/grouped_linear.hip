@@ -453,9 +453,14 @@ hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const 
     if (a.R <= 16 * a.N)
         return launch_rows_tile<T, TileProduct<T, 64, 16, 4, 1, WK, true, 4, 4>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
     if (n_out <= 16)
-        return launch_rows_tile<T, TileProduct<T, 16, 256, 1, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
-    if (n_out <= 64)
+        return launch_rows_tile<T, TileProduct<T, 16, 128, 1, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+    if (n_out <= 64) {
+        if constexpr (sizeof(T) == 2)
+            if (a.R >= 256 * 256)
+                return launch_rows_tile<T, TileProduct<T, 64, 256, 1, 8, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
+                                                                                             wide);
         return launch_rows_tile<T, TileProduct<T, 64, 128, 1, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+    }
     if constexpr (sizeof(T) == 2)
         if (vec && n_out > 128 && a.R >= 512 * a.N)
             return launch_rows_tile<T, TileProduct<T, 256, 256, 4, 2, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
@@ -555,6 +560,7 @@ GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bo
     int64_t rows = want > 0 ? (R + want - 1) / want : R;
     rows = (rows + 127) / 128 * 128;
     rows = rows < 512 ? 512 : rows > 8192 ? 8192 : rows;
+    if (R <= 1024) rows = 1024;   // short enough to need no second launch
     return {(int)rows, (int)side, R > rows ? 2 * (R / rows) : 0};
 }
 

@@ -117,48 +117,66 @@ struct OperandTile {
         return o;
     }
 
-    // Stages k in [k0, k0 + BK) of rows [0, ROWS): zero where the row is not
-    // below `rows` or k not below K. `base` points at row 0 and k = 0.
-    // VEC: base and ld are multiples of 16 bytes, and so is the extent of the
+    // Loads k in [k0, k0 + BK) of rows [0, ROWS) into LDS: zero where the row
+    // is not below `rows` or k not below K. `base` points at row 0 and k = 0;
+    // it and ld are multiples of 16 bytes, and so is the extent of the
     // contiguous direction, so that a chunk is inside or outside as a whole.
-    template <bool VEC>
-    static __device__ __forceinline__ void stage(char* lds, const T* base, int64_t ld, int rows, const Offsets& o, int k0,
-                                                 int K, int tid) {
+    static __device__ __forceinline__ void stage(char* lds, const T* base, int64_t ld, const Offsets& o, int k0, int K,
+                                                 int tid) {
         const T* at = KMAJOR ? base + k0 : base + (int64_t)k0 * ld;
         const int kleft = K - k0;
-        if constexpr (VEC) {
-            const __amdgpu_buffer_rsrc_t rsrc =
-                __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, kBufferRange, 0x00020000);
-            const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-            const bool whole = kleft >= BK;
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, kBufferRange, 0x00020000);
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const bool whole = kleft >= BK;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                if (kChunks % THREADS != 0 && i * THREADS + wave * 64 >= kChunks) break;
-                uint32_t off = o.at[i];
-                if (!whole) {
-                    const int c = i * THREADS + tid, line = c / kLine;
-                    const int k = KMAJOR ? ((c % kLine) ^ swizzle(line)) * kElems : line;
-                    if (k >= kleft) off = kNowhere;
-                }
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (DMR_LDS void*)(lds + (i * THREADS + wave * 64) * 16), 16,
-                                                         off, 0, 0, 0);
+        for (int i = 0; i < kLoads; ++i) {
+            if (kChunks % THREADS != 0 && i * THREADS + wave * 64 >= kChunks) break;
+            uint32_t off = o.at[i];
+            if (!whole) {
+                const int c = i * THREADS + tid, line = c / kLine;
+                const int k = KMAJOR ? ((c % kLine) ^ swizzle(line)) * kElems : line;
+                if (k >= kleft) off = kNowhere;
             }
-        } else {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (DMR_LDS void*)(lds + (i * THREADS + wave * 64) * 16), 16, off, 0, 0,
+                                                     0);
+        }
+    }
+
+    // The same for arrays that are not so aligned, one element a load, by way
+    // of registers: fetch issues the loads, put writes them to LDS.
+    struct Held {
+        u32x4 chunk[kLoads];
+    };
+    static __device__ __forceinline__ void fetch(Held& h, const T* base, int64_t ld, int rows, int k0, int K, int tid) {
+        const T* at = KMAJOR ? base + k0 : base + (int64_t)k0 * ld;
+        const int kleft = K - k0;
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, kBufferRange, 0x00020000);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int c = i * THREADS + tid;
-                if (kChunks % THREADS != 0 && c >= kChunks) break;
-                const int line = c / kLine, chunk = (c % kLine) ^ swizzle(line);
-                const int row = KMAJOR ? line : chunk * kElems, k = KMAJOR ? chunk * kElems : line;
-                const T* from = at + (int64_t)line * ld + chunk * kElems;
-                alignas(16) T v[kElems];
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = i * THREADS + tid;
+            const int line = c / kLine, chunk = (c % kLine) ^ swizzle(line);
+            const int row = KMAJOR ? line : chunk * kElems, k = KMAJOR ? chunk * kElems : line;
+            const uint32_t off = (uint32_t)line * (uint32_t)(ld * sizeof(T)) + (uint32_t)chunk * 16u;
+            alignas(16) T v[kElems];
 #pragma unroll
-                for (int e = 0; e < kElems; ++e) {
-                    const bool in = KMAJOR ? row < rows && k + e < kleft : row + e < rows && k < kleft;
-                    v[e] = in ? from[e] : (T)0.0f;
-                }
-                *reinterpret_cast<u32x4*>(lds + c * 16) = *reinterpret_cast<const u32x4*>(v);
+            for (int e = 0; e < kElems; ++e) {
+                const bool in = c < kChunks && (KMAJOR ? row < rows && k + e < kleft : row + e < rows && k < kleft);
+                const uint32_t o = in ? off + e * (uint32_t)sizeof(T) : kNowhere;
+                if constexpr (sizeof(T) == 2)
+                    v[e] = __builtin_bit_cast(T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0));
+                else
+                    v[e] = __builtin_bit_cast(T, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0));
             }
+            h.chunk[i] = *reinterpret_cast<const u32x4*>(v);
+        }
+    }
+    static __device__ __forceinline__ void put(char* lds, const Held& h, int tid) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = i * THREADS + tid;
+            if (kChunks % THREADS == 0 || c < kChunks) *reinterpret_cast<u32x4*>(lds + c * 16) = h.chunk[i];
         }
     }
 
@@ -239,15 +257,16 @@ struct TileProduct {
         return ((tid >> 6) / WN) * MT * 16 + b * 16 + (tid & 15);
     }
 
-    template <bool VEC>
-    static __device__ __forceinline__ void stage_p(char* lds, const Source& p, const typename P::Offsets& o, int k0, int K,
-                                                   int tid) {
-        P::template stage<VEC>(lds, p.at, p.ld, p.rows, o, k0, K, tid);
-    }
-    template <bool VEC>
-    static __device__ __forceinline__ void stage_q(char* lds, const Source& q, const typename Q::Offsets& o, int k0, int K,
-                                                   int tid) {
-        Q::template stage<VEC>(lds, q.at, q.ld, q.rows, o, k0, K, tid);
+    template <bool VEC, class Operand>
+    static __device__ __forceinline__ void stage(char* lds, const Source& s, const typename Operand::Offsets& o, int k0, int K,
+                                                 int tid) {
+        if constexpr (VEC) {
+            Operand::stage(lds, s.at, s.ld, o, k0, K, tid);
+        } else {
+            typename Operand::Held h;
+            Operand::fetch(h, s.at, s.ld, s.rows, k0, K, tid);
+            Operand::put(lds, h, tid);
+        }
     }
 
     static __device__ __forceinline__ void read(Fragments& f, const char* lds_p, const char* lds_q, int kk, int tid) {
@@ -285,11 +304,11 @@ struct TileProduct {
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
 #pragma unroll
         for (int t = 0; t < kAhead; ++t)
-            if (t < steps) stage_p<VEC>(lds + t * kP, p, po, t * BK, K, tid);
+            if (t < steps) stage<VEC, P>(lds + t * kP, p, po, t * BK, K, tid);
 #pragma unroll
         for (int t = 0; t < SQ; ++t) {
-            if (t < steps) stage_q<VEC>(lds + SP * kP + t * kQ, q, qo, t * BK, K, tid);
-            if (t + kAhead < steps) stage_p<VEC>(lds + (t + kAhead) * kP, p, po, (t + kAhead) * BK, K, tid);
+            if (t < steps) stage<VEC, Q>(lds + SP * kP + t * kQ, q, qo, t * BK, K, tid);
+            if (t + kAhead < steps) stage<VEC, P>(lds + (t + kAhead) * kP, p, po, (t + kAhead) * BK, K, tid);
         }
     }
 
@@ -323,12 +342,24 @@ struct TileProduct {
             // step t is read, and the loads of step t + 1 have arrived
             if (SQ > 1 && t - 1 + SP < steps) step_barrier<kBehind + (SQ > 1 ? SQ - 2 : 0) * (kPLoads + kQLoads)>();
             else step_barrier<0>();
-            if (t + SQ < steps) stage_q<VEC>(lds_q + at_q, q, qo, (t + SQ) * BK, K, tid);
-            if (t + SP < steps) stage_p<VEC>(lds_p + at_p, p, po, (t + SP) * BK, K, tid);
+            typename P::Held held_p;
+            typename Q::Held held_q;
+            char *const free_p = lds_p + at_p, *const free_q = lds_q + at_q;
+            if constexpr (VEC) {
+                if (t + SQ < steps) Q::stage(free_q, q.at, q.ld, qo, (t + SQ) * BK, K, tid);
+                if (t + SP < steps) P::stage(free_p, p.at, p.ld, po, (t + SP) * BK, K, tid);
+            } else {
+                if (t + SQ < steps) Q::fetch(held_q, q.at, q.ld, q.rows, (t + SQ) * BK, K, tid);
+                if (t + SP < steps) P::fetch(held_p, p.at, p.ld, p.rows, (t + SP) * BK, K, tid);
+            }
             at_p = at_p + kP == SP * kP ? 0 : at_p + kP;
             at_q = at_q + kQ == SQ * kQ ? 0 : at_q + kQ;
             if (SQ > 1) read(first, lds_p + at_p, lds_q + at_q, 0, tid);   // past the end: not used
             multiply(second, sums);
+            if constexpr (!VEC) {
+                if (t + SQ < steps) Q::put(free_q, held_q, tid);
+                if (t + SP < steps) P::put(free_p, held_p, tid);
+            }
         }
         step_barrier<0>();
     }
@@ -388,8 +419,8 @@ struct PairProduct {
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
         constexpr int kLoads = P::kLoadsLeast + Q::kLoadsLeast;
         const auto stage = [&](char* to, int t) {
-            P::template stage<true>(to, p.at, p.ld, rows_p, po, t * P::BK, steps * P::BK, tid);
-            Q::template stage<true>(to + P::kBytes, q.at, q.ld, q.rows, qo, t * Q::BK, steps * Q::BK, tid);
+            P::stage(to, p.at, p.ld, po, t * P::BK, steps * P::BK, tid);
+            Q::stage(to + P::kBytes, q.at, q.ld, qo, t * Q::BK, steps * Q::BK, tid);
         };
 #pragma unroll
         for (int t = 0; t < S - 1; ++t)
