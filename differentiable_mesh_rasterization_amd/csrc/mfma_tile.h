@@ -73,11 +73,12 @@ __device__ __forceinline__ f32x4 mma<float>(u32x4 p, u32x4 q, f32x4 c) {
 }
 
 // One operand's staged step: ROWS rows of KB bytes of k (K-major: 128).
+// SPREAD: M-major fragments of 16-bit rows are paired.
 //
 // LDS holds it in 16-byte chunks in the order memory has it (the loads write
 // LDS linearly, lane after lane), with the chunks of a line exchanged by a
 // swizzle so that the 16 lanes of a fragment read hit different banks.
-template <class T, int ROWS, bool KMAJOR, int THREADS, int KB = kStepBytes>
+template <class T, int ROWS, bool KMAJOR, int THREADS, int KB = kStepBytes, bool SPREAD = false>
 struct OperandTile {
     static constexpr int kElems = 16 / (int)sizeof(T);   // elements of a chunk
     static constexpr int BK = KB / (int)sizeof(T);
@@ -94,7 +95,10 @@ struct OperandTile {
             // 16 different 16-byte slots of 256
             return ((line >> 1) & 1) | (((line >> 2) ^ (line >> 4)) & 1) << 1 | ((line >> 3) & 1) << 2;
         } else if constexpr (sizeof(T) == 2) {
-            return kLine >= 16 ? (line & 3) << 2 : kLine == 8 ? (line & 2) << 1 : 0;
+            // paired: the lanes of one k use halves of 4 chunks; not paired: 2
+            // whole chunks, and the next 8 of k other ones
+            if constexpr (SPREAD) return kLine >= 16 ? (line & 3) << 2 : kLine == 8 ? (line & 2) << 1 : 0;
+            else return kLine >= 16 ? ((line & 3) << 1) | (((line >> 3) & 1) << 3) : kLine == 8 ? (line & 2) | ((line >> 3) & 1) << 2 : 0;
         } else {
             return kLine >= 16 ? ((line >> 2) & 3) << 2 : 0;
         }
@@ -211,6 +215,22 @@ struct OperandTile {
     }
 };
 
+// Two M-major fragments of 16-bit rows that are paired (rows first + 8 a + i,
+// and 4 further): the lanes of one k read halves of chunks, so lanes of odd q
+// read the other fragment's half first, and together they use whole chunks and
+// all banks.
+template <class Tile>
+__device__ __forceinline__ void paired_fragments(const char* lds, int kk, int first, int lane, u32x4& even, u32x4& odd) {
+    const int q = lane >> 4;
+    const u32x4 a = Tile::fragment(lds, kk, first + 4 * (q & 1), 8, lane);
+    const u32x4 b = Tile::fragment(lds, kk, first + 4 - 4 * (q & 1), 8, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        even[j] = q & 1 ? b[j] : a[j];
+        odd[j] = q & 1 ? a[j] : b[j];
+    }
+}
+
 // Waits until at most N of this wave's loads into LDS are outstanding and all
 // its reads from LDS are done, then for the other waves. (A barrier alone
 // waits for neither.)
@@ -230,7 +250,7 @@ struct TileProduct {
     static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
     static constexpr int BK = kStepBytes / (int)sizeof(T);
     static constexpr bool PAIRED = sizeof(T) == 2 && NT % 2 == 0;
-    using P = OperandTile<T, BN, PK, THREADS>;
+    using P = OperandTile<T, BN, PK, THREADS, kStepBytes, PAIRED>;
     using Q = OperandTile<T, BM, QK, THREADS>;
     static constexpr int kP = P::kBytes, kQ = Q::kBytes;   // bytes of a stage
     static constexpr int kLdsBytes = SP * kP + SQ * kQ;
@@ -273,7 +293,9 @@ struct TileProduct {
         const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
 #pragma unroll
         for (int a = 0; a < NT; ++a)
-            f.p[a] = P::fragment(lds_p, kk, wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 4 * (a & 1) : a * 16), PAIRED ? 8 : 4, lane);
+            if constexpr (PAIRED && !PK) {
+                if (a % 2 == 0) paired_fragments<P>(lds_p, kk, wn * NT * 16 + a * 16, lane, f.p[a], f.p[a + 1]);
+            } else f.p[a] = P::fragment(lds_p, kk, wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 4 * (a & 1) : a * 16), PAIRED ? 8 : 4, lane);
 #pragma unroll
         for (int b = 0; b < MT; ++b) f.q[b] = Q::fragment(lds_q, kk, (wm * MT + b) * 16, 4, lane);
     }
@@ -283,13 +305,21 @@ struct TileProduct {
         for (int a = 0; a < NT; ++a)
 #pragma unroll
             for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(f.p[a], f.q[b], acc[a][b]);
-        if constexpr (SUMS)
+        if constexpr (SUMS && sizeof(T) == 4) {
+            // on the vector units, which are free beside float32 products (a
+            // product with ones is half as long again as a 64 x 64 tile's):
+            // each lane its k, added over the lanes in the end
+            if (sums)
+#pragma unroll
+                for (int b = 0; b < MT; ++b) ones[b] += __builtin_bit_cast(f32x4, f.q[b]);
+        } else if constexpr (SUMS) {
             if (sums) {
                 constexpr uint32_t w = one_bits<T>();
                 const u32x4 one = {w, w, w, w};
 #pragma unroll
                 for (int b = 0; b < MT; ++b) ones[b] = mma<T>(one, f.q[b], ones[b]);
             }
+        }
     }
 
     // Loads are issued as P(0) .. P(SP - SQ - 1), then Q(t), P(t + SP - SQ)
@@ -362,6 +392,15 @@ struct TileProduct {
             }
         }
         step_barrier<0>();
+        if constexpr (SUMS && sizeof(T) == 4)
+            if (sums)
+#pragma unroll
+                for (int b = 0; b < MT; ++b) {
+                    float s = (ones[b][0] + ones[b][1]) + (ones[b][2] + ones[b][3]);
+                    s += __shfl_xor(s, 16, 64);
+                    s += __shfl_xor(s, 32, 64);
+                    ones[b][0] = s;
+                }
     }
 
     template <bool VEC>
@@ -386,7 +425,7 @@ struct PairProduct {
     static constexpr bool PAIRED = true;
     static_assert(NT % 2 == 0 && S >= 2, "");
     // M-major, the 2 BN float16 of a line and 32 lines
-    using P = OperandTile<T, PK ? BN : 2 * BN, PK, THREADS, PK ? 128 : 64>;
+    using P = OperandTile<T, PK ? BN : 2 * BN, PK, THREADS, PK ? 128 : 64, true>;
     using Q = OperandTile<T, BM, true, THREADS>;
     static constexpr int kStage = P::kBytes + Q::kBytes, kLdsBytes = S * kStage;
     static_assert(kLdsBytes <= 160 * 1024, "");
