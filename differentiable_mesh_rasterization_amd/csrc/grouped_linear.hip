@@ -162,12 +162,22 @@ __device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, i
         return;
     }
 #pragma unroll
-    for (int a = 0; a < Tile::NT; ++a)
+    for (int a = 0; a < Tile::NT; a += STEP) {
+        const int n = n0 + Tile::n_of(tid, a);
 #pragma unroll
         for (int b = 0; b < Tile::MT; ++b) {
             const int m = Tile::m_of(tid, b);
-            if (m < rows) store4<T>(out + (int64_t)m * ld, n0 + Tile::n_of(tid, a), N, t.acc[a][b] + add[a]);
+            if (m >= rows) continue;
+            T* row = out + (int64_t)m * ld;
+            if (CHUNKS && n + 4 * STEP <= N) {
+                const u32x4 v = packed<T>(t.acc[a][b] + add[a], t.acc[a + STEP - 1][b] + add[a + STEP - 1]);
+                __builtin_memcpy(row + n, &v, 16);   // at whatever alignment it has
+            } else {
+#pragma unroll
+                for (int s = 0; s < STEP; ++s) store4<T>(row, n + 4 * s, N, t.acc[a + s][b] + add[a + s]);
+            }
         }
+    }
 }
 
 // y = x W^T + b (WK: the weight's contiguous direction is summed over) or
@@ -364,21 +374,19 @@ __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restr
         if (group < base + 64) mine = __builtin_amdgcn_readlane(pieces, (int)(group - base));
     }
     if (mine <= 1 || slot + mine > slot_count) return;
-    // the sum of pieces first, first + step, ..
-    const auto sum = [&](int64_t i, int first, int step) {
+    // the sum of pieces first, first + 4, .. at value i
+    const auto sum = [&](int64_t i, int first) {
         const float* from = slots + (slot + first) * width + i;   // slots are padded to whole vectors
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = first; k < mine; k += 8 * step) {
+        for (int k = first; k < mine; k += 32) {
             f32x4 v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {   // past the end: this one again, not added
-                const bool in = k + j * step < mine;
-                v[j] = *reinterpret_cast<const f32x4*>(from + (in ? (int64_t)j * step * width : 0));
-            }
+            for (int j = 0; j < 8; ++j)   // past the end: this one again, not added
+                v[j] = *reinterpret_cast<const f32x4*>(from + (k + 4 * j < mine ? (int64_t)(4 * j) * width : 0));
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (k + j * step < mine) s += v[j];
-            from += (int64_t)8 * step * width;
+                if (k + 4 * j < mine) s += v[j];
+            from += 32 * width;
         }
         return s;
     };
@@ -396,7 +404,7 @@ __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restr
     const int64_t begin = (int64_t)(blockIdx.x % blocks) * kAddValues<SPLIT>;
     if constexpr (SPLIT) {
         const int64_t i = begin + lane * 4;
-        if (i < values && wave < mine) part[wave][lane] = sum(i, wave, 4);
+        if (i < values && wave < mine) part[wave][lane] = sum(i, wave);
         __syncthreads();
         if (wave > 0 || i >= values) return;
         f32x4 s = part[0][lane];
@@ -405,7 +413,32 @@ __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restr
             if (w < mine) s += part[w][lane];
         write(i, s);
     } else {
-        for (int64_t i = begin + tid * 4; i < values && i < begin + kAddValues<SPLIT>; i += 1024) write(i, sum(i, 0, 1));
+        // four vectors a lane, 1024 values apart, all in flight
+        const float* from = slots + slot * width;
+        f32x4 s[4];
+        int64_t at[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = begin + j * 1024 + tid * 4;
+            at[j] = i < values ? i : 0;   // past the end: not written
+            s[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        for (int k = 0; k < mine; k += 2) {
+            f32x4 v[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[u][j] = *reinterpret_cast<const f32x4*>(from + (k + (k + u < mine ? u : 0)) * width + at[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[j] += v[0][j];
+                if (k + 1 < mine) s[j] += v[1][j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (begin + j * 1024 + tid * 4 < values) write(at[j], s[j]);
     }
 }
 
@@ -465,7 +498,7 @@ hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const 
         if (vec && n_out > 128 && a.R >= 512 * a.N)
             return launch_rows_tile<T, TileProduct<T, 256, 256, 4, 2, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
                                                                                            wide);
-    return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 2, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+    return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
 }
 
 template <class T, class Tile>

@@ -147,33 +147,33 @@ struct OperandTile {
         }
     }
 
-    // The same for arrays that are not so aligned, one element a load, by way
-    // of registers: fetch issues the loads, put writes them to LDS.
+    // The same for arrays that are not so aligned, by way of registers: fetch
+    // issues the loads, put writes them to LDS. A chunk that lies inside is
+    // one load at whatever alignment it has; one that crosses the end is read
+    // element by element.
     struct Held {
         u32x4 chunk[kLoads];
     };
     static __device__ __forceinline__ void fetch(Held& h, const T* base, int64_t ld, int rows, int k0, int K, int tid) {
         const T* at = KMAJOR ? base + k0 : base + (int64_t)k0 * ld;
         const int kleft = K - k0;
-        const __amdgpu_buffer_rsrc_t rsrc =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(at), 0, kBufferRange, 0x00020000);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int c = i * THREADS + tid;
             const int line = c / kLine, chunk = (c % kLine) ^ swizzle(line);
-            const int row = KMAJOR ? line : chunk * kElems, k = KMAJOR ? chunk * kElems : line;
-            const uint32_t off = (uint32_t)line * (uint32_t)(ld * sizeof(T)) + (uint32_t)chunk * 16u;
-            alignas(16) T v[kElems];
+            // of the contiguous direction, this chunk's elements that exist
+            const bool is = c < kChunks && line < (KMAJOR ? rows : kleft);
+            const int left = is ? (KMAJOR ? kleft : rows) - chunk * kElems : 0;
+            const T* from = at + (int64_t)line * ld + chunk * kElems;
+            h.chunk[i] = u32x4{0, 0, 0, 0};
+            if (left >= kElems) {
+                __builtin_memcpy(&h.chunk[i], from, 16);
+            } else if (left > 0) {
+                T v[kElems];
 #pragma unroll
-            for (int e = 0; e < kElems; ++e) {
-                const bool in = c < kChunks && (KMAJOR ? row < rows && k + e < kleft : row + e < rows && k < kleft);
-                const uint32_t o = in ? off + e * (uint32_t)sizeof(T) : kNowhere;
-                if constexpr (sizeof(T) == 2)
-                    v[e] = __builtin_bit_cast(T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0));
-                else
-                    v[e] = __builtin_bit_cast(T, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0));
+                for (int e = 0; e < kElems; ++e) v[e] = e < left ? from[e] : (T)0.0f;
+                __builtin_memcpy(&h.chunk[i], v, 16);
             }
-            h.chunk[i] = *reinterpret_cast<const u32x4*>(v);
         }
     }
     static __device__ __forceinline__ void put(char* lds, const Held& h, int tid) {
