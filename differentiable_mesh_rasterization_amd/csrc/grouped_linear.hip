@@ -484,21 +484,21 @@ template <class T, bool WK>
 hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const T* bias, T* out, int n_out, bool vec,
                        bool wide) {
     if (a.R <= 16 * a.N)
-        return launch_rows_tile<T, TileProduct<T, 64, 16, 4, 1, WK, true, 4, 4>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+        return launch_rows_tile<T, TileProduct<T, 64, 16, 4, 1, WK, true, 4>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
     if (n_out <= 16)
-        return launch_rows_tile<T, TileProduct<T, 16, 128, 1, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+        return launch_rows_tile<T, TileProduct<T, 16, 128, 1, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
     if (n_out <= 64) {
         if constexpr (sizeof(T) == 2)
             if (a.R >= 256 * 256)
-                return launch_rows_tile<T, TileProduct<T, 64, 256, 1, 8, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
+                return launch_rows_tile<T, TileProduct<T, 64, 256, 1, 8, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
                                                                                              wide);
-        return launch_rows_tile<T, TileProduct<T, 64, 128, 1, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+        return launch_rows_tile<T, TileProduct<T, 64, 128, 1, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
     }
     if constexpr (sizeof(T) == 2)
         if (vec && n_out > 128 && a.R >= 512 * a.N)
-            return launch_rows_tile<T, TileProduct<T, 256, 256, 4, 2, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
+            return launch_rows_tile<T, TileProduct<T, 256, 256, 4, 2, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
                                                                                            wide);
-    return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 4, WK, true, 2, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
+    return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
 }
 
 template <class T, class Tile>
@@ -543,13 +543,13 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
         bool done = false;
         if constexpr (sizeof(T) == 2)
             if (p.side == 256 && vec) {
-                err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, 2, true>>(a, p, vec, wide);
+                err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, true>>(a, p, vec, wide);
                 done = true;
             }
         if (!done)
             err = p.side == 64
-                      ? launch_weight_tile<T, TileProduct<T, 64, 64, 2, 2, false, false, 2, 2, true>>(a, p, vec, wide)
-                      : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, 2, true>>(a, p, vec, wide);
+                      ? launch_weight_tile<T, TileProduct<T, 64, 64, 2, 2, false, false, 2, true>>(a, p, vec, wide)
+                      : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, true>>(a, p, vec, wide);
         if (err == hipSuccess && p.slots > 0) {
             const int64_t weights = (int64_t)a.cin * a.cout, values = weights + a.cout;
             const bool split = values <= 65536;

@@ -2,13 +2,19 @@
 //
 // A workgroup computes a BM x BN tile of C[m][n] = sum_k Q[m][k] P[n][k] in
 // float32 accumulators. Both operands are staged in LDS 128 bytes of k (whole
-// cache lines of a row) at a time, in rings of SP and SQ stages. A step is two
-// slices
+// cache lines of a row) at a time, in a ring of S stages. A step is two slices
 // of 64 bytes of k: while the matrix cores work on one slice's fragments, the
 // next slice's are read from LDS into a second set of registers. In the middle
 // of a step its last fragments have been read, so its stage is free there:
 // that is where the one barrier of a step stands, and where the loads, which
-// go straight from memory into LDS, are issued SP and SQ steps ahead.
+// go straight from memory into LDS, are issued S steps ahead.
+//
+// What bounds a tile: 256 x 256 16-bit tiles take 64 KB of loads for 2048
+// cycles of the matrix cores, and the LDS holds two steps. On 131072 rows of
+// 2048 to 2048 the products alone take 752 us, the loads alone 849 and both
+// 990 (1.1 PFLOP/s). Steps of 64 bytes (half lines, four stages) are 9%
+// slower, 128 x 128 tiles 35%; a ring of three stages for one operand, loads
+// into L2 ahead, and a fixed order of loads, reads and products change little.
 //
 // P is the first operand of the matrix instruction and n its row index, so
 // that a lane's four accumulators are four consecutive n of one row m of C:
@@ -244,7 +250,7 @@ __device__ __forceinline__ void step_barrier() {
 // The tile product of one workgroup: WN x WM waves, each NT x MT blocks of
 // 16 x 16. Of 16-bit types, neighbouring blocks of n are paired so that a lane
 // holds eight consecutive n. SUMS: sum over k of Q[m][k] as well.
-template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int SP, int SQ, bool SUMS = false>
+template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int S, bool SUMS = false>
 struct TileProduct {
     static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64;
     static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
@@ -252,9 +258,8 @@ struct TileProduct {
     static constexpr bool PAIRED = sizeof(T) == 2 && NT % 2 == 0;
     using P = OperandTile<T, BN, PK, THREADS, kStepBytes, PAIRED>;
     using Q = OperandTile<T, BM, QK, THREADS>;
-    static constexpr int kP = P::kBytes, kQ = Q::kBytes;   // bytes of a stage
-    static constexpr int kLdsBytes = SP * kP + SQ * kQ;
-    static_assert(SP >= SQ && SQ >= 1 && kLdsBytes <= 160 * 1024, "");
+    static constexpr int kStage = P::kBytes + Q::kBytes, kLdsBytes = S * kStage;
+    static_assert(S >= 2 && kLdsBytes <= 160 * 1024, "");
 
     struct Source {   // an operand, at row 0 of the tile and k = 0
         const T* at;
@@ -322,10 +327,6 @@ struct TileProduct {
         }
     }
 
-    // Loads are issued as P(0) .. P(SP - SQ - 1), then Q(t), P(t + SP - SQ)
-    // for t = 0, 1, ..; a wave's loads arrive in that order.
-    static constexpr int kAhead = SP - SQ;
-
     // Issues the loads of the first steps of a product over k in [0, K).
     template <bool VEC>
     static __device__ __forceinline__ void begin(char* lds, const Source& p, const Source& q, int K, int tid) {
@@ -333,17 +334,15 @@ struct TileProduct {
         const typename P::Offsets po = P::offsets(p.ld, p.rows, tid);
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
 #pragma unroll
-        for (int t = 0; t < kAhead; ++t)
-            if (t < steps) stage<VEC, P>(lds + t * kP, p, po, t * BK, K, tid);
-#pragma unroll
-        for (int t = 0; t < SQ; ++t) {
-            if (t < steps) stage<VEC, Q>(lds + SP * kP + t * kQ, q, qo, t * BK, K, tid);
-            if (t + kAhead < steps) stage<VEC, P>(lds + (t + kAhead) * kP, p, po, (t + kAhead) * BK, K, tid);
-        }
+        for (int t = 0; t < S; ++t)
+            if (t < steps) {
+                stage<VEC, P>(lds + t * kStage, p, po, t * BK, K, tid);
+                stage<VEC, Q>(lds + t * kStage + P::kBytes, q, qo, t * BK, K, tid);
+            }
     }
 
     // acc = sum over k in [0, K), begun with the same arguments; the LDS is
-    // free for other use afterwards. SQ = 1: K is at most one step.
+    // free for other use afterwards.
     template <bool VEC>
     __device__ __forceinline__ void finish(char* lds, const Source& p, const Source& q, int K, int tid, bool sums = false) {
 #pragma unroll
@@ -357,39 +356,40 @@ struct TileProduct {
         const int steps = (K + BK - 1) / BK;
         const typename P::Offsets po = P::offsets(p.ld, p.rows, tid);
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
-        char *const lds_p = lds, *const lds_q = lds + SP * kP;
-        // After Q(t): one P if P is ahead, and both of the later steps.
-        constexpr int kPLoads = VEC ? P::kLoadsLeast : 0, kQLoads = VEC ? Q::kLoadsLeast : 0;
-        constexpr int kBehind = kAhead > 0 ? kPLoads : 0;
-        if (SP <= steps) step_barrier<kBehind + (SQ - 1) * (kPLoads + kQLoads)>();   // step 0 is here
+        // a wave's loads of a step; they arrive in the order of their issue
+        constexpr int kLoads = VEC ? P::kLoadsLeast + Q::kLoadsLeast : 0;
+        if (S <= steps) step_barrier<(S - 1) * kLoads>();   // step 0 is here
         else step_barrier<0>();
         Fragments first, second;
-        read(first, lds_p, lds_q, 0, tid);
-        int at_p = 0, at_q = 0;   // this step's stages
+        read(first, lds, lds + P::kBytes, 0, tid);
+        int cur = 0;   // this step's stage
         for (int t = 0; t < steps; ++t) {
-            read(second, lds_p + at_p, lds_q + at_q, 1, tid);
+            char* const here = lds + cur;
+            read(second, here, here + P::kBytes, 1, tid);
             multiply(first, sums);
             // step t is read, and the loads of step t + 1 have arrived
-            if (SQ > 1 && t - 1 + SP < steps) step_barrier<kBehind + (SQ > 1 ? SQ - 2 : 0) * (kPLoads + kQLoads)>();
+            if (t - 1 + S < steps) step_barrier<(S - 2) * kLoads>();
             else step_barrier<0>();
+            const bool more = t + S < steps;
             typename P::Held held_p;
             typename Q::Held held_q;
-            char *const free_p = lds_p + at_p, *const free_q = lds_q + at_q;
-            if constexpr (VEC) {
-                if (t + SQ < steps) Q::stage(free_q, q.at, q.ld, qo, (t + SQ) * BK, K, tid);
-                if (t + SP < steps) P::stage(free_p, p.at, p.ld, po, (t + SP) * BK, K, tid);
-            } else {
-                if (t + SQ < steps) Q::fetch(held_q, q.at, q.ld, q.rows, (t + SQ) * BK, K, tid);
-                if (t + SP < steps) P::fetch(held_p, p.at, p.ld, p.rows, (t + SP) * BK, K, tid);
+            if (more) {
+                if constexpr (VEC) {
+                    P::stage(here, p.at, p.ld, po, (t + S) * BK, K, tid);
+                    Q::stage(here + P::kBytes, q.at, q.ld, qo, (t + S) * BK, K, tid);
+                } else {
+                    P::fetch(held_p, p.at, p.ld, p.rows, (t + S) * BK, K, tid);
+                    Q::fetch(held_q, q.at, q.ld, q.rows, (t + S) * BK, K, tid);
+                }
             }
-            at_p = at_p + kP == SP * kP ? 0 : at_p + kP;
-            at_q = at_q + kQ == SQ * kQ ? 0 : at_q + kQ;
-            if (SQ > 1) read(first, lds_p + at_p, lds_q + at_q, 0, tid);   // past the end: not used
+            cur = cur + kStage == kLdsBytes ? 0 : cur + kStage;
+            read(first, lds + cur, lds + cur + P::kBytes, 0, tid);   // past the end: not used
             multiply(second, sums);
-            if constexpr (!VEC) {
-                if (t + SQ < steps) Q::put(free_q, held_q, tid);
-                if (t + SP < steps) P::put(free_p, held_p, tid);
-            }
+            if constexpr (!VEC)
+                if (more) {
+                    P::put(here, held_p, tid);
+                    Q::put(here + P::kBytes, held_q, tid);
+                }
         }
         step_barrier<0>();
         if constexpr (SUMS && sizeof(T) == 4)

@@ -591,13 +591,13 @@ hipError_t launch_tiled(const OrthogonalizeArgs& a) {
         return launch_steps<T, PairProduct<64, 64, 2, 4, true, 8>, PairProduct<64, 64, 2, 4, false, 8>, 2>(a, w, low);
     } else {
         if (count(256) >= kBig)
-            return launch_steps<T, TileProduct<h16, 256, 256, 4, 2, true, true, 2, 2>,
-                                TileProduct<h16, 256, 256, 4, 2, false, true, 2, 2>, 1>(a, w, low);
+            return launch_steps<T, TileProduct<h16, 256, 256, 4, 2, true, true, 2>,
+                                TileProduct<h16, 256, 256, 4, 2, false, true, 2>, 1>(a, w, low);
         if (count(128) >= kMid)
-            return launch_steps<T, TileProduct<h16, 128, 128, 4, 4, true, true, 2, 2>,
-                                TileProduct<h16, 128, 128, 4, 4, false, true, 2, 2>, 1>(a, w, low);
-        return launch_steps<T, TileProduct<h16, 64, 64, 2, 2, true, true, 4, 4>,
-                            TileProduct<h16, 64, 64, 2, 2, false, true, 4, 4>, 1>(a, w, low);
+            return launch_steps<T, TileProduct<h16, 128, 128, 4, 4, true, true, 2>,
+                                TileProduct<h16, 128, 128, 4, 4, false, true, 2>, 1>(a, w, low);
+        return launch_steps<T, TileProduct<h16, 64, 64, 2, 2, true, true, 4>,
+                            TileProduct<h16, 64, 64, 2, 2, false, true, 4>, 1>(a, w, low);
     }
 }
 

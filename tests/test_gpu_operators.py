@@ -315,3 +315,65 @@ def test_update_shapes_streams_and_refusals(dmr):
             dmr.dmr_orthogonalize(big, out, ws, **kw)
     with pytest.raises(dmr.DmrError):
         dmr.dmr_orthogonalize(big, out, ws[:256])
+
+
+def test_layer_of_very_many_groups(dmr):
+    # more groups than a launch has places in one grid dimension
+    sizes = (np.arange(70000) % 3 == 0).astype(np.int64) * 2
+    _check_layer(dmr, list(sizes), 8, 8, "float32")
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_layer_past_32_bit_offsets(dmr, dtype):
+    # x holds more than 2^32 bytes: rows at the end, aligned and not
+    for cin, cout in ((2048, 16), (2047, 3)):
+        R = (1 << 20) + 3000
+        say(f"[gpu] grouped_linear {dtype} {R} rows of {cin}")
+        x = torch.zeros((R, cin), dtype=TORCH[dtype], device=DEV)
+        off = np.array([0, 1 << 20, R - 70, R], np.int64)
+        tail = 200
+        xt, x64 = _typed(np.random.default_rng(1).normal(size=(tail, cin)), dtype)
+        x[R - tail:] = xt
+        w, w64 = _typed(np.random.default_rng(2).normal(size=(3, cout, cin)), dtype)
+        g = torch.zeros((R, cout), dtype=TORCH[dtype], device=DEV)
+        gt, g64 = _typed(np.random.default_rng(3).normal(size=(tail, cout)), dtype)
+        g[R - tail:] = gt
+        offd = torch.from_numpy(off).to(DEV)
+        last = np.array([0, 0, tail - 70, tail], np.int64)     # the groups of the rows that are not zero
+        y = dmr.grouped_linear(x, offd, w)
+        _check(y[R - tail:], grouped_linear_forward(x64, last, w64), forward_error_bound(x64, last, w64, None, dtype), "y")
+        assert (y[:R - tail] == 0).all()
+        grads = _backward(dmr, x, offd, w, g)
+        ref, bound = grouped_linear_backward(x64, last, w64, g64), backward_error_bound(x64, last, w64, g64, dtype)
+        _check(grads[0][R - tail:], ref[0], bound[0], "gx")
+        for k in (1, 2):
+            _check(grads[k], ref[k], bound[k], "gw, gb")
+        del x, y, g, grads
+
+
+def test_layers_and_updates_in_a_graph(dmr):
+    off = torch.tensor([0, 300, 300, 2000], dtype=torch.int64, device=DEV)
+    x, w, g = torch.randn(2000, 64, device=DEV), torch.randn(3, 32, 64, device=DEV), torch.randn(2000, 32, device=DEV)
+    u = torch.randn(2, 100, 200, device=DEV)
+
+    def work():
+        y = dmr.grouped_linear(x, off, w)
+        return [y, dmr.orthogonalize(u), dmr.orthogonalize(w)] + _backward(dmr, x, off, w, g)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for k in range(4):
+        x.copy_(torch.randn_like(x))
+        u.copy_(torch.randn_like(u))
+        eager = work()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
