@@ -524,8 +524,9 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
 }
 
 // The tiles of X that make larger tiles worth while: about one for each of the
-// 256 compute units of the larger kind, half as many of the middle one.
-constexpr int64_t kBig = 224, kMid = 128;
+// 256 compute units (one 1024 x 2048 in float32, 128 tiles of 128 x 128: 549
+// us with them, 419 with 64 x 64; one 2048 x 2048, 256 of them: 814 and 1499).
+constexpr int64_t kBig = 224, kMid = 256;
 
 template <class Kernel>
 hipError_t allow_lds(Kernel kernel, int bytes) {
@@ -583,21 +584,30 @@ hipError_t launch_tiled(const OrthogonalizeArgs& a) {
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     const auto count = [&](int t) { return a.B * ((w.sp + t - 1) / t) * ((w.lp + t - 1) / t); };   // tiles of X
+    // X takes 256 x 256 tiles where they fill the device and pad it by a
+    // quarter more than 128 x 128 ones at most (30 of 300 x 2000 in float32:
+    // 735 us with, 635 without), in 16 bits only from a short side of 1024
+    // on: with fewer k the tile's own loads and stores of X are most of its
+    // time, and two smaller workgroups on a compute unit overlap them (27 of
+    // 619 x 1680: 126 us an update with, 109 without; 32 of 1024 x 1024: 140
+    // and 158). The squares' halves take 128 x 128 tiles throughout (4 of
+    // 2048 x 2048 in float32: 143 us with 256 x 256, 123 with 128 x 128).
+    const bool big = count(256) >= kBig && count(256) * 16 <= count(128) * 5 && (PLANES == 2 || w.sp >= 1024);
     if constexpr (PLANES == 2) {
-        if (count(256) >= kBig)
-            return launch_steps<T, PairProduct<128, 128, 2, 4, true, 2>, PairProduct<256, 256, 4, 2, false, 2>, 2>(a, w, low);
-        if (count(128) >= kMid)
-            return launch_steps<T, PairProduct<128, 128, 2, 4, true, 2>, PairProduct<128, 128, 2, 4, false, 2>, 2>(a, w, low);
+        typedef PairProduct<128, 128, 2, 4, true, 2> Square;
+        if (big) return launch_steps<T, Square, PairProduct<256, 256, 4, 2, false, 2>, 2>(a, w, low);
+        if (count(128) >= kMid) return launch_steps<T, Square, PairProduct<128, 128, 2, 4, false, 2>, 2>(a, w, low);
         return launch_steps<T, PairProduct<64, 64, 2, 4, true, 8>, PairProduct<64, 64, 2, 4, false, 8>, 2>(a, w, low);
     } else {
-        if (count(256) >= kBig)
-            return launch_steps<T, TileProduct<h16, 256, 256, 4, 2, true, true, 2>,
-                                TileProduct<h16, 256, 256, 4, 2, false, true, 2>, 1>(a, w, low);
-        if (count(128) >= kMid)
-            return launch_steps<T, TileProduct<h16, 128, 128, 4, 4, true, true, 2>,
-                                TileProduct<h16, 128, 128, 4, 4, false, true, 2>, 1>(a, w, low);
-        return launch_steps<T, TileProduct<h16, 64, 64, 2, 2, true, true, 4>,
-                            TileProduct<h16, 64, 64, 2, 2, false, true, 4>, 1>(a, w, low);
+        typedef TileProduct<h16, 128, 128, 4, 4, true, true, 2> Square;
+        if (big) return launch_steps<T, Square, TileProduct<h16, 256, 256, 4, 2, false, true, 2>, 1>(a, w, low);
+        // with up to 512 k a step of the iteration is mostly its start and its
+        // stores, which many small workgroups overlap better (5 of 512 x
+        // 2048: 289 us with 128 x 128 tiles, 224 with 64 x 64)
+        if (count(128) >= kMid && w.sp > 512)
+            return launch_steps<T, Square, TileProduct<h16, 128, 128, 4, 4, false, true, 2>, 1>(a, w, low);
+        return launch_steps<T, TileProduct<h16, 64, 64, 2, 2, true, true, 4>, TileProduct<h16, 64, 64, 2, 2, false, true, 4>, 1>(
+            a, w, low);
     }
 }
 
