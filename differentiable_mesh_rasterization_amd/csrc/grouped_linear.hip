@@ -480,22 +480,30 @@ hipError_t launch_rows_tile(const GroupedLinearArgs& a, const T* in, int k_in, c
     return hipGetLastError();
 }
 
+// The tile by the widths and by how many there are: the larger, the fewer
+// bytes for a product, but they have to fill 256 compute units. (bfloat16,
+// forward: 2048 rows of 512 to 512, 19.3 us with 256 x 256 tiles, 11.0 with
+// 128 x 128, 9.4 with 64 x 128; 8192 of 1024 to 1024, 128 tiles of 256 x 256,
+// 35.3 and 31.5 with 128 x 128, but the backward's transposed weight 103 and
+// 117. 2^20 rows of 64 to 64: 60 us with 64 x 256, 63 with 64 x 128. 217632 rows
+// of 64 to 3 in float32: 17.7 us with 16 x 256, 14.3 with 16 x 128.)
 template <class T, bool WK>
 hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const T* bias, T* out, int n_out, bool vec,
                        bool wide) {
+    const auto tiles = [&](int bn, int bm) { return (a.R / bm + 1) * ceil_div(n_out, bn); };
     if (a.R <= 16 * a.N)
         return launch_rows_tile<T, TileProduct<T, 64, 16, 4, 1, WK, true, 4>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
     if (n_out <= 16)
         return launch_rows_tile<T, TileProduct<T, 16, 128, 1, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
-    if (n_out <= 64) {
+    if (n_out <= 64 || tiles(128, 128) < 256) {
         if constexpr (sizeof(T) == 2)
-            if (a.R >= 256 * 256)
+            if (tiles(64, 256) >= 256)
                 return launch_rows_tile<T, TileProduct<T, 64, 256, 1, 8, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
                                                                                              wide);
         return launch_rows_tile<T, TileProduct<T, 64, 128, 1, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
     }
     if constexpr (sizeof(T) == 2)
-        if (vec && n_out > 128 && a.R >= 512 * a.N)
+        if (vec && n_out > 128 && a.R >= 512 * a.N && tiles(256, 256) >= (WK ? 224 : 112))
             return launch_rows_tile<T, TileProduct<T, 256, 256, 4, 2, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
                                                                                            wide);
     return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
@@ -585,7 +593,11 @@ hipError_t launch_typed(const GroupedLinearArgs& a, bool backward) {
 // that the pieces of groups longer than one piece can take: a group of
 // r > rows has at most 2 floor(r / rows) of them.
 GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half) {
-    const int64_t side = cin <= 64 && cout <= 64 ? 64 : !half || cin <= 128 || cout <= 128 || R < 512 * N ? 128 : 256;
+    // 256 only where the groups' tiles are many before any piece is cut (2
+    // groups of 256 to 512, 16384 rows in bfloat16: 59 us with, 50 without)
+    const int64_t weights256 = N * ((cin + 255) / 256) * ((cout + 255) / 256);
+    const bool large = half && cin > 128 && cout > 128 && R >= 512 * N && weights256 >= 64;
+    const int64_t side = cin <= 64 && cout <= 64 ? 64 : large ? 256 : 128;
     const int64_t tiles = ((cin + side - 1) / side) * ((cout + side - 1) / side);
     // a piece is at most one of the places' shares of the work: 256 compute
     // units with one workgroup of the largest tiles, two or four of the others
