@@ -37,7 +37,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Bytes of k in a step.
@@ -49,11 +48,9 @@ constexpr int kStepBytes = 128;
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 constexpr uint32_t kBufferRange = 0x80000000u;
 
-// The bits of 1 (16-bit types: twice).
+// The bits of 1, twice.
 template <class T>
 constexpr uint32_t one_bits();
-template <>
-constexpr uint32_t one_bits<float>() { return 0x3F800000u; }
 template <>
 constexpr uint32_t one_bits<_Float16>() { return 0x3C003C00u; }
 template <>
