@@ -185,12 +185,12 @@ __device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, i
 // `k_in` that of `rows_in`; the weight of a group is [n_out][k_in] if WK and
 // [k_in][n_out] if not.
 template <class T, class Tile, bool WK, bool VEC>
-__global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restrict__ rows_in, int64_t R, int k_in,
-                                                              const int64_t* __restrict__ off, int64_t N,
-                                                              const T* __restrict__ weight, int n_out,
-                                                              const T* __restrict__ bias, T* __restrict__ out, bool wide,
-                                                              int64_t tiles, int n_tiles, uint32_t places) {
-    __shared__ alignas(16) char lds[Tile::kLdsBytes];
+__device__ __forceinline__ void rows_of_workgroup(char* lds, uint32_t block, uint32_t blocks,
+                                                  const T* __restrict__ rows_in, int64_t R, int k_in,
+                                                  const int64_t* __restrict__ off, int64_t N,
+                                                  const T* __restrict__ weight, int n_out, const T* __restrict__ bias,
+                                                  T* __restrict__ out, bool wide, int64_t tiles, int n_tiles,
+                                                  uint32_t places) {
     const int tid = threadIdx.x;
     const auto find = [&](uint32_t place) {
         const int64_t id = tile_of_workgroup<kRun>(place);
@@ -207,12 +207,12 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restric
     };
     // A workgroup that takes several tiles finds the next one while a tile is
     // multiplied and issues its first loads before it stores.
-    uint32_t place = blockIdx.x;
+    uint32_t place = block;
     RowTile at = find(place);
     int n0 = column(place);
     if (at.group >= 0) Tile::template begin<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
     while (at.group >= 0) {
-        place += gridDim.x;
+        place += blocks;
         const RowTile next = place < places ? find(place) : RowTile{-1, 0, 0};
         const int next_n0 = column(place);
         Tile t;
@@ -223,6 +223,17 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restric
         at = next;
         n0 = next_n0;
     }
+}
+
+template <class T, class Tile, bool WK, bool VEC>
+__global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restrict__ rows_in, int64_t R, int k_in,
+                                                              const int64_t* __restrict__ off, int64_t N,
+                                                              const T* __restrict__ weight, int n_out,
+                                                              const T* __restrict__ bias, T* __restrict__ out, bool wide,
+                                                              int64_t tiles, int n_tiles, uint32_t places) {
+    __shared__ alignas(16) char lds[Tile::kLdsBytes];
+    rows_of_workgroup<T, Tile, WK, VEC>(lds, blockIdx.x, gridDim.x, rows_in, R, k_in, off, N, weight, n_out, bias, out, wide,
+                                        tiles, n_tiles, places);
 }
 
 // ---------------------------------------------------------------------------
@@ -291,12 +302,11 @@ __device__ __forceinline__ Piece find_piece(const int64_t* __restrict__ off, int
 }
 
 template <class T, class Tile, bool VEC>
-__global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
-    const T* __restrict__ x, const T* __restrict__ g, int64_t R, int cin, int cout, const int64_t* __restrict__ off,
-    int64_t N, int per, T* __restrict__ grad_weight, T* __restrict__ grad_bias, bool wide, float* __restrict__ slots,
-    int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
-    __shared__ alignas(16) char lds[Tile::kLdsBytes];
-    const int64_t id = tile_of_workgroup<kPieceRun>(blockIdx.x);
+__device__ __forceinline__ void weight_grad_of_workgroup(
+    char* lds, uint32_t block, const T* __restrict__ x, const T* __restrict__ g, int64_t R, int cin, int cout,
+    const int64_t* __restrict__ off, int64_t N, int per, T* __restrict__ grad_weight, T* __restrict__ grad_bias, bool wide,
+    float* __restrict__ slots, int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
+    const int64_t id = tile_of_workgroup<kPieceRun>(block);
     if (id >= items) return;
     const int tiles = n_tiles * m_tiles;
     const Piece at = find_piece(off, N, R, per, (int)(id / tiles));
@@ -344,6 +354,35 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
             const int m = Tile::m_of(tid, b);
             if (m < rows) slot[(int64_t)cout * cin + m0 + m] = t.ones[b][0];
         }
+}
+
+template <class T, class Tile, bool VEC>
+__global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
+    const T* __restrict__ x, const T* __restrict__ g, int64_t R, int cin, int cout, const int64_t* __restrict__ off,
+    int64_t N, int per, T* __restrict__ grad_weight, T* __restrict__ grad_bias, bool wide, float* __restrict__ slots,
+    int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
+    __shared__ alignas(16) char lds[Tile::kLdsBytes];
+    weight_grad_of_workgroup<T, Tile, VEC>(lds, blockIdx.x, x, g, R, cin, cout, off, N, per, grad_weight, grad_bias, wide,
+                                           slots, slot_count, items, n_tiles, m_tiles);
+}
+
+// Both gradients in one launch: the workgroups of the weight's, whose chains
+// are the longer ones, and then the rows'.
+template <class T, class RowTile, class WeightTile, bool VEC>
+__global__ __launch_bounds__(RowTile::THREADS) void grouped_both_grads(
+    const T* __restrict__ x, const T* __restrict__ g, int64_t R, int cin, int cout, const int64_t* __restrict__ off,
+    int64_t N, const T* __restrict__ weight, T* __restrict__ grad_x, bool wide_x, int64_t row_tiles, int row_n_tiles,
+    uint32_t row_places, uint32_t weight_places, int per, T* __restrict__ grad_weight, T* __restrict__ grad_bias,
+    bool wide_w, float* __restrict__ slots, int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
+    static_assert(RowTile::THREADS == WeightTile::THREADS, "");
+    __shared__ alignas(16) char lds[RowTile::kLdsBytes > WeightTile::kLdsBytes ? RowTile::kLdsBytes : WeightTile::kLdsBytes];
+    if (blockIdx.x < weight_places)
+        weight_grad_of_workgroup<T, WeightTile, VEC>(lds, blockIdx.x, x, g, R, cin, cout, off, N, per, grad_weight, grad_bias,
+                                                     wide_w, slots, slot_count, items, n_tiles, m_tiles);
+    else
+        rows_of_workgroup<T, RowTile, false, VEC>(lds, blockIdx.x - weight_places, row_places, g, R, cout, off, N, weight,
+                                                  cin, (const T*)nullptr, grad_x, wide_x, row_tiles, row_n_tiles,
+                                                  row_places);
 }
 
 // Adds the pieces of the groups that have more than one, in a fixed order,
@@ -509,6 +548,9 @@ hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const 
     return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
 }
 
+template <class T>
+using SmallWeightTile = TileProduct<T, 64, 64, 2, 2, false, false, 2, true>;
+
 template <class T, class Tile>
 hipError_t launch_weight_tile(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide) {
     const int n_tiles = ceil_div(a.cin, Tile::BN), m_tiles = ceil_div(a.cout, Tile::BM);
@@ -526,6 +568,51 @@ hipError_t launch_weight_tile(const GroupedLinearArgs& a, const GroupedPieces& p
     return hipGetLastError();
 }
 
+template <class T, class RowTile>
+hipError_t launch_both(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide_x, bool wide_w,
+                       int64_t row_tiles, int64_t items) {
+    using WeightTile = SmallWeightTile<T>;
+    const int n_tiles = ceil_div(a.cin, WeightTile::BN), m_tiles = ceil_div(a.cout, WeightTile::BM);
+    const unsigned weights = run_grid<kPieceRun>(items), rows = run_grid<kRun>(row_tiles);
+    const auto both = vec ? grouped_both_grads<T, RowTile, WeightTile, true> : grouped_both_grads<T, RowTile, WeightTile, false>;
+    both<<<weights + rows, RowTile::THREADS, 0, a.stream>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(a.grad_y), a.R, a.cin, a.cout, a.off, a.N,
+        static_cast<const T*>(a.weight), static_cast<T*>(a.grad_x), wide_x, row_tiles, ceil_div(a.cin, RowTile::BN), rows,
+        weights, p.rows, static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias), wide_w, a.workspace, p.slots, items,
+        n_tiles, m_tiles);
+    return hipGetLastError();
+}
+
+// Both gradients in one launch where small tiles serve both: narrow layers,
+// and calls of so few tiles that one gradient's leave the device unfilled.
+// What one waits for, the other fills, and the upstream gradients are read
+// while they are near. false: not such a call. (One launch against two, us.
+// Float32: 217632 rows of 64 to 64, 53 and 64, of 16 to 256, 100 and 172;
+// 8192 of 256 to 256, 37 and 70; 2048 of 1024 to 1024, 1552 tiles, 115 and
+// 94. 16 bits: 1003 rows of 37 to 19, 15.9 and 20.7; 2^20 of 64 to 64, 120
+// and 129; 8192 of 256 to 256, 18.4 and 30.8; 16384 of 256 to 512, 2112
+// tiles, 41 and 49; 64 groups of one row, 1024 to 1024, 16384 tiles, 187 and
+// 118; 166428 rows of 240 to 64, 61 and 66, but 400000 of 512 to 64, 276 and
+// 261.)
+template <class T>
+bool launch_small(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide_x, bool wide_w, hipError_t& err) {
+    constexpr int64_t kFew = sizeof(T) == 4 ? 1536 : 2304;
+    const bool narrow = a.cin <= 64 || (a.cin <= 256 && a.cout <= 64);
+    const int side = SmallWeightTile<T>::BN;
+    if (!a.grad_x || a.R == 0) return false;
+    const bool few_rows = a.R <= 16 * a.N;
+    const int64_t row_tiles = most_row_tiles(a.R, a.N, few_rows ? 16 : 128) * ceil_div(a.cin, 64);
+    const int64_t items = (a.R / p.rows + a.N) * ceil_div(a.cin, side) * ceil_div(a.cout, side);
+    if ((row_tiles + items > kFew && !narrow) || row_tiles + items > 1 << 23) return false;
+    if (few_rows)
+        err = launch_both<T, TileProduct<T, 64, 16, 4, 1, false, true, 4>>(a, p, vec, wide_x, wide_w, row_tiles, items);
+    else if (a.cin <= 16)
+        err = launch_both<T, TileProduct<T, 16, 128, 1, 4, false, true, 2>>(a, p, vec, wide_x, wide_w, row_tiles, items);
+    else
+        err = launch_both<T, TileProduct<T, 64, 128, 1, 4, false, true, 2>>(a, p, vec, wide_x, wide_w, row_tiles, items);
+    return true;
+}
+
 template <class T>
 hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
     const T* bias = static_cast<const T*>(a.bias);
@@ -540,26 +627,28 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
     }
     timing_begin(kKGroupedLinearBwd, a.stream);
     hipError_t err = hipSuccess;
-    if (a.grad_x && a.R > 0)
+    const bool weights = (a.grad_weight || a.grad_bias) && a.N > 0;
+    const bool whole = in16 && out16 && aligned16(a.grad_y);
+    const bool vec_rows = whole && aligned16(a.weight), vec_weights = whole && aligned16(a.x);
+    const bool wide_x = in16 && aligned16(a.grad_x), wide_w = in16 && aligned16(a.grad_weight);
+    const GroupedPieces p = weights ? grouped_pieces(a.R, a.N, a.cin, a.cout, sizeof(T) == 2) : GroupedPieces{};
+    const bool together = weights && launch_small<T>(a, p, vec_rows && vec_weights, wide_x, wide_w, err);
+    if (!together && a.grad_x && a.R > 0)
         err = launch_rows<T, false>(a, static_cast<const T*>(a.grad_y), a.cout, (const T*)nullptr, static_cast<T*>(a.grad_x),
-                                    a.cin, in16 && out16 && aligned16(a.grad_y) && aligned16(a.weight),
-                                    in16 && aligned16(a.grad_x));
-    if (err == hipSuccess && (a.grad_weight || a.grad_bias) && a.N > 0) {
-        const bool vec = in16 && out16 && aligned16(a.x) && aligned16(a.grad_y);
-        const bool wide = in16 && aligned16(a.grad_weight);
-        const GroupedPieces p = grouped_pieces(a.R, a.N, a.cin, a.cout, sizeof(T) == 2);
-        bool done = false;
+                                    a.cin, vec_rows, wide_x);
+    if (err == hipSuccess && weights) {
+        bool done = together;
         if constexpr (sizeof(T) == 2)
-            if (p.side == 256 && vec) {
-                err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, true>>(a, p, vec, wide);
+            if (!done && p.side == 256 && vec_weights) {
+                err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, true>>(a, p, true, wide_w);
                 done = true;
             }
         if (!done)
-            err = p.side == 64
-                      ? launch_weight_tile<T, TileProduct<T, 64, 64, 2, 2, false, false, 2, true>>(a, p, vec, wide)
-                      : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, true>>(a, p, vec, wide);
+            err = p.side == 64 ? launch_weight_tile<T, SmallWeightTile<T>>(a, p, vec_weights, wide_w)
+                               : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, true>>(a, p, vec_weights,
+                                                                                                             wide_w);
         if (err == hipSuccess && p.slots > 0) {
-            const int64_t weights = (int64_t)a.cin * a.cout, values = weights + a.cout;
+            const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout;
             const bool split = values <= 65536;
             const int64_t blocks = split ? (values + kAddValues<true> - 1) / kAddValues<true>
                                          : (values + kAddValues<false> - 1) / kAddValues<false>;
@@ -568,7 +657,7 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
             } else {
                 const auto add = split ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
                 add<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
-                    a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), weights, a.workspace, p.slots,
+                    a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), size, a.workspace, p.slots,
                     (unsigned)blocks, static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
                 err = hipGetLastError();
             }

@@ -123,6 +123,23 @@ def test_layer_gradients_one_at_a_time(dmr, dtype):
         assert torch.equal(some[k], every[k])
 
 
+# the gradients of the rows and of the weights each in a launch of its own:
+# rows of few per group, narrow, wide and unaligned; weights of one small tile
+# and of larger ones; and, of more tiles than one launch of both takes, together
+@pytest.mark.parametrize("dtype", list(TORCH))
+@pytest.mark.parametrize("sizes,cin,cout", [([3, 0, 16, 1, 17], 64, 48), ([3, 0, 16, 1, 17], 37, 65), ([200, 0, 333], 16, 72),
+                                            ([200, 0, 333], 13, 19), ([200, 0, 333], 64, 24), ([200, 0, 333], 61, 130),
+                                            ([200, 0, 333], 136, 200), ([5, 300], 1000, 1100), ([1] * 12, 777, 808)])
+@pytest.mark.parametrize("grads", [(True, False, False), (False, True, True), (True, True, True)])
+def test_layer_gradients_apart(dmr, sizes, cin, cout, dtype, grads):
+    off, (x, x64), (w, w64), _, (g, g64) = _layer_inputs(sizes, cin, cout, dtype, 6)
+    got = _backward(dmr, x, torch.from_numpy(off).to(DEV), w, g, grads)
+    for v, ref, bound, what in zip(got, grouped_linear_backward(x64, off, w64, g64),
+                                   backward_error_bound(x64, off, w64, g64, dtype), ("gx", "gw", "gb")):
+        if v is not None:
+            _check(v, ref, bound, what)
+
+
 @pytest.mark.parametrize("dtype", list(TORCH))
 def test_layer_unaligned_arrays(dmr, dtype):
     # arrays that start one element past a 16-byte boundary, of widths that
