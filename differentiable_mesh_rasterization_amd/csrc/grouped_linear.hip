@@ -595,7 +595,7 @@ hipError_t launch_both(const GroupedLinearArgs& a, const GroupedPieces& p, bool 
 // 118; 166428 rows of 240 to 64, 61 and 66, but 400000 of 512 to 64, 276 and
 // 261.)
 template <class T>
-bool launch_small(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide_x, bool wide_w, hipError_t& err) {
+bool launch_together(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide_x, bool wide_w, hipError_t& err) {
     constexpr int64_t kFew = sizeof(T) == 4 ? 1536 : 2304;
     const bool narrow = a.cin <= 64 || (a.cin <= 256 && a.cout <= 64);
     const int side = SmallWeightTile<T>::BN;
@@ -632,7 +632,7 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
     const bool vec_rows = whole && aligned16(a.weight), vec_weights = whole && aligned16(a.x);
     const bool wide_x = in16 && aligned16(a.grad_x), wide_w = in16 && aligned16(a.grad_weight);
     const GroupedPieces p = weights ? grouped_pieces(a.R, a.N, a.cin, a.cout, sizeof(T) == 2) : GroupedPieces{};
-    const bool together = weights && launch_small<T>(a, p, vec_rows && vec_weights, wide_x, wide_w, err);
+    const bool together = weights && launch_together<T>(a, p, vec_rows && vec_weights, wide_x, wide_w, err);
     if (!together && a.grad_x && a.R > 0)
         err = launch_rows<T, false>(a, static_cast<const T*>(a.grad_y), a.cout, (const T*)nullptr, static_cast<T*>(a.grad_x),
                                     a.cin, vec_rows, wide_x);
