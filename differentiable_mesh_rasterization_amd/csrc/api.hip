@@ -534,7 +534,7 @@ dmr_status check_orthogonalize(int64_t B, int32_t m, int32_t n, dmr_dtype dtype)
     if (B < 0 || m < 1 || n < 1) return DMR_ERROR_INVALID_VALUE;
     if (dtype != DMR_FLOAT32 && dtype != DMR_FLOAT16 && dtype != DMR_BFLOAT16) return DMR_ERROR_INVALID_VALUE;
     if (m > DMR_MAX_LINEAR_WIDTH || n > DMR_MAX_LINEAR_WIDTH) return DMR_ERROR_UNSUPPORTED;
-    if (B > 0 && orthogonalize_workspace(B, m, n, dtype) == 0) return DMR_ERROR_UNSUPPORTED;
+    if (B > 0 && orthogonalize_workspace(B, m, n) == 0) return DMR_ERROR_UNSUPPORTED;
     return DMR_SUCCESS;
 }
 
@@ -542,7 +542,7 @@ dmr_status check_orthogonalize(int64_t B, int32_t m, int32_t n, dmr_dtype dtype)
 
 size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dtype dtype) {
     if (check_orthogonalize(B, m, n, dtype) != DMR_SUCCESS) return 0;
-    return B > 0 ? orthogonalize_workspace(B, m, n, dtype) : 256;
+    return B > 0 ? orthogonalize_workspace(B, m, n) : 256;
 }
 
 dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n, dmr_dtype dtype, int32_t steps, float eps,
@@ -553,7 +553,7 @@ dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n
     if (steps > DMR_MAX_ORTHOGONALIZE_STEPS) return DMR_ERROR_UNSUPPORTED;
     if (B == 0) return DMR_SUCCESS;
     if (!update || !out) return DMR_ERROR_INVALID_VALUE;
-    if (workspace == nullptr || workspace_bytes < orthogonalize_workspace(B, m, n, dtype))
+    if (workspace == nullptr || workspace_bytes < orthogonalize_workspace(B, m, n))
         return DMR_ERROR_WORKSPACE_TOO_SMALL;
     if (!ws_aligned(workspace)) return DMR_ERROR_INVALID_VALUE;
     OrthogonalizeArgs a{};

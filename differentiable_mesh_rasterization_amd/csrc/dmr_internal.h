@@ -457,7 +457,7 @@ struct OrthogonalizeArgs {
     void* out; char* workspace;
     hipStream_t stream;
 };
-size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n, dmr_dtype dtype);   // 0: too large
+size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n);   // 0: too large
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a);
 
 // Timing hooks (api.hip).

@@ -14,13 +14,13 @@
 //       (A A)_ij = (O O)_ij + (d_i + d_j) O_ij,   i != j,
 //       (A A)_ii = (O O)_ii + d_i^2,
 //       X <- (a + B_ii) X_i + (off-diagonal B) X;
-//   X, O and the off-diagonal B are pairs of float16, high + low (22 bits).
-// With PLANES = 2 (float32 and float16 updates) a product is high high +
-// high low + low high, as exact as float32 products at three times the cost of
-// one; with PLANES = 1 (bfloat16 updates) only the high parts are multiplied,
-// and X alone carries its low part. Against the definition in 64 bits on
-// matrices of 64 to 2048 that gives 0.6 times the error of float32 products,
-// and for bfloat16 an error of about a third of its output rounding.
+//   X, O and the off-diagonal B are pairs of float16, high + low (22 bits),
+// and a product is high high + high low + low high, as exact as float32
+// products at three times the cost of one: against the definition in 64 bits
+// on matrices of 64 to 2048 that gives 0.6 times the error of float32 products.
+// bfloat16 updates take the same products: with the high parts alone the error
+// of a 256 x 256 update of 32 strong directions over weak ones is 1.6e-3 of its
+// norm, as much as the rounding of the result; with pairs 1e-5.
 #include "dmr_internal.h"
 #include "mfma_tile.h"
 
@@ -167,10 +167,8 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
 // ---------------------------------------------------------------------------
 
 // Sides are padded to multiples of kPad with zeros, which the iteration
-// keeps. X is [sp, lp], the off-diagonal A and B are [sp, sp]. With PLANES = 2
-// they are held as the pairs that PairProduct reads (32 high parts, 32 low
-// parts, ..); with PLANES = 1 the high parts are a plane for TileProduct, and
-// the low parts of X, which no product reads, another one after it.
+// keeps. X is [sp, lp], the off-diagonal A and B are [sp, sp], held as the
+// pairs that PairProduct reads (32 high parts, 32 low parts, ..).
 constexpr int kPad = 64;
 constexpr int kNormBlocks = 64;
 
@@ -180,7 +178,7 @@ struct Layout {
     size_t bytes;
 };
 
-Layout layout(int64_t B, int m, int n, bool two) {
+Layout layout(int64_t B, int m, int n) {
     Layout w{};
     w.s = m < n ? m : n;
     w.l = m < n ? n : m;
@@ -194,8 +192,8 @@ Layout layout(int64_t B, int m, int n, bool two) {
     };
     const int64_t xs = B * w.sp * w.lp, as = B * w.sp * w.sp;
     for (int k = 0; k < 2; ++k) w.x[k] = take(xs * 4);
-    w.o = take(as * (two ? 4 : 2));
-    w.b = take(as * (two ? 4 : 2));
+    w.o = take(as * 4);
+    w.b = take(as * 4);
     w.diag = take(B * w.sp * 4);
     w.bdiag = take(B * w.sp * 4);
     w.norm = take(B * kNormBlocks * 8);
@@ -205,11 +203,9 @@ Layout layout(int64_t B, int m, int n, bool two) {
 }
 
 // Where a matrix of rows of `ld` values holds value n of row m: its high
-// part, in float16 from the matrix's start.
-template <int PLANES>
-__device__ __forceinline__ int64_t place(int64_t m, int ld, int n) {
-    return PLANES == 2 ? m * 2 * ld + (n >> 5) * 64 + (n & 31) : m * ld + n;
-}
+// part, in float16 from the matrix's start, and kLow further its low part.
+constexpr int kLow = 32;
+__device__ __forceinline__ int64_t place(int64_t m, int ld, int n) { return m * 2 * ld + (n >> 5) * 64 + (n & 31); }
 
 // v as a pair. v is pinned to its float32 value first: the compiler may
 // otherwise round the product or sum that gives it straight to float16 for the
@@ -270,11 +266,11 @@ __global__ __launch_bounds__(256) void orthogonalize_norm(const T* __restrict__ 
 }
 
 // X_0 as float16 pairs, padded; a 64 x 64 tile a workgroup, through LDS when
-// the update is taken transposed. `low`: from a high part to its low part.
-template <class T, int PLANES>
+// the update is taken transposed.
+template <class T>
 __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__ update, int m, int n, float eps,
                                                            int steps, const double* __restrict__ norm, int sp, int lp,
-                                                           h16* __restrict__ x, int64_t low, float* __restrict__ lift) {
+                                                           h16* __restrict__ x, float* __restrict__ lift) {
     __shared__ float tile[64][65];
     __shared__ float s_inv;
     const int tiles_l = lp / 64, tiles = tiles_l * (sp / 64);
@@ -304,7 +300,7 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
     }
     __syncthreads();
     const float inv = s_inv;
-    x += b * sp * (int64_t)lp * PLANES;
+    x += b * sp * (int64_t)lp * 2;
     for (int r = tid >> 3; r < 64; r += 32) {   // 8 values a thread
         const int c = (tid & 7) * 8;
         f16x8 hi, lo;
@@ -315,9 +311,9 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
             hi[i] = h;
             lo[i] = w;
         }
-        h16* at = x + place<PLANES>(i0 + r, lp, j0 + c);
+        h16* at = x + place(i0 + r, lp, j0 + c);
         *reinterpret_cast<f16x8*>(at) = hi;
-        *reinterpret_cast<f16x8*>(at + low) = lo;
+        *reinterpret_cast<f16x8*>(at + kLow) = lo;
     }
 }
 
@@ -338,25 +334,18 @@ __device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
     tj = id - ti * (ti + 1) / 2;
 }
 
-template <class Tile, int PLANES>
-__device__ __forceinline__ void run_tile(Tile& t, char* lds, const h16* p, int64_t ldp, int rows_n, const h16* q, int64_t ldq,
-                                         int rows_m, int K, int tid) {
-    if constexpr (PLANES == 2) t.run(lds, {p, ldp, rows_n}, {q, ldq, rows_m}, K, tid);
-    else t.template run<true>(lds, {p, ldp, rows_n}, {q, ldq, rows_m}, K, tid);
-}
-
 // Off-diagonal pairs and the diagonal of a symmetric matrix, from the tiles
 // of its lower triangle: POLY = false: A = X X^T; true: B = b A + c A A. The
 // upper triangle is written from the same tiles, transposed in LDS by each
 // wave for itself.
-template <class Tile, int PLANES, bool POLY>
+template <class Tile, bool POLY>
 __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16* __restrict__ in, int sp, int K,
                                                                       const float* __restrict__ lift,
                                                                       const float* __restrict__ diag, h16* __restrict__ out,
                                                                       float* __restrict__ out_diag, int tiles, int64_t count) {
     constexpr int BT = Tile::BN;
     // a wave's transposed pair of blocks: 32 rows n of MT 16 columns m
-    constexpr int kTurnRow = Tile::MT * 16 + 8, kTurn = 32 * kTurnRow * PLANES;
+    constexpr int kTurnRow = Tile::MT * 16 + 8, kTurn = 32 * kTurnRow * 2;
     constexpr int kTurnBytes = kTurn * 2 * (Tile::THREADS / 64);
     __shared__ alignas(16) char lds[Tile::kLdsBytes > kTurnBytes ? Tile::kLdsBytes : kTurnBytes];
     int ti, tj;
@@ -365,15 +354,14 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
     const int64_t b = id / tiles;
     triangle_tile((int)(id % tiles), ti, tj);
     const int tid = threadIdx.x, lane = tid & 63, m0 = ti * BT, n0 = tj * BT;
-    in += b * (int64_t)sp * K * PLANES;
-    out += b * (int64_t)sp * sp * PLANES;
+    in += b * (int64_t)sp * K * 2;
+    out += b * (int64_t)sp * sp * 2;
     out_diag += b * sp;
     float back = 1.0f;   // undoes the lift of both factors of X X^T
     if constexpr (POLY) diag += b * sp;
     else back = 1.0f / (lift[b] * lift[b]);
     Tile t;
-    run_tile<Tile, PLANES>(t, lds, in + (int64_t)n0 * K * PLANES, (int64_t)K * PLANES, sp - n0,
-                           in + (int64_t)m0 * K * PLANES, (int64_t)K * PLANES, sp - m0, K, tid);
+    t.run(lds, {in + (int64_t)n0 * K * 2, (int64_t)K * 2, sp - n0}, {in + (int64_t)m0 * K * 2, (int64_t)K * 2, sp - m0}, K, tid);
     h16* turn = reinterpret_cast<h16*>(lds) + (tid >> 6) * kTurn;
 #pragma unroll
     for (int a = 0; a < Tile::NT; a += 2) {
@@ -387,9 +375,9 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
             f32x4 dn[2];
             if constexpr (POLY) {
                 const int ms = m < sp ? m : sp - 1, ns = n < sp ? n : sp - 8;   // outside: any value, not stored
-                const h16* at = in + place<PLANES>(ms, sp, ns);
+                const h16* at = in + place(ms, sp, ns);
                 ohi = *reinterpret_cast<const f16x8*>(at);
-                if constexpr (PLANES == 2) olo = *reinterpret_cast<const f16x8*>(at + 32);
+                olo = *reinterpret_cast<const f16x8*>(at + kLow);
                 dm = diag[ms];
                 dn[0] = *reinterpret_cast<const f32x4*>(diag + ns);
                 dn[1] = *reinterpret_cast<const f32x4*>(diag + ns + 4);
@@ -400,8 +388,7 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
                 const float v = t.acc[a + (i >> 2)][c][i & 3];
                 float off;   // the off-diagonal value, scaled
                 if constexpr (POLY) {
-                    float o = (float)ohi[i];
-                    if constexpr (PLANES == 2) o += (float)olo[i];
+                    const float o = (float)ohi[i] + (float)olo[i];
                     // v = kScaleO^2 (O O)_mn, o = kScaleO O_mn
                     off = (kC * kScaleB / (kScaleO * kScaleO)) * v +
                           (kScaleB / kScaleO) * (kB + kC * (dm + dn[i >> 2][i & 3])) * o;
@@ -417,13 +404,13 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
                 if (ti != tj) {
                     h16* to = turn + (8 * (lane >> 4) + i) * kTurnRow + c * 16 + (lane & 15);
                     to[0] = h;
-                    if constexpr (PLANES == 2) to[32 * kTurnRow] = l;
+                    to[32 * kTurnRow] = l;
                 }
             }
             if (inside) {
-                h16* to = out + place<PLANES>(m, sp, n);
+                h16* to = out + place(m, sp, n);
                 *reinterpret_cast<f16x8*>(to) = vhi;
-                if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(to + 32) = vlo;
+                *reinterpret_cast<f16x8*>(to + kLow) = vlo;
             }
         }
         if (ti != tj) {
@@ -436,12 +423,11 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
                 const int rn = row0 + row, cm = col0 + chunk * 8;
                 const h16* from = turn + row * kTurnRow + chunk * 8;
                 const f16x8 hi = *reinterpret_cast<const f16x8*>(from);
-                f16x8 lo;
-                if constexpr (PLANES == 2) lo = *reinterpret_cast<const f16x8*>(from + 32 * kTurnRow);
+                const f16x8 lo = *reinterpret_cast<const f16x8*>(from + 32 * kTurnRow);
                 if (rn < sp && cm < sp) {
-                    h16* to = out + place<PLANES>(rn, sp, cm);
+                    h16* to = out + place(rn, sp, cm);
                     *reinterpret_cast<f16x8*>(to) = hi;
-                    if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(to + 32) = lo;
+                    *reinterpret_cast<f16x8*>(to + kLow) = lo;
                 }
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -451,9 +437,9 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
 
 // X <- (a + B_ii) X_i + (off-diagonal B) X. LAST: the result goes to `out` in
 // its own type and orientation ([m, n], transposed if `turned`) instead.
-template <class T, class Tile, int PLANES, bool LAST>
+template <class T, class Tile, bool LAST>
 __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
-    const h16* __restrict__ poly, const float* __restrict__ bdiag, const h16* __restrict__ x, int64_t low, int sp, int lp,
+    const h16* __restrict__ poly, const float* __restrict__ bdiag, const h16* __restrict__ x, int sp, int lp,
     h16* __restrict__ y, int tiles_n, int tiles, int64_t count, const float* __restrict__ lift, T* __restrict__ out, int s, int l,
     bool turned, bool wide) {
     constexpr int BN = Tile::BN, BM = Tile::BM;
@@ -464,9 +450,9 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
     const int tile = (int)(id % tiles);
     const int m0 = tile / tiles_n * BM, n0 = tile % tiles_n * BN;
     const int tid = threadIdx.x;
-    poly += (b * sp + m0) * (int64_t)sp * PLANES;
-    x += b * sp * (int64_t)lp * PLANES;
-    y += b * sp * (int64_t)lp * PLANES;
+    poly += (b * sp + m0) * (int64_t)sp * 2;
+    x += b * sp * (int64_t)lp * 2;
+    y += b * sp * (int64_t)lp * 2;
     bdiag += b * sp;
     float back = 1.0f;
     if constexpr (LAST) {
@@ -474,7 +460,7 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
         out += b * (int64_t)s * l;
     }
     Tile t;
-    run_tile<Tile, PLANES>(t, lds, x + n0 * PLANES, (int64_t)lp * PLANES, lp - n0, poly, (int64_t)sp * PLANES, sp - m0, sp, tid);
+    t.run(lds, {x + n0 * 2, (int64_t)lp * 2, lp - n0}, {poly, (int64_t)sp * 2, sp - m0}, sp, tid);
 #pragma unroll
     for (int a = 0; a < Tile::NT; a += 2) {
         const int n = n0 + Tile::n_of(tid, a);
@@ -483,8 +469,8 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
         for (int c = 0; c < Tile::MT; ++c) {
             const int m = m0 + Tile::m_of(tid, c);
             if (m >= sp) continue;
-            const int64_t at = place<PLANES>(m, lp, n);
-            const f16x8 ohi = *reinterpret_cast<const f16x8*>(x + at), olo = *reinterpret_cast<const f16x8*>(x + at + low);
+            const int64_t at = place(m, lp, n);
+            const f16x8 ohi = *reinterpret_cast<const f16x8*>(x + at), olo = *reinterpret_cast<const f16x8*>(x + at + kLow);
             const float scale = kA + bdiag[m];
             float v[8];
 #pragma unroll
@@ -500,7 +486,7 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
                     vlo[i] = w;
                 }
                 *reinterpret_cast<f16x8*>(y + at) = vhi;
-                *reinterpret_cast<f16x8*>(y + at + low) = vlo;
+                *reinterpret_cast<f16x8*>(y + at + kLow) = vlo;
             } else if (m < s) {
                 if (!turned && wide) {   // rows of whole 16 bytes
                     if (n < l) {
@@ -535,8 +521,8 @@ hipError_t allow_lds(Kernel kernel, int bytes) {
                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <class T, class Square, class Update, int PLANES>
-hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w, int64_t low) {
+template <class T, class Square, class Update>
+hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w) {
     auto half = [&](int64_t o) { return reinterpret_cast<h16*>(a.workspace + o); };
     auto real = [&](int64_t o) { return reinterpret_cast<float*>(a.workspace + o); };
     const int side = (w.sp + Square::BN - 1) / Square::BN, triangle = side * (side + 1) / 2;
@@ -544,22 +530,22 @@ hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w, int64_t low
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.n % (16 / (int)sizeof(T)) == 0;
     int cur = 0;
     for (int k = 0; k < a.steps; ++k) {
-        orthogonalize_square<Square, PLANES, false><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
+        orthogonalize_square<Square, false><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
             half(w.x[cur]), w.sp, w.lp, real(w.lift), nullptr, half(w.o), real(w.diag), triangle, a.B * triangle);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
-        orthogonalize_square<Square, PLANES, true><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
+        orthogonalize_square<Square, true><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
             half(w.o), w.sp, w.sp, nullptr, real(w.diag), half(w.b), real(w.bdiag), triangle, a.B * triangle);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
         auto update = [&](auto kernel) {
             kernel<<<die_grid(a.B * tiles), Update::THREADS, 0, a.stream>>>(
-                half(w.b), real(w.bdiag), half(w.x[cur]), low, w.sp, w.lp, half(w.x[cur ^ 1]), tiles_n, tiles, a.B * tiles,
+                half(w.b), real(w.bdiag), half(w.x[cur]), w.sp, w.lp, half(w.x[cur ^ 1]), tiles_n, tiles, a.B * tiles,
                 real(w.lift),
                 static_cast<T*>(a.out), w.s, w.l, a.m > a.n, wide);
         };
-        if (k + 1 < a.steps) update(orthogonalize_update<T, Update, PLANES, false>);
-        else update(orthogonalize_update<T, Update, PLANES, true>);
+        if (k + 1 < a.steps) update(orthogonalize_update<T, Update, false>);
+        else update(orthogonalize_update<T, Update, true>);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
         cur ^= 1;
@@ -567,48 +553,33 @@ hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w, int64_t low
     return hipSuccess;
 }
 
-template <class T, int PLANES>
+template <class T>
 hipError_t launch_tiled(const OrthogonalizeArgs& a) {
-    const Layout w = layout(a.B, a.m, a.n, PLANES == 2);
+    const Layout w = layout(a.B, a.m, a.n);
     const T* u = static_cast<const T*>(a.update);
     double* norm = reinterpret_cast<double*>(a.workspace + w.norm);
     const unsigned tiles64 = (unsigned)(a.B * (w.sp / 64) * (w.lp / 64));
-    const int64_t size = (int64_t)a.m * a.n, low = PLANES == 2 ? 32 : a.B * w.sp * w.lp;
+    const int64_t size = (int64_t)a.m * a.n;
     orthogonalize_norm<T><<<(unsigned)(a.B * kNormBlocks), 256, 0, a.stream>>>(
         u, size, (reinterpret_cast<uintptr_t>(u) & 15) == 0 && size * sizeof(T) % 16 == 0, norm);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    orthogonalize_begin<T, PLANES><<<tiles64, 256, 0, a.stream>>>(
-        u, a.m, a.n, a.eps, a.steps, norm, w.sp, w.lp, reinterpret_cast<h16*>(a.workspace + w.x[0]), low,
+    orthogonalize_begin<T><<<tiles64, 256, 0, a.stream>>>(
+        u, a.m, a.n, a.eps, a.steps, norm, w.sp, w.lp, reinterpret_cast<h16*>(a.workspace + w.x[0]),
         reinterpret_cast<float*>(a.workspace + w.lift));
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     const auto count = [&](int t) { return a.B * ((w.sp + t - 1) / t) * ((w.lp + t - 1) / t); };   // tiles of X
     // X takes 256 x 256 tiles where they fill the device and pad it by a
     // quarter more than 128 x 128 ones at most (30 of 300 x 2000 in float32:
-    // 735 us with, 635 without), in 16 bits only from a short side of 1024
-    // on: with fewer k the tile's own loads and stores of X are most of its
-    // time, and two smaller workgroups on a compute unit overlap them (27 of
-    // 619 x 1680: 126 us an update with, 109 without; 32 of 1024 x 1024: 140
-    // and 158). The squares' halves take 128 x 128 tiles throughout (4 of
-    // 2048 x 2048 in float32: 143 us with 256 x 256, 123 with 128 x 128).
-    const bool big = count(256) >= kBig && count(256) * 16 <= count(128) * 5 && (PLANES == 2 || w.sp >= 1024);
-    if constexpr (PLANES == 2) {
-        typedef PairProduct<128, 128, 2, 4, true, 2> Square;
-        if (big) return launch_steps<T, Square, PairProduct<256, 256, 4, 2, false, 2>, 2>(a, w, low);
-        if (count(128) >= kMid) return launch_steps<T, Square, PairProduct<128, 128, 2, 4, false, 2>, 2>(a, w, low);
-        return launch_steps<T, PairProduct<64, 64, 2, 4, true, 8>, PairProduct<64, 64, 2, 4, false, 8>, 2>(a, w, low);
-    } else {
-        typedef TileProduct<h16, 128, 128, 4, 4, true, true, 2> Square;
-        if (big) return launch_steps<T, Square, TileProduct<h16, 256, 256, 4, 2, false, true, 2>, 1>(a, w, low);
-        // with up to 512 k a step of the iteration is mostly its start and its
-        // stores, which many small workgroups overlap better (5 of 512 x
-        // 2048: 289 us with 128 x 128 tiles, 224 with 64 x 64)
-        if (count(128) >= kMid && w.sp > 512)
-            return launch_steps<T, Square, TileProduct<h16, 128, 128, 4, 4, false, true, 2>, 1>(a, w, low);
-        return launch_steps<T, TileProduct<h16, 64, 64, 2, 2, true, true, 4>, TileProduct<h16, 64, 64, 2, 2, false, true, 4>, 1>(
-            a, w, low);
-    }
+    // 735 us with, 635 without). The squares' halves take 128 x 128 tiles
+    // throughout (4 of 2048 x 2048 in float32: 143 us with 256 x 256, 123 with
+    // 128 x 128).
+    typedef PairProduct<128, 128, 2, 4, true, 2> Square;
+    if (count(256) >= kBig && count(256) * 16 <= count(128) * 5)
+        return launch_steps<T, Square, PairProduct<256, 256, 4, 2, false, 2>>(a, w);
+    if (count(128) >= kMid) return launch_steps<T, Square, PairProduct<128, 128, 2, 4, false, 2>>(a, w);
+    return launch_steps<T, PairProduct<64, 64, 2, 4, true, 8>, PairProduct<64, 64, 2, 4, false, 8>>(a, w);
 }
 
 template <class T>
@@ -626,14 +597,14 @@ hipError_t launch_small(const OrthogonalizeArgs& a) {
 
 }  // namespace
 
-size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n, dmr_dtype dtype) {
+size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n) {
     if (is_small(m, n)) return B <= INT32_MAX ? 256 : 0;
-    const Layout one = layout(1, m, n, true);
+    const Layout one = layout(1, m, n);
     // one workgroup for every 64 x 64 tile, 31 bits of them; plane sizes in 63 bits
     const int64_t xs = (int64_t)one.sp * one.lp;
     const int64_t tiles = (xs / 4096 > kNormBlocks ? xs / 4096 : kNormBlocks);
     if (tiles > INT32_MAX || B > INT32_MAX / tiles) return 0;
-    return layout(B, m, n, dtype != DMR_BFLOAT16).bytes;
+    return layout(B, m, n).bytes;
 }
 
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a) {
@@ -641,9 +612,9 @@ hipError_t launch_orthogonalize(const OrthogonalizeArgs& a) {
     const bool small = is_small(a.m, a.n);
     hipError_t err = hipErrorInvalidValue;
     switch (a.dtype) {
-        case DMR_FLOAT32: err = small ? launch_small<float>(a) : launch_tiled<float, 2>(a); break;
-        case DMR_FLOAT16: err = small ? launch_small<_Float16>(a) : launch_tiled<_Float16, 2>(a); break;
-        case DMR_BFLOAT16: err = small ? launch_small<__bf16>(a) : launch_tiled<__bf16, 1>(a); break;
+        case DMR_FLOAT32: err = small ? launch_small<float>(a) : launch_tiled<float>(a); break;
+        case DMR_FLOAT16: err = small ? launch_small<_Float16>(a) : launch_tiled<_Float16>(a); break;
+        case DMR_BFLOAT16: err = small ? launch_small<__bf16>(a) : launch_tiled<__bf16>(a); break;
     }
     timing_end(kKOrthogonalize, a.stream);
     return err;

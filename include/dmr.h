@@ -392,10 +392,9 @@ size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_featur
  *   update, out [B, m, n] of dtype; out is overwritten and may not alias.
  *   steps      1..DMR_MAX_ORTHOGONALIZE_STEPS; eps finite and > 0.
  *   workspace  16-byte aligned, of dmr_orthogonalize_workspace_size() bytes.
- * float32 and float16 are computed to float32 accuracy; for bfloat16 the
- * factors of the products are rounded to 11 bits, which its own rounding
- * hides (sums and X stay in more). A matrix of zeros gives zeros; one with
- * an infinity or NaN gives NaN throughout, and leaves the others as they are.
+ * Every type is computed to float32 accuracy and rounded once. A matrix of
+ * zeros gives zeros; one with an infinity or NaN gives NaN throughout, and
+ * leaves the others as they are.
  * Errors: negative sizes, sides below 1, missing pointers, an unknown dtype,
  * steps below 1, eps not > 0 and finite: DMR_ERROR_INVALID_VALUE; steps above
  * the limit, sides above DMR_MAX_LINEAR_WIDTH or beyond what a launch can

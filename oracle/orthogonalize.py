@@ -77,3 +77,16 @@ def expected_error(update, steps, eps, factor_unit, out_unit):
         s = polynomial(s, 1)[0]
         total += (amplification(np.abs(s), long_, steps - k - 1) * d_next) ** 2
     return float(np.sqrt(total + (out_unit / 2 * np.linalg.norm(s)) ** 2))
+
+
+def float32_error(update, steps, eps):
+    """Frobenius error that the iteration makes on [m, n] when X, A and B are
+    held in binary32 and every product and sum is rounded to it (the norm and
+    X_0's division are exact but for one rounding)."""
+    u = np.asarray(update, np.float64)
+    x = (u / (np.sqrt(np.sum(u * u)) + eps)).astype(np.float32)
+    a, b, c = np.float32(A), np.float32(B), np.float32(C)
+    for _ in range(steps):
+        gram = x @ x.T
+        x = a * x + (b * gram + c * (gram @ gram)) @ x
+    return float(np.linalg.norm(x.astype(np.float64) - orthogonalize(u, steps, eps)))

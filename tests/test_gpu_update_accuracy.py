@@ -1,0 +1,55 @@
+"""The orthogonalised updates on the GPU where their arithmetic is hardest.
+
+Tolerance: X and the factors of the products hold at least 22 bits where
+float32 holds 24, so the result may be off by four times what the same
+iteration in float32 is off by (oracle/orthogonalize.py: float32_error), plus
+its rounding to the output's type (the exact result's own rounding error, and
+a twentieth more, since the values that are rounded differ a little)."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV, require_gpu, say
+from oracle.orthogonalize import float32_error, orthogonalize
+
+pytestmark = pytest.mark.gpu
+
+TORCH = {"float32": torch.float32, "float16": torch.float16, "bfloat16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def dmr():
+    return require_gpu()
+
+
+def _typed(a, dtype):
+    """(device tensor of the type, the values it holds in float64)"""
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(TORCH[dtype])
+    return t.to(DEV), t.to(torch.float64).numpy()
+
+
+def _rounding(ref, dtype):
+    return float(np.linalg.norm(torch.from_numpy(ref).to(TORCH[dtype]).to(torch.float64).numpy() - ref))
+
+
+def check_update(got, u64, dtype, steps=5, eps=1e-7):
+    got = got.to(torch.float64).cpu().numpy()
+    assert got.shape == u64.shape
+    for k in range(len(u64)):
+        ref = orthogonalize(u64[k], steps, eps)
+        bound = 1.05 * _rounding(ref, dtype) + 4 * float32_error(u64[k], steps, eps)
+        err = np.linalg.norm(got[k] - ref)
+        assert err <= bound, (k, err / bound, err / np.linalg.norm(ref))    # a NaN fails too
+
+
+# a momentum of few strong directions: the weak ones are stretched most, and
+# with them what the products of the strong ones lose
+@pytest.mark.parametrize("dtype", list(TORCH))
+@pytest.mark.parametrize("m,n,rank,noise", [(60, 60, 8, 1e-3), (256, 256, 32, 1e-3), (300, 130, 16, 1e-2), (512, 600, 64, 1e-3)])
+def test_update_of_few_strong_directions(dmr, m, n, rank, noise, dtype):
+    say(f"[gpu] orthogonalize {dtype} {m}x{n} rank {rank}")
+    rng = np.random.default_rng(rank)
+    strong = rng.normal(size=(2, m, rank)) @ rng.normal(size=(2, rank, n)) / np.sqrt(rank)
+    u, u64 = _typed(1e-2 * (strong + noise * rng.normal(size=(2, m, n))), dtype)
+    check_update(dmr.orthogonalize(u), u64, dtype)
