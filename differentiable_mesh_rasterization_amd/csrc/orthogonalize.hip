@@ -33,6 +33,13 @@ typedef h16 h16x4 __attribute__((ext_vector_type(4)));
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 16384.0f, kScaleO = 16384.0f, kScaleB = 8192.0f;
 
+// What U is multiplied by to give X_0 times `up`. In float64, and the product
+// with U too: the norm of finite values may pass float32's range, and so may
+// one over a small norm and eps. An infinity or NaN in U gives NaN throughout.
+__device__ __forceinline__ double scale_of(double norm, float eps, float up) {
+    return __builtin_isfinite(norm) ? (double)up / (norm + (double)eps) : __builtin_nan("");
+}
+
 // ---------------------------------------------------------------------------
 // matrices that fit into one workgroup's LDS: one workgroup each, one launch
 // ---------------------------------------------------------------------------
@@ -96,9 +103,8 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
     sum = 0.0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) sum += part[w];
-    const float norm = (float)sqrt(sum);
-    const float inv = __builtin_isfinite(norm) ? 1.0f / (norm + eps) : __builtin_nanf("");
-    for (int i = tid; i < h.sp * h.ldx; i += THREADS) x[i] *= inv;
+    const double inv = scale_of(sqrt(sum), eps, 1.0f);
+    for (int i = tid; i < h.sp * h.ldx; i += THREADS) x[i] = (float)((double)x[i] * inv);
     __syncthreads();
 
     const int st = h.sp / 16, lt = h.lp / 16, tri = st * (st + 1) / 2;
@@ -221,8 +227,8 @@ __device__ __forceinline__ void split(float v, h16& hi, h16& lo) {
 // eps, and a step multiplies it by less than 4: X is held times 2^e as well,
 // with the largest e that keeps 2^e 4^steps t below 1 (or 1), so that its
 // float16 pairs do not lose it below their range. A then counts for nothing.
-__device__ __forceinline__ float lift_of(float norm, float eps, int steps) {
-    const float t = norm / (norm + eps);
+__device__ __forceinline__ float lift_of(double norm, float eps, int steps) {
+    const float t = (float)(norm / (norm + (double)eps));
     if (!(t > 0.0f)) return 1.0f;
     int e = 0;
     (void)__builtin_frexpf(t, &e);   // t < 2^e
@@ -272,7 +278,7 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
                                                            int steps, const double* __restrict__ norm, int sp, int lp,
                                                            h16* __restrict__ x, float* __restrict__ lift) {
     __shared__ float tile[64][65];
-    __shared__ float s_inv;
+    __shared__ double s_inv;
     const int tiles_l = lp / 64, tiles = tiles_l * (sp / 64);
     const int64_t b = blockIdx.x / tiles;
     const int i0 = (int)(blockIdx.x % tiles) / tiles_l * 64, j0 = (int)(blockIdx.x % tiles) % tiles_l * 64;
@@ -281,10 +287,10 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
         double sum = norm[b * kNormBlocks + tid];
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-        const float f = (float)sqrt(sum);
         if (tid == 0) {
+            const double f = sqrt(sum);
             const float up = lift_of(f, eps, steps);
-            s_inv = __builtin_isfinite(f) ? kScaleX * up / (f + eps) : __builtin_nanf("");
+            s_inv = scale_of(f, eps, kScaleX * up);
             if (blockIdx.x % tiles == 0) lift[b] = up;
         }
     }
@@ -299,7 +305,7 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
         else tile[r][tid & 63] = v;
     }
     __syncthreads();
-    const float inv = s_inv;
+    const double inv = s_inv;
     x += b * sp * (int64_t)lp * 2;
     for (int r = tid >> 3; r < 64; r += 32) {   // 8 values a thread
         const int c = (tid & 7) * 8;
@@ -307,7 +313,7 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             h16 h, w;
-            split(tile[r][c + i] * inv, h, w);
+            split((float)((double)tile[r][c + i] * inv), h, w);
             hi[i] = h;
             lo[i] = w;
         }

@@ -53,3 +53,31 @@ def test_update_of_few_strong_directions(dmr, m, n, rank, noise, dtype):
     strong = rng.normal(size=(2, m, rank)) @ rng.normal(size=(2, rank, n)) / np.sqrt(rank)
     u, u64 = _typed(1e-2 * (strong + noise * rng.normal(size=(2, m, n))), dtype)
     check_update(dmr.orthogonalize(u), u64, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("m,n", [(64, 64), (100, 260)])
+@pytest.mark.parametrize("top", [1e37, 3e38])
+def test_update_whose_norm_passes_float32(dmr, m, n, top, dtype):
+    u, u64 = _typed(np.random.default_rng(4).uniform(-top, top, size=(2, m, n)), dtype)
+    assert np.isfinite(u64).all() and np.linalg.norm(u64[0]) > 3.5e38
+    check_update(dmr.orthogonalize(u), u64, dtype)
+
+
+@pytest.mark.parametrize("dtype", list(TORCH))
+@pytest.mark.parametrize("m,n", [(8, 12), (100, 260)])
+@pytest.mark.parametrize("eps", [2.0 ** -149, 2.0 ** -126, 1e-30])
+def test_update_of_zeros_for_any_eps(dmr, m, n, eps, dtype):
+    u = torch.zeros((2, m, n), dtype=TORCH[dtype], device=DEV)
+    for steps in (1, 5):
+        assert (dmr.orthogonalize(u, steps, eps) == 0).all()
+
+
+# |U| and eps both far below 1, down to float32's subnormal values
+@pytest.mark.parametrize("m,n", [(8, 12), (100, 260)])
+@pytest.mark.parametrize("norm,eps", [(1e-36, 1e-12), (1e-36, 1e-38), (1e-38, 2.0 ** -126), (1e-40, 2.0 ** -140)])
+@pytest.mark.parametrize("steps", [1, 5])
+def test_update_of_tiny_values(dmr, m, n, norm, eps, steps):
+    eps = float(np.float32(eps))
+    u, u64 = _typed(np.random.default_rng(6).normal(size=(1, m, n)) * norm / np.sqrt(m * n), "float32")
+    check_update(dmr.orthogonalize(u, steps, eps), u64, "float32", steps, eps)
