@@ -31,13 +31,14 @@ typedef _Float16 h16;
 typedef h16 h16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kScaleX = 16384.0f, kScaleO = 16384.0f, kScaleB = 8192.0f;
+constexpr int kLogScaleX = 14;
+constexpr float kScaleX = 1 << kLogScaleX, kScaleO = 16384.0f, kScaleB = 8192.0f;
 
-// What U is multiplied by to give X_0 times `up`. In float64, and the product
+// What U is multiplied by to give X_0 times 2^up. In float64, and the product
 // with U too: the norm of finite values may pass float32's range, and so may
 // one over a small norm and eps. An infinity or NaN in U gives NaN throughout.
-__device__ __forceinline__ double scale_of(double norm, float eps, float up) {
-    return __builtin_isfinite(norm) ? (double)up / (norm + (double)eps) : __builtin_nan("");
+__device__ __forceinline__ double scale_of(double norm, float eps, int up) {
+    return __builtin_isfinite(norm) ? __builtin_ldexp(1.0, up) / (norm + (double)eps) : __builtin_nan("");
 }
 
 // ---------------------------------------------------------------------------
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
     sum = 0.0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) sum += part[w];
-    const double inv = scale_of(sqrt(sum), eps, 1.0f);
+    const double inv = scale_of(sqrt(sum), eps, 0);
     for (int i = tid; i < h.sp * h.ldx; i += THREADS) x[i] = (float)((double)x[i] * inv);
     __syncthreads();
 
@@ -224,16 +225,20 @@ __device__ __forceinline__ void split(float v, h16& hi, h16& lo) {
 }
 
 // X_0 has the norm t = |U| / (|U| + eps), which is tiny when |U| is far below
-// eps, and a step multiplies it by less than 4: X is held times 2^e as well,
-// with the largest e that keeps 2^e 4^steps t below 1 (or 1), so that its
-// float16 pairs do not lose it below their range. A then counts for nothing.
-__device__ __forceinline__ float lift_of(double norm, float eps, int steps) {
-    const float t = (float)(norm / (norm + (double)eps));
-    if (!(t > 0.0f)) return 1.0f;
+// eps, and a step multiplies it by 3.4445 < 2^1.785 at most. So that its float16
+// pairs do not lose it below their range, X is held times a power of two, the
+// largest that keeps this bound below 1 (or 1): 2^lift_of for X_0, 2^lift_at
+// after `step` steps, brought down as X grows. A is put back to its own scale.
+__device__ __forceinline__ int lift_of(double norm, float eps) {
+    const double t = norm / (norm + (double)eps);
+    if (!(t > 0.0)) return 0;   // zeros, or NaN
     int e = 0;
-    (void)__builtin_frexpf(t, &e);   // t < 2^e
-    e = -e - 2 * steps;
-    return e > 0 ? __builtin_ldexpf(1.0f, e < 88 ? e : 88) : 1.0f;
+    (void)__builtin_frexp(t, &e);   // t < 2^e
+    return e < 0 ? -e : 0;
+}
+__device__ __forceinline__ int lift_at(int lift, int step) {
+    const int e = lift - (step * 1828 + 1023) / 1024;
+    return step > 0 ? (e > 0 ? e : 0) : lift;
 }
 
 // Sum of squares of a slice of each matrix (float64: no overflow, and the
@@ -275,8 +280,8 @@ __global__ __launch_bounds__(256) void orthogonalize_norm(const T* __restrict__ 
 // the update is taken transposed.
 template <class T>
 __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__ update, int m, int n, float eps,
-                                                           int steps, const double* __restrict__ norm, int sp, int lp,
-                                                           h16* __restrict__ x, float* __restrict__ lift) {
+                                                           const double* __restrict__ norm, int sp, int lp,
+                                                           h16* __restrict__ x, int* __restrict__ lift) {
     __shared__ float tile[64][65];
     __shared__ double s_inv;
     const int tiles_l = lp / 64, tiles = tiles_l * (sp / 64);
@@ -289,8 +294,8 @@ __global__ __launch_bounds__(256) void orthogonalize_begin(const T* __restrict__
         for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
         if (tid == 0) {
             const double f = sqrt(sum);
-            const float up = lift_of(f, eps, steps);
-            s_inv = scale_of(f, eps, kScaleX * up);
+            const int up = lift_of(f, eps);
+            s_inv = scale_of(f, eps, kLogScaleX + up);
             if (blockIdx.x % tiles == 0) lift[b] = up;
         }
     }
@@ -332,6 +337,9 @@ __device__ __forceinline__ int64_t die_place(int64_t count) {
 }
 __host__ __forceinline__ unsigned die_grid(int64_t count) { return (unsigned)((count + 7) / 8 * 8); }
 
+// (The squares' arguments, and the updates' that come before the last step's
+// own, fill one 64-byte line: a second one costs 0.3 us a launch.)
+
 // Tile (ti, tj), ti >= tj, of the lower triangle.
 __device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
     ti = (int)((__builtin_sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
@@ -341,14 +349,14 @@ __device__ __forceinline__ void triangle_tile(int id, int& ti, int& tj) {
 }
 
 // Off-diagonal pairs and the diagonal of a symmetric matrix, from the tiles
-// of its lower triangle: POLY = false: A = X X^T; true: B = b A + c A A. The
-// upper triangle is written from the same tiles, transposed in LDS by each
+// of its lower triangle: POLY = false: A = X X^T; true: a + B = a + b A + c A A,
+// times what takes X to the next step's lift. The upper triangle is written from the same tiles, transposed in LDS by each
 // wave for itself.
 template <class Tile, bool POLY>
-__global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16* __restrict__ in, int sp, int K,
-                                                                      const float* __restrict__ lift,
+__global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16* __restrict__ in, int sp, int K, int tiles,
+                                                                      int count, const int* __restrict__ lift,
                                                                       const float* __restrict__ diag, h16* __restrict__ out,
-                                                                      float* __restrict__ out_diag, int tiles, int64_t count) {
+                                                                      float* __restrict__ out_diag, int step) {
     constexpr int BT = Tile::BN;
     // a wave's transposed pair of blocks: 32 rows n of MT 16 columns m
     constexpr int kTurnRow = Tile::MT * 16 + 8, kTurn = 32 * kTurnRow * 2;
@@ -363,11 +371,13 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
     in += b * (int64_t)sp * K * 2;
     out += b * (int64_t)sp * sp * 2;
     out_diag += b * sp;
-    float back = 1.0f;   // undoes the lift of both factors of X X^T
     if constexpr (POLY) diag += b * sp;
-    else back = 1.0f / (lift[b] * lift[b]);
+    const int lifted = lift[b];
+    asm("" : "+s"(step));   // both are loaded here, not after the product
     Tile t;
     t.run(lds, {in + (int64_t)n0 * K * 2, (int64_t)K * 2, sp - n0}, {in + (int64_t)m0 * K * 2, (int64_t)K * 2, sp - m0}, K, tid);
+    const int held = lift_at(lifted, step);
+    const float scale = __builtin_ldexpf(1.0f, POLY ? lift_at(lifted, step + 1) - held : -2 * held);
     h16* turn = reinterpret_cast<h16*>(lds) + (tid >> 6) * kTurn;
 #pragma unroll
     for (int a = 0; a < Tile::NT; a += 2) {
@@ -396,12 +406,13 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
                 if constexpr (POLY) {
                     const float o = (float)ohi[i] + (float)olo[i];
                     // v = kScaleO^2 (O O)_mn, o = kScaleO O_mn
-                    off = (kC * kScaleB / (kScaleO * kScaleO)) * v +
-                          (kScaleB / kScaleO) * (kB + kC * (dm + dn[i >> 2][i & 3])) * o;
-                    if (m == n + i && inside) out_diag[m] = kC * (v * (1.0f / (kScaleO * kScaleO)) + dm * dm) + kB * dm;
+                    off = ((kC * kScaleB / (kScaleO * kScaleO)) * v +
+                           (kScaleB / kScaleO) * (kB + kC * (dm + dn[i >> 2][i & 3])) * o) * scale;
+                    if (m == n + i && inside)
+                        out_diag[m] = (kA + (kC * (v * (1.0f / (kScaleO * kScaleO)) + dm * dm) + kB * dm)) * scale;
                 } else {
-                    off = v * (kScaleO / (kScaleX * kScaleX)) * back;
-                    if (m == n + i && inside) out_diag[m] = v * (1.0f / (kScaleX * kScaleX)) * back;
+                    off = v * (kScaleO / (kScaleX * kScaleX)) * scale;
+                    if (m == n + i && inside) out_diag[m] = v * (1.0f / (kScaleX * kScaleX)) * scale;
                 }
                 h16 h, l;
                 split(m == n + i ? 0.0f : off, h, l);
@@ -446,8 +457,8 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_square(const h16*
 template <class T, class Tile, bool LAST>
 __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
     const h16* __restrict__ poly, const float* __restrict__ bdiag, const h16* __restrict__ x, int sp, int lp,
-    h16* __restrict__ y, int tiles_n, int tiles, int64_t count, const float* __restrict__ lift, T* __restrict__ out, int s, int l,
-    bool turned, bool wide) {
+    h16* __restrict__ y, int tiles_n, int tiles, int count, int step, const int* __restrict__ lift,
+    T* __restrict__ out, int s, int l, bool turned, bool wide) {
     constexpr int BN = Tile::BN, BM = Tile::BM;
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
     const int64_t id = die_place(count);
@@ -460,13 +471,15 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
     x += b * sp * (int64_t)lp * 2;
     y += b * sp * (int64_t)lp * 2;
     bdiag += b * sp;
-    float back = 1.0f;
+    int lifted = 0;
     if constexpr (LAST) {
-        back = 1.0f / (kScaleX * lift[b]);
+        lifted = lift[b];
+        asm("" : "+s"(step));   // both are loaded here, not after the product
         out += b * (int64_t)s * l;
     }
     Tile t;
     t.run(lds, {x + n0 * 2, (int64_t)lp * 2, lp - n0}, {poly, (int64_t)sp * 2, sp - m0}, sp, tid);
+    const int back = -kLogScaleX - lift_at(lifted, step + 1);
 #pragma unroll
     for (int a = 0; a < Tile::NT; a += 2) {
         const int n = n0 + Tile::n_of(tid, a);
@@ -477,7 +490,7 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
             if (m >= sp) continue;
             const int64_t at = place(m, lp, n);
             const f16x8 ohi = *reinterpret_cast<const f16x8*>(x + at), olo = *reinterpret_cast<const f16x8*>(x + at + kLow);
-            const float scale = kA + bdiag[m];
+            const float scale = bdiag[m];
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -498,7 +511,7 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
                     if (n < l) {
                         struct alignas(16) Row { T v[8]; } row;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) row.v[i] = (T)(v[i] * back);
+                        for (int i = 0; i < 8; ++i) row.v[i] = (T)__builtin_ldexpf(v[i], back);
                         T* to = out + (int64_t)m * l + n;
                         if (sizeof(T) == 2 || n + 4 < l) *reinterpret_cast<Row*>(to) = row;
                         else
@@ -508,7 +521,8 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (n + i < l) out[turned ? (int64_t)(n + i) * s + m : (int64_t)m * l + n + i] = (T)(v[i] * back);
+                        if (n + i < l)
+                            out[turned ? (int64_t)(n + i) * s + m : (int64_t)m * l + n + i] = (T)__builtin_ldexpf(v[i], back);
                 }
             }
         }
@@ -531,24 +545,25 @@ template <class T, class Square, class Update>
 hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w) {
     auto half = [&](int64_t o) { return reinterpret_cast<h16*>(a.workspace + o); };
     auto real = [&](int64_t o) { return reinterpret_cast<float*>(a.workspace + o); };
+    const int* lift = reinterpret_cast<const int*>(a.workspace + w.lift);
     const int side = (w.sp + Square::BN - 1) / Square::BN, triangle = side * (side + 1) / 2;
     const int tiles_n = (w.lp + Update::BN - 1) / Update::BN, tiles = tiles_n * ((w.sp + Update::BM - 1) / Update::BM);
+    const int squares = (int)a.B * triangle, updates = (int)a.B * tiles;   // no more than 64 x 64 tiles of X
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.n % (16 / (int)sizeof(T)) == 0;
     int cur = 0;
     for (int k = 0; k < a.steps; ++k) {
-        orthogonalize_square<Square, false><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
-            half(w.x[cur]), w.sp, w.lp, real(w.lift), nullptr, half(w.o), real(w.diag), triangle, a.B * triangle);
+        orthogonalize_square<Square, false><<<die_grid(squares), Square::THREADS, 0, a.stream>>>(
+            half(w.x[cur]), w.sp, w.lp, triangle, squares, lift, nullptr, half(w.o), real(w.diag), k);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
-        orthogonalize_square<Square, true><<<die_grid(a.B * triangle), Square::THREADS, 0, a.stream>>>(
-            half(w.o), w.sp, w.sp, nullptr, real(w.diag), half(w.b), real(w.bdiag), triangle, a.B * triangle);
+        orthogonalize_square<Square, true><<<die_grid(squares), Square::THREADS, 0, a.stream>>>(
+            half(w.o), w.sp, w.sp, triangle, squares, lift, real(w.diag), half(w.b), real(w.bdiag), k);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
         auto update = [&](auto kernel) {
-            kernel<<<die_grid(a.B * tiles), Update::THREADS, 0, a.stream>>>(
-                half(w.b), real(w.bdiag), half(w.x[cur]), w.sp, w.lp, half(w.x[cur ^ 1]), tiles_n, tiles, a.B * tiles,
-                real(w.lift),
-                static_cast<T*>(a.out), w.s, w.l, a.m > a.n, wide);
+            kernel<<<die_grid(updates), Update::THREADS, 0, a.stream>>>(
+                half(w.b), real(w.bdiag), half(w.x[cur]), w.sp, w.lp, half(w.x[cur ^ 1]), tiles_n, tiles, updates, k,
+                lift, static_cast<T*>(a.out), w.s, w.l, a.m > a.n, wide);
         };
         if (k + 1 < a.steps) update(orthogonalize_update<T, Update, false>);
         else update(orthogonalize_update<T, Update, true>);
@@ -571,8 +586,8 @@ hipError_t launch_tiled(const OrthogonalizeArgs& a) {
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     orthogonalize_begin<T><<<tiles64, 256, 0, a.stream>>>(
-        u, a.m, a.n, a.eps, a.steps, norm, w.sp, w.lp, reinterpret_cast<h16*>(a.workspace + w.x[0]),
-        reinterpret_cast<float*>(a.workspace + w.lift));
+        u, a.m, a.n, a.eps, norm, w.sp, w.lp, reinterpret_cast<h16*>(a.workspace + w.x[0]),
+        reinterpret_cast<int*>(a.workspace + w.lift));
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     const auto count = [&](int t) { return a.B * ((w.sp + t - 1) / t) * ((w.lp + t - 1) / t); };   // tiles of X

@@ -81,3 +81,27 @@ def test_update_of_tiny_values(dmr, m, n, norm, eps, steps):
     eps = float(np.float32(eps))
     u, u64 = _typed(np.random.default_rng(6).normal(size=(1, m, n)) * norm / np.sqrt(m * n), "float32")
     check_update(dmr.orthogonalize(u, steps, eps), u64, "float32", steps, eps)
+
+
+# |U| = t eps: X starts at t and grows by 3.4445 a step at most
+@pytest.mark.parametrize("dtype", list(TORCH))
+@pytest.mark.parametrize("m,n", [(40, 30), (96, 200), (150, 90)])
+@pytest.mark.parametrize("t,steps", [(1e-25, 5), (1e-6, 8), (1e-8, 12), (1e-10, 16), (1e-9, 20), (1e-33, 64)])
+def test_update_far_below_eps(dmr, m, n, t, steps, dtype):
+    say(f"[gpu] orthogonalize {dtype} {m}x{n} at {t} of eps, {steps} steps")
+    u, u64 = _typed(np.random.default_rng(steps).normal(size=(2, m, n)) * 1e-2, dtype)
+    eps = float(np.float32(np.linalg.norm(u64[0]) / t))
+    check_update(dmr.orthogonalize(u, steps, eps), u64, dtype, steps, eps)
+
+
+@pytest.mark.parametrize("m,n", [(40, 30), (150, 90)])
+def test_update_of_matrices_of_different_norms(dmr, m, n):
+    u, u64 = _typed(np.random.default_rng(3).normal(size=(4, m, n)) * np.array([1.0, 1e-13, 1e-7, 1e-30])[:, None, None], "float32")
+    check_update(dmr.orthogonalize(u, 10), u64, "float32", 10)
+
+
+@pytest.mark.parametrize("m,n", [(8, 12), (100, 260)])
+@pytest.mark.parametrize("steps", [1, 5, 40, 64])
+def test_update_of_subnormal_values_far_below_eps(dmr, m, n, steps):
+    u, u64 = _typed(np.random.default_rng(7).normal(size=(1, m, n)) * 3e-43, "float32")
+    check_update(dmr.orthogonalize(u, steps, 1.0), u64, "float32", steps, 1.0)
