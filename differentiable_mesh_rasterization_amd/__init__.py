@@ -25,6 +25,7 @@ import os
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdmr.so")
@@ -714,8 +715,10 @@ def grouped_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Ten
     """y_r = W_n x_r + b_n for the rows r of every group n (a mesh's
     vertices, an image's pixels): x [R, in], row_offsets [N + 1] int64,
     weight [N, out, in], bias [N, out], all of one type (float32, float16 or
-    bfloat16). Differentiable with respect to x, weight and bias."""
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
+    bfloat16). Differentiable with respect to x, weight and bias (in reverse
+    mode; forward mode raises)."""
+    if forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+            x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
         return _GroupedLinear.apply(x, row_offsets, weight, bias)
     dev, dt, R, cin, N, cout, code = _grouped_inputs(x, row_offsets, weight)
     if bias is not None and not _alike(bias, dt, dev, (N, cout)):

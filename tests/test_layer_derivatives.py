@@ -1,0 +1,71 @@
+"""The derivatives of the per-group layer beyond the first backward pass, on
+the CPU: the library's calls are replaced by the same products in 64 bits, so
+that what is tested is how the autograd functions put them together."""
+
+import numpy as np
+import pytest
+import torch
+import torch.autograd.forward_ad as forward_ad
+
+import differentiable_mesh_rasterization_amd as dmr
+from oracle.grouped_linear import grouped_linear_backward, grouped_linear_forward
+
+SIZES = [3, 0, 1, 4]
+
+
+def _np(t):
+    return t.detach().numpy()
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    def forward(x, off, weight, bias, y):
+        y.copy_(torch.from_numpy(grouped_linear_forward(_np(x), _np(off), _np(weight), None if bias is None else _np(bias))))
+
+    def backward(x, off, weight, g, gx, gw, gb, workspace=None):
+        assert all(t.is_contiguous() for t in (x, off, weight, g))
+        for to, value in zip((gx, gw, gb), grouped_linear_backward(_np(x), _np(off), _np(weight), _np(g))):
+            if to is not None:
+                to.copy_(torch.from_numpy(value))
+
+    monkeypatch.setitem(dmr.DTYPES, torch.float64, 3)
+    monkeypatch.setattr(dmr, "dmr_grouped_linear_fwd", forward)
+    monkeypatch.setattr(dmr, "dmr_grouped_linear_bwd", backward)
+    monkeypatch.setattr(dmr, "dmr_grouped_linear_workspace_size", lambda *a: 256)
+    monkeypatch.setattr(dmr, "_launch_grouped", lambda x, R, cin, off, N, w, b, cout, code, y, dev: forward(x, off, w, b, y))
+
+
+def _inputs(cin=4, cout=3, needs=(True, True, True)):
+    gen = torch.Generator().manual_seed(1)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(SIZES)]), dtype=torch.int64)
+    shapes = ((sum(SIZES), cin), (len(SIZES), cout, cin), (len(SIZES), cout))
+    x, w, b = (torch.randn(s, generator=gen, dtype=torch.float64).requires_grad_(n) for s, n in zip(shapes, needs))
+    return off, x, w, b
+
+
+def _formula(x, off, w, b=None):
+    group = torch.repeat_interleave(torch.arange(len(SIZES)), torch.tensor(SIZES))
+    y = (w[group] @ x[:, :, None])[:, :, 0]
+    return y if b is None else y + b[group]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_forward_mode_is_refused(plain, which):
+    # not implemented, as for the rasterizer and the projection: an error, not a tangent of zeros
+    off, *args = _inputs(needs=(False, False, False))
+    with forward_ad.dual_level():
+        args[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            dmr.grouped_linear(args[0], off, args[1], args[2])
+        # no tangent among the arguments: as ever
+        _, x, w, b = _inputs(needs=(False, False, False))
+        torch.testing.assert_close(dmr.grouped_linear(x, off, w, b), _formula(x, off, w, b))
+
+
+def test_forward_mode_transforms_are_refused(plain):
+    off, x, w, b = _inputs(needs=(False, False, False))
+    with pytest.raises((RuntimeError, NotImplementedError)):
+        torch.func.jvp(lambda v: dmr.grouped_linear(v, off, w, b), (x,), (torch.ones_like(x),))
+    with torch.no_grad(), forward_ad.dual_level():
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            dmr.grouped_linear(forward_ad.make_dual(x, torch.ones_like(x)), off, w, b)
