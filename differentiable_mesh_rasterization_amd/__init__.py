@@ -697,17 +697,56 @@ class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         x, row_offsets, weight = ctx.saved_tensors
-        N, cout, cin = weight.shape
         need_x, _, need_w, need_b = ctx.needs_input_grad
-        gx = torch.empty_like(x) if need_x else None
-        gw = torch.empty_like(weight) if need_w else None
-        gb = torch.empty((N, cout), dtype=weight.dtype, device=weight.device) if need_b else None
-        ws = None
-        if need_w or need_b:
-            ws = torch.empty(dmr_grouped_linear_workspace_size(x.shape[0], N, cin, cout, x.dtype), dtype=torch.uint8,
-                             device=x.device)
-        dmr_grouped_linear_bwd(x, row_offsets, weight, g.contiguous(), gx, gw, gb, ws)
+        grads = _GroupedLinearGrads.apply if torch.is_grad_enabled() else _grouped_grads   # create_graph, or not
+        gx, gw, gb = grads(x, row_offsets, weight, g.contiguous(), (need_x, need_w, need_b))
         return gx, None, gw, gb
+
+
+def _grouped_grads(x, row_offsets, weight, g, needs):
+    N, cout, cin = weight.shape
+    gx = torch.empty_like(x) if needs[0] else None
+    gw = torch.empty_like(weight) if needs[1] else None
+    gb = torch.empty((N, cout), dtype=weight.dtype, device=weight.device) if needs[2] else None
+    ws = None
+    if needs[1] or needs[2]:
+        ws = torch.empty(dmr_grouped_linear_workspace_size(x.shape[0], N, cin, cout, x.dtype), dtype=torch.uint8,
+                         device=x.device)
+    dmr_grouped_linear_bwd(x, row_offsets, weight, g, gx, gw, gb, ws)
+    return gx, gw, gb
+
+
+class _GroupedLinearGrads(torch.autograd.Function):
+    """The layer's backward pass as a function of x, weight and grad_y: each
+    result is a product of two of them (or a sum of grad_y), so its own
+    gradients are the layer's three products again."""
+
+    @staticmethod
+    def forward(ctx, x, row_offsets, weight, g, needs):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, row_offsets, weight, g)
+        return _grouped_grads(x, row_offsets, weight, g, needs)
+
+    @staticmethod
+    def backward(ctx, hx, hw, hb):
+        x, off, weight, g = ctx.saved_tensors
+        hx, hw, hb = (None if h is None else h.contiguous() for h in (hx, hw, hb))
+        need_x, _, need_w, need_g, _ = ctx.needs_input_grad
+        grads = _GroupedLinearGrads.apply if torch.is_grad_enabled() else _grouped_grads
+        # grad_x_r = W_n^T g_r, grad_W_n = sum_r g_r x_r^T, grad_b_n = sum_r g_r
+        dx = grads(x, off, hw, g, (True, False, False))[0] if need_x and hw is not None else None
+        dw = grads(hx, off, weight, g, (False, True, False))[1] if need_w and hx is not None else None
+        dg = None
+        if need_g:
+            parts, bias = [], hb
+            for rows, w in ((hx, weight), (x, hw)):
+                if rows is not None and w is not None:
+                    parts.append(grouped_linear(rows, off, w, bias))
+                    bias = None
+            if bias is not None:
+                parts.append(grouped_linear(g.new_ones((g.shape[0], 1)), off, bias.unsqueeze(2)))   # b_n for every row
+            dg = sum(parts[1:], parts[0]) if parts else None
+        return dx, None, dw, dg, None
 
 
 def grouped_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor,
@@ -715,8 +754,8 @@ def grouped_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Ten
     """y_r = W_n x_r + b_n for the rows r of every group n (a mesh's
     vertices, an image's pixels): x [R, in], row_offsets [N + 1] int64,
     weight [N, out, in], bias [N, out], all of one type (float32, float16 or
-    bfloat16). Differentiable with respect to x, weight and bias (in reverse
-    mode; forward mode raises)."""
+    bfloat16). Differentiable any number of times with respect to x, weight and
+    bias (in reverse mode; forward mode raises)."""
     if forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
             x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
         return _GroupedLinear.apply(x, row_offsets, weight, bias)

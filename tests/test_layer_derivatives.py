@@ -69,3 +69,43 @@ def test_forward_mode_transforms_are_refused(plain):
     with torch.no_grad(), forward_ad.dual_level():
         with pytest.raises((RuntimeError, NotImplementedError)):
             dmr.grouped_linear(forward_ad.make_dual(x, torch.ones_like(x)), off, w, b)
+
+
+@pytest.mark.parametrize("needs", [(True, True, True), (True, False, False), (False, True, False), (False, False, True),
+                                   (False, True, True), (True, False, True)])
+def test_first_and_second_derivatives_are_the_differences(plain, needs):
+    off, x, w, b = _inputs(needs=needs)
+    leaves = [t for t in (x, w, b) if t.requires_grad]
+    assert torch.autograd.gradcheck(lambda *a: dmr.grouped_linear(x, off, w, b), leaves)
+    if needs != (False, False, True):     # linear in the bias alone: nothing is left to differentiate
+        assert torch.autograd.gradgradcheck(lambda *a: dmr.grouped_linear(x, off, w, b), leaves)
+
+
+def test_a_penalty_on_the_gradients(plain):
+    # of each gradient alone, of all, and of the gradients' gradients
+    def run(layer):
+        off, x, w, b = _inputs()
+        out = []
+        y = torch.tanh(layer(x, off, w, b))
+        grads = torch.autograd.grad((y ** 2).sum(), (x, w, b), create_graph=True)
+        for some in ([0], [1], [2], [0, 1, 2]):
+            loss = sum((grads[k] ** 3).sum() for k in some)
+            second = torch.autograd.grad(loss, (x, w, b), create_graph=True)
+            out += list(second)
+            out += list(torch.autograd.grad(sum((s ** 2).sum() for s in second), (x, w, b), retain_graph=True))
+        return out
+
+    for got, want in zip(run(dmr.grouped_linear), run(_formula)):
+        torch.testing.assert_close(got, want, rtol=1e-10, atol=1e-10)
+
+
+def test_a_gradient_through_upstream_gradients_only(plain):
+    # the backward pass differentiated with respect to grad_y alone, by each of its results
+    off, x, w, b = _inputs()
+    g = torch.randn(sum(SIZES), 3, dtype=torch.float64, requires_grad=True)
+    grads = torch.autograd.grad(dmr.grouped_linear(x, off, w, b), (x, w, b), g, create_graph=True)
+    want = torch.autograd.grad(_formula(x, off, w, b), (x, w, b), g, create_graph=True)
+    for a, c in zip(grads, want):
+        assert a.requires_grad
+        torch.testing.assert_close(torch.autograd.grad((a ** 2).sum(), g, retain_graph=True)[0],
+                                   torch.autograd.grad((c ** 2).sum(), g, retain_graph=True)[0], rtol=1e-10, atol=1e-10)
