@@ -426,6 +426,9 @@ hipError_t launch_points_forward(const FwdArgs& a);
 hipError_t launch_points_backward(const PointBwdArgs& a);
 hipError_t launch_project_backward(const ProjectArgs& a);
 
+// Work-items that one launch holds.
+constexpr int64_t kMaxWorkItems = 0xFFFFFFFFll;
+
 struct GroupedLinearArgs {
     const void* x; int64_t R; int32_t cin;
     const int64_t* off; int64_t N;

@@ -543,6 +543,7 @@ hipError_t allow_lds(Kernel kernel, int bytes) {
 
 template <class T, class Square, class Update>
 hipError_t launch_steps(const OrthogonalizeArgs& a, const Layout& w) {
+    static_assert(Square::THREADS <= 512 && Update::THREADS <= 512, "orthogonalize_workspace counts on it");
     auto half = [&](int64_t o) { return reinterpret_cast<h16*>(a.workspace + o); };
     auto real = [&](int64_t o) { return reinterpret_cast<float*>(a.workspace + o); };
     const int* lift = reinterpret_cast<const int*>(a.workspace + w.lift);
@@ -603,28 +604,34 @@ hipError_t launch_tiled(const OrthogonalizeArgs& a) {
     return launch_steps<T, PairProduct<64, 64, 2, 4, true, 8>, PairProduct<64, 64, 2, 4, false, 8>>(a, w);
 }
 
+// Threads of a small matrix's workgroup.
+int small_threads(const SmallShape& h) {
+    const int st = h.sp / 16;
+    return st * (h.lp / 16) <= 16 && st * (st + 1) / 2 <= 4 ? 256 : kSmallThreads;
+}
+
 template <class T>
 hipError_t launch_small(const OrthogonalizeArgs& a) {
     const SmallShape h = small_shape(a.m, a.n);
-    const int st = h.sp / 16;
-    const bool few = st * (h.lp / 16) <= 16 && st * (st + 1) / 2 <= 4;
-    const auto kernel = few ? orthogonalize_small<T, 256> : orthogonalize_small<T, kSmallThreads>;
+    const int threads = small_threads(h);
+    const auto kernel = threads == 256 ? orthogonalize_small<T, 256> : orthogonalize_small<T, kSmallThreads>;
     const hipError_t err = allow_lds(kernel, (int)h.bytes);
     if (err != hipSuccess) return err;
-    kernel<<<(unsigned)a.B, few ? 256 : kSmallThreads, h.bytes, a.stream>>>(static_cast<const T*>(a.update), a.m, a.n, a.steps,
-                                                                           a.eps, static_cast<T*>(a.out));
+    kernel<<<(unsigned)a.B, threads, h.bytes, a.stream>>>(static_cast<const T*>(a.update), a.m, a.n, a.steps, a.eps,
+                                                          static_cast<T*>(a.out));
     return hipGetLastError();
 }
 
 }  // namespace
 
 size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n) {
-    if (is_small(m, n)) return B <= INT32_MAX ? 256 : 0;
+    if (is_small(m, n)) return B <= kMaxWorkItems / small_threads(small_shape(m, n)) ? 256 : 0;
     const Layout one = layout(1, m, n);
-    // one workgroup for every 64 x 64 tile, 31 bits of them; plane sizes in 63 bits
-    const int64_t xs = (int64_t)one.sp * one.lp;
-    const int64_t tiles = (xs / 4096 > kNormBlocks ? xs / 4096 : kNormBlocks);
-    if (tiles > INT32_MAX || B > INT32_MAX / tiles) return 0;
+    // the norm takes kNormBlocks workgroups of 256 for a matrix, the products
+    // one of 512 for a 64 x 64 tile (of larger tiles there are fewer), their
+    // number rounded up to 8
+    const int64_t tiles = (int64_t)(one.sp / 64) * (one.lp / 64);
+    if (B > kMaxWorkItems / (kNormBlocks * 256) || B > (kMaxWorkItems / 512 - 7) / tiles) return 0;
     return layout(B, m, n).bytes;
 }
 
