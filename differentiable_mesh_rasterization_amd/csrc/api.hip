@@ -500,7 +500,9 @@ dmr_status dmr_grouped_linear_fwd(const void* x, int64_t R, int32_t in_features,
 
 size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype) {
     static const int64_t none = 0;
-    if (check_grouped(R, in_features, N, out_features, dtype, &none) != DMR_SUCCESS) return 0;
+    if (check_grouped(R, in_features, N, out_features, dtype, &none) != DMR_SUCCESS ||
+        !grouped_sums_fit(R, N, in_features, out_features, dtype != DMR_FLOAT32))
+        return 0;
     const int64_t slots = grouped_pieces(R, N, in_features, out_features, dtype != DMR_FLOAT32).slots;
     return align_up((size_t)(slots * grouped_piece_values(in_features, out_features)) * sizeof(float) + 256, 256);
 }
@@ -516,6 +518,7 @@ dmr_status dmr_grouped_linear_bwd(const void* x, int64_t R, int32_t in_features,
     if (R > 0 && ((grad_x && !weight) || (sums && !x))) return DMR_ERROR_INVALID_VALUE;
     if (N == 0 || !(grad_x || sums)) return DMR_SUCCESS;
     if (sums) {
+        if (!grouped_sums_fit(R, N, in_features, out_features, dtype != DMR_FLOAT32)) return DMR_ERROR_UNSUPPORTED;
         if (workspace == nullptr ||
             workspace_bytes < dmr_grouped_linear_workspace_size(R, N, in_features, out_features, dtype))
             return DMR_ERROR_WORKSPACE_TOO_SMALL;

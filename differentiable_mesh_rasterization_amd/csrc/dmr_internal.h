@@ -446,6 +446,8 @@ struct GroupedPieces {
     int64_t slots;
 };
 GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half);
+// Whether launches hold the sums over rows (gradients of weights and biases).
+bool grouped_sums_fit(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half);
 // Values of a slot: the weight's, then the bias's, padded to 16 bytes.
 __host__ __device__ __forceinline__ int64_t grouped_piece_values(int32_t cin, int32_t cout) {
     return ((int64_t)cin * cout + cout + 3) / 4 * 4;

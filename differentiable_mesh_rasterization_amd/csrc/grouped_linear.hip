@@ -613,6 +613,13 @@ bool launch_together(const GroupedLinearArgs& a, const GroupedPieces& p, bool ve
     return true;
 }
 
+// How a group's values are shared out when its pieces are added.
+bool add_split(int64_t values) { return values <= 65536; }
+int64_t add_blocks(int64_t values) {
+    const int64_t each = add_split(values) ? kAddValues<true> : kAddValues<false>;
+    return (values + each - 1) / each;
+}
+
 template <class T>
 hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
     const T* bias = static_cast<const T*>(a.bias);
@@ -648,19 +655,12 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
                                : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, true>>(a, p, vec_weights,
                                                                                                              wide_w);
         if (err == hipSuccess && p.slots > 0) {
-            const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout;
-            const bool split = values <= 65536;
-            const int64_t blocks = split ? (values + kAddValues<true> - 1) / kAddValues<true>
-                                         : (values + kAddValues<false> - 1) / kAddValues<false>;
-            if (blocks * a.N > INT32_MAX) {
-                err = hipErrorInvalidValue;
-            } else {
-                const auto add = split ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
-                add<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
-                    a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), size, a.workspace, p.slots,
-                    (unsigned)blocks, static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
-                err = hipGetLastError();
-            }
+            const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout, blocks = add_blocks(values);
+            const auto add = add_split(values) ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
+            add<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
+                a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), size, a.workspace, p.slots,
+                (unsigned)blocks, static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
+            err = hipGetLastError();
         }
     }
     timing_end(kKGroupedLinearBwd, a.stream);
@@ -696,6 +696,15 @@ GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bo
     rows = rows < 512 ? 512 : rows > 8192 ? 8192 : rows;
     if (R <= 1024) rows = 1024;   // short enough to need no second launch
     return {(int)rows, (int)side, R > rows ? 2 * (R / rows) : 0};
+}
+
+bool grouped_sums_fit(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half) {
+    const GroupedPieces p = grouped_pieces(R, N, cin, cout, half);
+    // unaligned arrays take tiles of 128 where others take 256
+    const int side = p.side == 256 ? 128 : p.side;
+    const int64_t items = (R / p.rows + N) * ceil_div(cin, side) * ceil_div(cout, side), round = 8 * kPieceRun;
+    if ((items + round - 1) / round * round > kMaxWorkItems / 256) return false;
+    return p.slots == 0 || add_blocks((int64_t)cin * cout + cout) * N <= kMaxWorkItems / 256;
 }
 
 hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a) { return launch_typed(a, false); }

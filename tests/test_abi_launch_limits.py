@@ -8,7 +8,7 @@ import os
 import pytest
 import torch
 
-INVALID, WS_SMALL, UNSUPPORTED = 1, 2, 4
+WS_SMALL, UNSUPPORTED = 2, 4
 P = ctypes.c_void_p
 F = 0x1000   # never dereferenced: validation fails first
 
@@ -31,3 +31,23 @@ def test_updates_past_a_launch_are_refused(dmr, B, m, n):
     assert dmr.dmr_orthogonalize_workspace_size(B, m, n, torch.float32) == 0
     assert dmr.lib().dmr_orthogonalize(P(F), B, m, n, 0, 5, 1e-7, P(F), P(F), 1 << 62, None) == UNSUPPORTED
     assert dmr.dmr_orthogonalize_workspace_size(B - B // 16 - 1 if B > 16 else B - 1, m, n, torch.float32) > 0
+
+
+# groups whose weights' gradients take a workgroup of 256 each, 16 each, and
+# whose pieces are added by 17 workgroups of 256 each; and fewer of them
+@pytest.mark.parametrize("R,N,cin,cout,dtype,fewer", [(10, 1 << 24, 1, 1, torch.float32, (1 << 24) - 64),
+                                                      (1 << 29, 1 << 21, 512, 512, torch.bfloat16, 1 << 17),
+                                                      (1 << 21, 1 << 20, 64, 64, torch.float32, 1 << 19)])
+def test_sums_over_rows_past_a_launch_are_refused(dmr, R, N, cin, cout, dtype, fewer):
+    size, code = dmr.dmr_grouped_linear_workspace_size, dmr.DTYPES[dtype]
+    backward = dmr.lib().dmr_grouped_linear_bwd
+    assert size(R, N, cin, cout, dtype) == 0
+    for gx, gw, gb in ((F, F, F), (None, F, None), (None, None, F)):
+        assert backward(P(F), R, cin, P(F), N, P(F), cout, code, P(F), P(gx), P(gw), P(gb), P(F), 1 << 62, None) == UNSUPPORTED
+    assert size(R, fewer, cin, cout, dtype) > 0
+
+
+def test_rows_of_as_many_groups_are_not_refused(dmr):
+    # the rows' gradient walks its tiles, whatever their number: only the workspace of the sums is missing
+    backward = dmr.lib().dmr_grouped_linear_bwd
+    assert backward(P(F), 10, 1, P(F), (1 << 24) - 64, P(F), 1, 0, P(F), P(F), P(F), None, P(F), 16, None) == WS_SMALL
