@@ -44,7 +44,7 @@ EXPORTED = [
     "dmr_reset_kernel_timing", "dmr_blend_fwd", "dmr_blend_bwd", "dmr_project_fwd", "dmr_project_bwd",
     "rasterize_points_fwd", "rasterize_points_bwd", "dmr_points_workspace_min_size", "dmr_points_workspace_size_hint",
     "rasterize_meshes_fwd_noalloc", "dmr_grouped_linear_fwd", "dmr_grouped_linear_bwd", "dmr_grouped_linear_workspace_size",
-    "dmr_orthogonalize", "dmr_orthogonalize_workspace_size",
+    "dmr_grouped_linear_plan", "dmr_orthogonalize", "dmr_orthogonalize_workspace_size", "dmr_orthogonalize_tile",
 ]
 DMR_NOALLOC_SCRATCH_BYTES = 128 << 20
 DMR_MAX_LINEAR_WIDTH = 1 << 20
@@ -68,6 +68,11 @@ class dmr_stats(ctypes.Structure):
                 ("bin_capacity", ctypes.c_int64), ("bins", ctypes.c_int64),
                 ("overflow_bins", ctypes.c_int64), ("live_faces", ctypes.c_int64),
                 ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class dmr_linear_plan(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("y_columns", "y_rows", "grad_x_columns", "grad_x_rows", "grad_weight_side",
+                                              "piece_rows", "together")]
 
 
 _lib = None
@@ -137,6 +142,10 @@ def lib(path: Optional[str] = None):
     L.dmr_grouped_linear_bwd.argtypes = [P, I64, I32, P, I64, P, I32, ctypes.c_int, P, P, P, P, P, SZ, P]
     L.dmr_grouped_linear_workspace_size.restype = SZ
     L.dmr_grouped_linear_workspace_size.argtypes = [I64, I64, I32, I32, ctypes.c_int]
+    L.dmr_grouped_linear_plan.restype = ctypes.c_int
+    L.dmr_grouped_linear_plan.argtypes = [I64, I64, I32, I32, ctypes.c_int, I32, P]
+    L.dmr_orthogonalize_tile.restype = I32
+    L.dmr_orthogonalize_tile.argtypes = [I64, I32, I32]
     L.dmr_orthogonalize.restype = ctypes.c_int
     L.dmr_orthogonalize.argtypes = [P, I64, I32, I32, ctypes.c_int, I32, ctypes.c_float, P, P, SZ, P]
     L.dmr_orthogonalize_workspace_size.restype = SZ
@@ -512,6 +521,21 @@ def dmr_grouped_linear_bwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: t
                                       _address(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(dev))
     if rc != 0:
         raise DmrError("dmr_grouped_linear_bwd", rc)
+
+
+def dmr_grouped_linear_plan(R: int, N: int, in_features: int, out_features: int, dtype: torch.dtype,
+                            aligned: bool = True) -> dict:
+    """What calls of these sizes are computed by (include/dmr.h)."""
+    plan = dmr_linear_plan()
+    rc = lib().dmr_grouped_linear_plan(R, N, in_features, out_features, DTYPES.get(dtype, -1), int(aligned),
+                                       ctypes.byref(plan))
+    if rc != 0:
+        raise DmrError("dmr_grouped_linear_plan", rc)
+    return {f: getattr(plan, f) for f, _ in dmr_linear_plan._fields_}
+
+
+def dmr_orthogonalize_tile(B: int, m: int, n: int) -> int:
+    return int(lib().dmr_orthogonalize_tile(B, m, n))
 
 
 def dmr_orthogonalize_workspace_size(B: int, m: int, n: int, dtype: torch.dtype) -> int:

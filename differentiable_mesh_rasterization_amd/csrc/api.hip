@@ -507,6 +507,23 @@ size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_featur
     return align_up((size_t)(slots * grouped_piece_values(in_features, out_features)) * sizeof(float) + 256, 256);
 }
 
+dmr_status dmr_grouped_linear_plan(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype,
+                                   int32_t aligned, dmr_linear_plan* out) {
+    static const int64_t none = 0;
+    if (out == nullptr) return DMR_ERROR_INVALID_VALUE;
+    const dmr_status st = check_grouped(R, in_features, N, out_features, dtype, &none);
+    if (st != DMR_SUCCESS) return st;
+    const bool half = dtype != DMR_FLOAT32;
+    const int whole = half ? 8 : 4;
+    const bool vec = aligned && in_features % whole == 0 && out_features % whole == 0;
+    const RowsTile y = grouped_rows_tile(R, N, out_features, half, false, aligned && in_features % whole == 0);
+    const RowsTile gx = grouped_rows_tile(R, N, in_features, half, true, vec);
+    const GroupedPieces p = grouped_pieces(R, N, in_features, out_features, half);
+    *out = {y.columns, y.rows, gx.columns, gx.rows, grouped_weight_side(p, vec), p.rows,
+            grouped_together(R, N, in_features, out_features, half)};
+    return DMR_SUCCESS;
+}
+
 dmr_status dmr_grouped_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
                                   const void* weight, int32_t out_features, dmr_dtype dtype, const void* grad_y,
                                   void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
@@ -546,6 +563,11 @@ dmr_status check_orthogonalize(int64_t B, int32_t m, int32_t n, dmr_dtype dtype)
 size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dtype dtype) {
     if (check_orthogonalize(B, m, n, dtype) != DMR_SUCCESS) return 0;
     return B > 0 ? orthogonalize_workspace(B, m, n) : 256;
+}
+
+int32_t dmr_orthogonalize_tile(int64_t B, int32_t m, int32_t n) {
+    if (B < 1 || check_orthogonalize(B, m, n, DMR_FLOAT32) != DMR_SUCCESS) return -1;
+    return orthogonalize_tile(B, m, n);
 }
 
 dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n, dmr_dtype dtype, int32_t steps, float eps,

@@ -446,6 +446,14 @@ struct GroupedPieces {
     int64_t slots;
 };
 GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half);
+int grouped_weight_side(const GroupedPieces& p, bool vec);   // of the tiles that a call takes
+// The tile that rows of `n_out` values are computed by (backward: the rows'
+// gradient). vec: arrays and widths take 16-byte loads.
+struct RowsTile {
+    int columns, rows;
+};
+RowsTile grouped_rows_tile(int64_t R, int64_t N, int32_t n_out, bool half, bool backward, bool vec);
+bool grouped_together(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half);
 // Whether launches hold the sums over rows (gradients of weights and biases).
 bool grouped_sums_fit(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half);
 // Values of a slot: the weight's, then the bias's, padded to 16 bytes.
@@ -463,6 +471,7 @@ struct OrthogonalizeArgs {
     hipStream_t stream;
 };
 size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n);   // 0: too large
+int orthogonalize_tile(int64_t B, int32_t m, int32_t n);   // the side of the tiles of X; 0: one workgroup for a matrix
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a);
 
 // Timing hooks (api.hip).

@@ -519,32 +519,24 @@ hipError_t launch_rows_tile(const GroupedLinearArgs& a, const T* in, int k_in, c
     return hipGetLastError();
 }
 
-// The tile by the widths and by how many there are: the larger, the fewer
-// bytes for a product, but they have to fill 256 compute units. (bfloat16,
-// forward: 2048 rows of 512 to 512, 19.3 us with 256 x 256 tiles, 11.0 with
-// 128 x 128, 9.4 with 64 x 128; 8192 of 1024 to 1024, 128 tiles of 256 x 256,
-// 35.3 and 31.5 with 128 x 128, but the backward's transposed weight 103 and
-// 117. 2^20 rows of 64 to 64: 60 us with 64 x 256, 63 with 64 x 128. 217632 rows
-// of 64 to 3 in float32: 17.7 us with 16 x 256, 14.3 with 16 x 128.)
 template <class T, bool WK>
 hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const T* bias, T* out, int n_out, bool vec,
                        bool wide) {
-    const auto tiles = [&](int bn, int bm) { return (a.R / bm + 1) * ceil_div(n_out, bn); };
-    if (a.R <= 16 * a.N)
+    const RowsTile t = grouped_rows_tile(a.R, a.N, n_out, sizeof(T) == 2, !WK, vec);
+    if (t.rows == 16)
         return launch_rows_tile<T, TileProduct<T, 64, 16, 4, 1, WK, true, 4>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
-    if (n_out <= 16)
+    if (t.columns == 16)
         return launch_rows_tile<T, TileProduct<T, 16, 128, 1, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
-    if (n_out <= 64 || tiles(128, 128) < 256) {
-        if constexpr (sizeof(T) == 2)
-            if (tiles(64, 256) >= 256)
-                return launch_rows_tile<T, TileProduct<T, 64, 256, 1, 8, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
-                                                                                             wide);
-        return launch_rows_tile<T, TileProduct<T, 64, 128, 1, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
-    }
-    if constexpr (sizeof(T) == 2)
-        if (vec && n_out > 128 && a.R >= 512 * a.N && tiles(256, 256) >= (WK ? 224 : 112))
+    if constexpr (sizeof(T) == 2) {
+        if (t.columns == 64 && t.rows == 256)
+            return launch_rows_tile<T, TileProduct<T, 64, 256, 1, 8, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
+                                                                                         wide);
+        if (t.columns == 256)
             return launch_rows_tile<T, TileProduct<T, 256, 256, 4, 2, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec,
                                                                                            wide);
+    }
+    if (t.columns == 64)
+        return launch_rows_tile<T, TileProduct<T, 64, 128, 1, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
     return launch_rows_tile<T, TileProduct<T, 128, 128, 2, 4, WK, true, 2>, WK>(a, in, k_in, bias, out, n_out, vec, wide);
 }
 
@@ -583,27 +575,14 @@ hipError_t launch_both(const GroupedLinearArgs& a, const GroupedPieces& p, bool 
     return hipGetLastError();
 }
 
-// Both gradients in one launch where small tiles serve both: narrow layers,
-// and calls of so few tiles that one gradient's leave the device unfilled.
-// What one waits for, the other fills, and the upstream gradients are read
-// while they are near. false: not such a call. (One launch against two, us.
-// Float32: 217632 rows of 64 to 64, 53 and 64, of 16 to 256, 100 and 172;
-// 8192 of 256 to 256, 37 and 70; 2048 of 1024 to 1024, 1552 tiles, 115 and
-// 94. 16 bits: 1003 rows of 37 to 19, 15.9 and 20.7; 2^20 of 64 to 64, 120
-// and 129; 8192 of 256 to 256, 18.4 and 30.8; 16384 of 256 to 512, 2112
-// tiles, 41 and 49; 64 groups of one row, 1024 to 1024, 16384 tiles, 187 and
-// 118; 166428 rows of 240 to 64, 61 and 66, but 400000 of 512 to 64, 276 and
-// 261.)
+// false: the two are not launched together.
 template <class T>
 bool launch_together(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide_x, bool wide_w, hipError_t& err) {
-    constexpr int64_t kFew = sizeof(T) == 4 ? 1536 : 2304;
-    const bool narrow = a.cin <= 64 || (a.cin <= 256 && a.cout <= 64);
-    const int side = SmallWeightTile<T>::BN;
-    if (!a.grad_x || a.R == 0) return false;
+    if (!a.grad_x || !grouped_together(a.R, a.N, a.cin, a.cout, sizeof(T) == 2)) return false;
     const bool few_rows = a.R <= 16 * a.N;
+    const int side = SmallWeightTile<T>::BN;
     const int64_t row_tiles = most_row_tiles(a.R, a.N, few_rows ? 16 : 128) * ceil_div(a.cin, 64);
     const int64_t items = (a.R / p.rows + a.N) * ceil_div(a.cin, side) * ceil_div(a.cout, side);
-    if ((row_tiles + items > kFew && !narrow) || row_tiles + items > 1 << 23) return false;
     if (few_rows)
         err = launch_both<T, TileProduct<T, 64, 16, 4, 1, false, true, 4>>(a, p, vec, wide_x, wide_w, row_tiles, items);
     else if (a.cin <= 16)
@@ -644,16 +623,17 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
         err = launch_rows<T, false>(a, static_cast<const T*>(a.grad_y), a.cout, (const T*)nullptr, static_cast<T*>(a.grad_x),
                                     a.cin, vec_rows, wide_x);
     if (err == hipSuccess && weights) {
+        const int side = grouped_weight_side(p, vec_weights);
         bool done = together;
         if constexpr (sizeof(T) == 2)
-            if (!done && p.side == 256 && vec_weights) {
+            if (!done && side == 256) {
                 err = launch_weight_tile<T, TileProduct<T, 256, 256, 2, 4, false, false, 2, true>>(a, p, true, wide_w);
                 done = true;
             }
         if (!done)
-            err = p.side == 64 ? launch_weight_tile<T, SmallWeightTile<T>>(a, p, vec_weights, wide_w)
-                               : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, true>>(a, p, vec_weights,
-                                                                                                             wide_w);
+            err = side == 64 ? launch_weight_tile<T, SmallWeightTile<T>>(a, p, vec_weights, wide_w)
+                             : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, true>>(a, p, vec_weights,
+                                                                                                           wide_w);
         if (err == hipSuccess && p.slots > 0) {
             const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout, blocks = add_blocks(values);
             const auto add = add_split(values) ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
@@ -698,10 +678,48 @@ GroupedPieces grouped_pieces(int64_t R, int64_t N, int32_t cin, int32_t cout, bo
     return {(int)rows, (int)side, R > rows ? 2 * (R / rows) : 0};
 }
 
+// The largest tiles have no form for arrays that are not aligned.
+int grouped_weight_side(const GroupedPieces& p, bool vec) { return p.side == 256 && !vec ? 128 : p.side; }
+
+// The tile by the widths and by how many there are: the larger, the fewer
+// bytes for a product, but they have to fill 256 compute units. (bfloat16,
+// forward: 2048 rows of 512 to 512, 19.3 us with 256 x 256 tiles, 11.0 with
+// 128 x 128, 9.4 with 64 x 128; 8192 of 1024 to 1024, 128 tiles of 256 x 256,
+// 35.3 and 31.5 with 128 x 128, but the backward's transposed weight 103 and
+// 117. 2^20 rows of 64 to 64: 60 us with 64 x 256, 63 with 64 x 128. 217632 rows
+// of 64 to 3 in float32: 17.7 us with 16 x 256, 14.3 with 16 x 128.)
+RowsTile grouped_rows_tile(int64_t R, int64_t N, int32_t n_out, bool half, bool backward, bool vec) {
+    const auto tiles = [&](int bn, int bm) { return (R / bm + 1) * ceil_div(n_out, bn); };
+    if (R <= 16 * N) return {64, 16};
+    if (n_out <= 16) return {16, 128};
+    if (n_out <= 64 || tiles(128, 128) < 256) return half && tiles(64, 256) >= 256 ? RowsTile{64, 256} : RowsTile{64, 128};
+    if (half && vec && n_out > 128 && R >= 512 * N && tiles(256, 256) >= (backward ? 112 : 224)) return {256, 256};
+    return {128, 128};
+}
+
+// Both gradients in one launch where small tiles serve both: narrow layers,
+// and calls of so few tiles that one gradient's leave the device unfilled.
+// What one waits for, the other fills, and the upstream gradients are read
+// while they are near. (One launch against two, us.
+// Float32: 217632 rows of 64 to 64, 53 and 64, of 16 to 256, 100 and 172;
+// 8192 of 256 to 256, 37 and 70; 2048 of 1024 to 1024, 1552 tiles, 115 and
+// 94. 16 bits: 1003 rows of 37 to 19, 15.9 and 20.7; 2^20 of 64 to 64, 120
+// and 129; 8192 of 256 to 256, 18.4 and 30.8; 16384 of 256 to 512, 2112
+// tiles, 41 and 49; 64 groups of one row, 1024 to 1024, 16384 tiles, 187 and
+// 118; 166428 rows of 240 to 64, 61 and 66, but 400000 of 512 to 64, 276 and
+// 261.)
+bool grouped_together(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half) {
+    if (R == 0) return false;
+    const int64_t few = half ? 2304 : 1536;
+    const bool narrow = cin <= 64 || (cin <= 256 && cout <= 64);
+    const int64_t row_tiles = most_row_tiles(R, N, R <= 16 * N ? 16 : 128) * ceil_div(cin, 64);
+    const int64_t items = (R / grouped_pieces(R, N, cin, cout, half).rows + N) * ceil_div(cin, 64) * ceil_div(cout, 64);
+    return (row_tiles + items <= few || narrow) && row_tiles + items <= 1 << 23;
+}
+
 bool grouped_sums_fit(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half) {
     const GroupedPieces p = grouped_pieces(R, N, cin, cout, half);
-    // unaligned arrays take tiles of 128 where others take 256
-    const int side = p.side == 256 ? 128 : p.side;
+    const int side = grouped_weight_side(p, false);   // of the tiles that are more
     const int64_t items = (R / p.rows + N) * ceil_div(cin, side) * ceil_div(cout, side), round = 8 * kPieceRun;
     if ((items + round - 1) / round * round > kMaxWorkItems / 256) return false;
     return p.slots == 0 || add_blocks((int64_t)cin * cout + cout) * N <= kMaxWorkItems / 256;

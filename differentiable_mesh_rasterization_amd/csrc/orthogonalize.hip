@@ -529,10 +529,17 @@ __global__ __launch_bounds__(Tile::THREADS) void orthogonalize_update(
     }
 }
 
-// The tiles of X that make larger tiles worth while: about one for each of the
-// 256 compute units (one 1024 x 2048 in float32, 128 tiles of 128 x 128: 549
-// us with them, 419 with 64 x 64; one 2048 x 2048, 256 of them: 814 and 1499).
-constexpr int64_t kBig = 224, kMid = 256;
+// The side of the tiles of X: larger ones are worth while where about one is
+// there for each of the 256 compute units (one 1024 x 2048 in float32, 128 tiles
+// of 128 x 128: 549 us with them, 419 with 64 x 64; one 2048 x 2048, 256 of them:
+// 814 and 1499), and 256 where they pad X by a quarter more than 128 at most (30
+// of 300 x 2000: 735 us with, 635 without). The squares' halves take 128 x 128
+// tiles with either (4 of 2048 x 2048: 143 us with 256 x 256, 123 with 128 x 128).
+int tile_side(int64_t B, const Layout& w) {
+    const auto count = [&](int t) { return B * ((w.sp + t - 1) / t) * ((w.lp + t - 1) / t); };
+    if (count(256) >= 224 && count(256) * 16 <= count(128) * 5) return 256;
+    return count(128) >= 256 ? 128 : 64;
+}
 
 template <class Kernel>
 hipError_t allow_lds(Kernel kernel, int bytes) {
@@ -591,17 +598,12 @@ hipError_t launch_tiled(const OrthogonalizeArgs& a) {
         reinterpret_cast<int*>(a.workspace + w.lift));
     err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const auto count = [&](int t) { return a.B * ((w.sp + t - 1) / t) * ((w.lp + t - 1) / t); };   // tiles of X
-    // X takes 256 x 256 tiles where they fill the device and pad it by a
-    // quarter more than 128 x 128 ones at most (30 of 300 x 2000 in float32:
-    // 735 us with, 635 without). The squares' halves take 128 x 128 tiles
-    // throughout (4 of 2048 x 2048 in float32: 143 us with 256 x 256, 123 with
-    // 128 x 128).
     typedef PairProduct<128, 128, 2, 4, true, 2> Square;
-    if (count(256) >= kBig && count(256) * 16 <= count(128) * 5)
-        return launch_steps<T, Square, PairProduct<256, 256, 4, 2, false, 2>>(a, w);
-    if (count(128) >= kMid) return launch_steps<T, Square, PairProduct<128, 128, 2, 4, false, 2>>(a, w);
-    return launch_steps<T, PairProduct<64, 64, 2, 4, true, 8>, PairProduct<64, 64, 2, 4, false, 8>>(a, w);
+    switch (tile_side(a.B, w)) {
+        case 256: return launch_steps<T, Square, PairProduct<256, 256, 4, 2, false, 2>>(a, w);
+        case 128: return launch_steps<T, Square, PairProduct<128, 128, 2, 4, false, 2>>(a, w);
+        default: return launch_steps<T, PairProduct<64, 64, 2, 4, true, 8>, PairProduct<64, 64, 2, 4, false, 8>>(a, w);
+    }
 }
 
 // Threads of a small matrix's workgroup.
@@ -634,6 +636,8 @@ size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n) {
     if (B > kMaxWorkItems / (kNormBlocks * 256) || B > (kMaxWorkItems / 512 - 7) / tiles) return 0;
     return layout(B, m, n).bytes;
 }
+
+int orthogonalize_tile(int64_t B, int32_t m, int32_t n) { return is_small(m, n) ? 0 : tile_side(B, layout(B, m, n)); }
 
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a) {
     timing_begin(kKOrthogonalize, a.stream);

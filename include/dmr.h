@@ -380,6 +380,18 @@ dmr_status dmr_grouped_linear_bwd(const void* x, int64_t R, int32_t in_features,
 /* Workspace of dmr_grouped_linear_bwd in bytes; 0 on invalid arguments. */
 size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype);
 
+/* What calls of these sizes are computed by (for measurement and tests; the
+ * results do not depend on it but for the order of sums): the tile of y and of
+ * grad_x, in columns and rows, the side of the weight gradient's tile, the
+ * most rows of one of its pieces, and whether both gradients are computed in
+ * one launch (by tiles of at most 64 x 128 then). aligned: the arrays start
+ * on 16 bytes. */
+typedef struct dmr_linear_plan {
+    int32_t y_columns, y_rows, grad_x_columns, grad_x_rows, grad_weight_side, piece_rows, together;
+} dmr_linear_plan;
+dmr_status dmr_grouped_linear_plan(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype,
+                                   int32_t aligned, dmr_linear_plan* out);
+
 /*
  * Orthogonalised updates of B weight matrices (an optimiser's step for the
  * layers above): with U a matrix [m, n] of the batch,
@@ -403,6 +415,9 @@ size_t dmr_grouped_linear_workspace_size(int64_t R, int64_t N, int32_t in_featur
 #define DMR_MAX_ORTHOGONALIZE_STEPS 64
 dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n, dmr_dtype dtype, int32_t steps, float eps,
                              void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* The side of the tiles that X is computed by: 64, 128 or 256; 0: each matrix
+ * by one workgroup; -1 on invalid arguments. For measurement and tests. */
+int32_t dmr_orthogonalize_tile(int64_t B, int32_t m, int32_t n);
 /* Workspace of dmr_orthogonalize in bytes; 0 on invalid arguments. */
 size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dtype dtype);
 

@@ -51,3 +51,15 @@ def test_rows_of_as_many_groups_are_not_refused(dmr):
     # the rows' gradient walks its tiles, whatever their number: only the workspace of the sums is missing
     backward = dmr.lib().dmr_grouped_linear_bwd
     assert backward(P(F), 10, 1, P(F), (1 << 24) - 64, P(F), 1, 0, P(F), P(F), P(F), None, P(F), 16, None) == WS_SMALL
+
+
+def test_plans_refuse_what_the_calls_refuse(dmr):
+    plan, tile = dmr.dmr_grouped_linear_plan, dmr.dmr_orthogonalize_tile
+    assert plan(1 << 20, 4, 64, 64, torch.bfloat16)["y_rows"] == 256
+    for bad in ((-1, 2, 8, 4, torch.float32), (10, 0, 8, 4, torch.float32), (10, 2, 0, 4, torch.float32),
+                (10, 2, 8, 1 << 21, torch.float32), (10, 2, 8, 4, torch.float64)):
+        with pytest.raises(dmr.DmrError):
+            plan(*bad)
+    assert dmr.lib().dmr_grouped_linear_plan(10, 2, 8, 4, 0, 1, None) == 1
+    assert tile(4, 16, 16) == 0 and tile(1, 200, 300) == 64
+    assert tile(0, 16, 16) == tile(2, 0, 5) == tile(1 << 40, 200, 300) == -1
