@@ -20,7 +20,7 @@
 // on matrices of 64 to 2048 that gives 0.6 times the error of float32 products.
 // bfloat16 updates take the same products: with the high parts alone the error
 // of a 256 x 256 update of 32 strong directions over weak ones is 1.6e-3 of its
-// norm, as much as the rounding of the result; with pairs 1e-5.
+// norm, as much as the rounding of the result; with pairs 7e-6.
 #include "dmr_internal.h"
 #include "mfma_tile.h"
 
