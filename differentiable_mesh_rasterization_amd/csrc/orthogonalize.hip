@@ -41,6 +41,24 @@ __device__ __forceinline__ double scale_of(double norm, float eps, int up) {
     return __builtin_isfinite(norm) ? __builtin_ldexp(1.0, up) / (norm + (double)eps) : __builtin_nan("");
 }
 
+// X_0 has the norm t = |U| / (|U| + eps), which is tiny when |U| is far below
+// eps, and a step multiplies it by 3.4445 < 2^1.785 at most. So that float16
+// pairs (or float32) do not lose it below their range, X is held times a power
+// of two, the largest that keeps this bound below 1 (or 1): 2^lift_of for X_0,
+// 2^lift_at after `step` steps, brought down as X grows. A is put back to its
+// own scale.
+__device__ __forceinline__ int lift_of(double norm, float eps) {
+    const double t = norm / (norm + (double)eps);
+    if (!(t > 0.0)) return 0;   // zeros, or NaN
+    int e = 0;
+    (void)__builtin_frexp(t, &e);   // t < 2^e
+    return e < 0 ? -e : 0;
+}
+__device__ __forceinline__ int lift_at(int lift, int step) {
+    const int e = lift - (step * 1828 + 1023) / 1024;
+    return step > 0 ? (e > 0 ? e : 0) : lift;
+}
+
 // ---------------------------------------------------------------------------
 // matrices that fit into one workgroup's LDS: one workgroup each, one launch
 // ---------------------------------------------------------------------------
@@ -104,7 +122,9 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
     sum = 0.0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) sum += part[w];
-    const double inv = scale_of(sqrt(sum), eps, 0);
+    sum = sqrt(sum);
+    const int lift = __builtin_amdgcn_readfirstlane(lift_of(sum, eps));
+    const double inv = scale_of(sum, eps, lift);
     for (int i = tid; i < h.sp * h.ldx; i += THREADS) x[i] = (float)((double)x[i] * inv);
     __syncthreads();
 
@@ -115,6 +135,8 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
     const int tj = wave - ti * (ti + 1) / 2;
     const bool gram = wave < tri;
     for (int step = 0; step < steps; ++step) {
+        const int held = lift_at(lift, step);
+        const float back = __builtin_ldexpf(1.0f, -2 * held), down = __builtin_ldexpf(1.0f, lift_at(lift, step + 1) - held);
         f32x4 acc;
         for (int poly = 0; poly < 2; ++poly) {
             const float* from = poly ? a : x;
@@ -125,7 +147,8 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
                 const float* pi = from + (ti * 16 + r) * ld + 4 * q;
                 for (int k = 0; k < K; k += 16)
                     acc = mma<float>(*reinterpret_cast<const u32x4*>(pj + k), *reinterpret_cast<const u32x4*>(pi + k), acc);
-                if (poly)
+                if (!poly) acc *= back;
+                else
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[i] = kB * a[(ti * 16 + r) * h.lda + tj * 16 + 4 * q + i] + kC * acc[i];
             }
@@ -154,7 +177,7 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
                 c = mma<float>(p, *reinterpret_cast<const u32x4*>(a + (xi * 16 + r) * h.lda + k + 4 * q), c);
             }
             const f32x4 old = *reinterpret_cast<const f32x4*>(x + (xi * 16 + r) * h.ldx + xj * 16 + 4 * q);
-            next[u] = kA * old + c;
+            next[u] = (kA * old + c) * down;
         }
         __syncthreads();
 #pragma unroll
@@ -166,7 +189,7 @@ __global__ __launch_bounds__(THREADS) void orthogonalize_small(const T* __restri
         __syncthreads();
     }
     for (int i = tid; i < m * n; i += THREADS)
-        out[base + i] = (T)x[turned ? (i % n) * h.ldx + i / n : (i / n) * h.ldx + i % n];
+        out[base + i] = (T)__builtin_ldexpf(x[turned ? (i % n) * h.ldx + i / n : (i / n) * h.ldx + i % n], -lift_at(lift, steps));
 }
 
 // ---------------------------------------------------------------------------
@@ -222,23 +245,6 @@ __device__ __forceinline__ void split(float v, h16& hi, h16& lo) {
     asm("" : "+v"(v));
     hi = (h16)v;
     lo = (h16)(v - (float)hi);
-}
-
-// X_0 has the norm t = |U| / (|U| + eps), which is tiny when |U| is far below
-// eps, and a step multiplies it by 3.4445 < 2^1.785 at most. So that its float16
-// pairs do not lose it below their range, X is held times a power of two, the
-// largest that keeps this bound below 1 (or 1): 2^lift_of for X_0, 2^lift_at
-// after `step` steps, brought down as X grows. A is put back to its own scale.
-__device__ __forceinline__ int lift_of(double norm, float eps) {
-    const double t = norm / (norm + (double)eps);
-    if (!(t > 0.0)) return 0;   // zeros, or NaN
-    int e = 0;
-    (void)__builtin_frexp(t, &e);   // t < 2^e
-    return e < 0 ? -e : 0;
-}
-__device__ __forceinline__ int lift_at(int lift, int step) {
-    const int e = lift - (step * 1828 + 1023) / 1024;
-    return step > 0 ? (e > 0 ? e : 0) : lift;
 }
 
 // Sum of squares of a slice of each matrix (float64: no overflow, and the

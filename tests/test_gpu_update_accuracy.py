@@ -105,3 +105,16 @@ def test_update_of_matrices_of_different_norms(dmr, m, n):
 def test_update_of_subnormal_values_far_below_eps(dmr, m, n, steps):
     u, u64 = _typed(np.random.default_rng(7).normal(size=(1, m, n)) * 3e-43, "float32")
     check_update(dmr.orthogonalize(u, steps, 1.0), u64, "float32", steps, 1.0)
+
+
+@pytest.mark.parametrize("m,n", [(1, 1), (3, 64), (8, 12), (40, 30), (64, 400), (100, 260)])
+@pytest.mark.parametrize("norm,eps,steps", [(1e-40, 1.0, 40), (1e-30, 1e13, 40), (1e-2, 1e38, 25), (1e-43, 1e-3, 64)])
+def test_update_below_float32_of_eps_is_linear(dmr, m, n, norm, eps, steps):
+    # X_0 itself is below float32's normal values, the result, 3.4445^steps X_0, is not: a step rounds X to
+    # 22 bits or more and adds float32 values, 2^-20 together
+    eps = float(np.float32(eps))
+    u, u64 = _typed(np.random.default_rng(8).normal(size=(2, m, n)) * norm / np.sqrt(m * n), "float32")
+    got = dmr.orthogonalize(u, steps, eps).to(torch.float64).cpu().numpy()
+    ref = orthogonalize(u64, steps, eps)
+    for g, r in zip(got, ref):
+        assert np.linalg.norm(g - r) <= steps * 2.0 ** -20 * np.linalg.norm(r)
