@@ -13,19 +13,24 @@ libdmr.so is missing, every call raises.
     rasterize_points_fwd / rasterize_points_bwd   point clouds
     dmr_grouped_linear_fwd / _bwd                 linear layers, one weight per mesh (or other group)
     dmr_orthogonalize                             orthogonalised updates of their weights
+    dmr_grouped_layer_norm_fwd / _bwd             layer norms, one scale and shift per mesh
+    dmr_clip_norm                                 norms of gradients over many tensors, and clipping
     rasterize_meshes, project_meshes,
-    rasterize_points, grouped_linear              autograd-aware conveniences
-    orthogonalize                                 dmr_orthogonalize with its buffers allocated
+    rasterize_points, grouped_linear,
+    grouped_layer_norm                            autograd-aware conveniences
+    orthogonalize, clip_grad_norm                 dmr_orthogonalize and dmr_clip_norm with their buffers allocated
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+import struct
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdmr.so")
@@ -45,6 +50,8 @@ EXPORTED = [
     "rasterize_points_fwd", "rasterize_points_bwd", "dmr_points_workspace_min_size", "dmr_points_workspace_size_hint",
     "rasterize_meshes_fwd_noalloc", "dmr_grouped_linear_fwd", "dmr_grouped_linear_bwd", "dmr_grouped_linear_workspace_size",
     "dmr_grouped_linear_plan", "dmr_orthogonalize", "dmr_orthogonalize_workspace_size", "dmr_orthogonalize_tile",
+    "dmr_grouped_layer_norm_fwd", "dmr_grouped_layer_norm_bwd", "dmr_grouped_layer_norm_workspace_size",
+    "dmr_clip_norm", "dmr_clip_norm_workspace_size",
 ]
 DMR_NOALLOC_SCRATCH_BYTES = 128 << 20
 DMR_MAX_LINEAR_WIDTH = 1 << 20
@@ -150,6 +157,17 @@ def lib(path: Optional[str] = None):
     L.dmr_orthogonalize.argtypes = [P, I64, I32, I32, ctypes.c_int, I32, ctypes.c_float, P, P, SZ, P]
     L.dmr_orthogonalize_workspace_size.restype = SZ
     L.dmr_orthogonalize_workspace_size.argtypes = [I64, I32, I32, ctypes.c_int]
+    F32, INT = ctypes.c_float, ctypes.c_int
+    L.dmr_grouped_layer_norm_fwd.restype = INT
+    L.dmr_grouped_layer_norm_fwd.argtypes = [P, I64, I32, P, I64, P, P, F32, INT, P, P]
+    L.dmr_grouped_layer_norm_bwd.restype = INT
+    L.dmr_grouped_layer_norm_bwd.argtypes = [P, I64, I32, P, I64, P, F32, INT, P, P, P, P, P, SZ, P]
+    L.dmr_grouped_layer_norm_workspace_size.restype = SZ
+    L.dmr_grouped_layer_norm_workspace_size.argtypes = [I64, I64, I32, INT]
+    L.dmr_clip_norm.restype = INT
+    L.dmr_clip_norm.argtypes = [P, I32, I64, F32, F32, P, P, SZ, P]
+    L.dmr_clip_norm_workspace_size.restype = SZ
+    L.dmr_clip_norm_workspace_size.argtypes = [P, I32, I64]
     if path is None:
         _lib = L
     return L
@@ -559,6 +577,122 @@ def dmr_orthogonalize(update: torch.Tensor, out: torch.Tensor, workspace: torch.
         raise DmrError("dmr_orthogonalize", rc)
 
 
+def _launch(fn, dev, *args) -> None:
+    """Calls the library's `fn` on the current stream of `dev`, with that device current."""
+    stream = _raw_stream(dev)
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise DmrError(fn.__name__, rc)
+
+
+def _layer_norm_inputs(x, row_offsets, weight):
+    dev, dt = x.device, x.dtype
+    if x.dim() != 2 or row_offsets.dim() != 1 or row_offsets.shape[0] < 1:
+        raise ValueError("x must be [R, features] and row_offsets [N + 1]")
+    R, C = x.shape
+    N = row_offsets.shape[0] - 1
+    if not (x.is_contiguous() and _alike(row_offsets, torch.int64, dev, (N + 1,))
+            and (weight is None or _alike(weight, dt, dev, (N, C)))):
+        _check(x, "x", dt, dev)
+        _check(row_offsets, "row_offsets", torch.int64, dev, (N + 1,))
+        _check(weight, "weight", dt, dev, (N, C), optional=True)
+    return dev, dt, R, C, N, _dtype(x, "x")
+
+
+def dmr_grouped_layer_norm_fwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: Optional[torch.Tensor],
+                               bias: Optional[torch.Tensor], y: torch.Tensor, eps: float = 1e-5) -> None:
+    """C-ABI layer norm with one scale and shift per group of rows, on
+    preallocated device tensors (include/dmr.h): y [R, C] from x [R, C],
+    row_offsets [N + 1] int64, weight and bias [N, C] or None."""
+    dev, dt, R, C, N, code = _layer_norm_inputs(x, row_offsets, weight)
+    if not (_alike(y, dt, dev, (R, C)) and (bias is None or _alike(bias, dt, dev, (N, C)))):
+        _check(bias, "bias", dt, dev, (N, C), optional=True)
+        _check(y, "y", dt, dev, (R, C))
+    _launch(lib().dmr_grouped_layer_norm_fwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, _address(weight),
+            _address(bias), eps, code, y.data_ptr())
+
+
+def dmr_grouped_layer_norm_workspace_size(R: int, N: int, features: int, dtype: torch.dtype) -> int:
+    return int(lib().dmr_grouped_layer_norm_workspace_size(R, N, features, DTYPES.get(dtype, -1)))
+
+
+def dmr_grouped_layer_norm_bwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: Optional[torch.Tensor],
+                               grad_y: torch.Tensor, grad_x: Optional[torch.Tensor],
+                               grad_weight: Optional[torch.Tensor], grad_bias: Optional[torch.Tensor],
+                               workspace: Optional[torch.Tensor] = None, eps: float = 1e-5) -> None:
+    """C-ABI backward of the layer norm (include/dmr.h); each of the three
+    gradients may be None. grad_weight and grad_bias need a workspace of
+    dmr_grouped_layer_norm_workspace_size() bytes."""
+    dev, dt, R, C, N, code = _layer_norm_inputs(x, row_offsets, weight)
+    sums = grad_weight is not None or grad_bias is not None
+    if not (_alike(grad_y, dt, dev, (R, C)) and (grad_x is None or _alike(grad_x, dt, dev, (R, C)))
+            and (grad_weight is None or _alike(grad_weight, dt, dev, (N, C)))
+            and (grad_bias is None or _alike(grad_bias, dt, dev, (N, C)))):
+        _check(grad_y, "grad_y", dt, dev, (R, C))
+        _check(grad_x, "grad_x", dt, dev, (R, C), optional=True)
+        _check(grad_weight, "grad_weight", dt, dev, (N, C), optional=True)
+        _check(grad_bias, "grad_bias", dt, dev, (N, C), optional=True)
+    _check(workspace, "workspace", torch.uint8, dev, optional=not sums)
+    _launch(lib().dmr_grouped_layer_norm_bwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, _address(weight), eps, code,
+            grad_y.data_ptr(), _address(grad_x), _address(grad_weight), _address(grad_bias), _address(workspace),
+            0 if workspace is None else workspace.numel())
+
+
+def _spans(tensors, outs, groups) -> Tuple[torch.device, bytes]:
+    """The device of `tensors` and the library's table of them."""
+    if len(tensors) == 0:
+        raise ValueError("there must be a tensor")
+    dev, table = tensors[0].device, []
+    for t, o in zip(tensors, outs):
+        if not (t.is_contiguous() and t.device == dev and t.numel() % max(groups, 1) == 0):
+            _check(t, "tensors", t.dtype, dev)
+            raise ValueError(f"a tensor of {tuple(t.shape)} cannot be shared by {groups} groups")
+        if o is not t and not _alike(o, t.dtype, dev, t.shape):
+            _check(o, "outs", t.dtype, dev, tuple(t.shape))
+        table += (t.data_ptr(), o.data_ptr(), t.numel() // groups if groups else 0, _dtype(t, "tensors"), 0)
+    return dev, struct.pack("QQqii" * len(tensors), *table)
+
+
+def dmr_clip_norm_workspace_size(tensors: Sequence[torch.Tensor], groups: int = 1) -> int:
+    return int(lib().dmr_clip_norm_workspace_size(_spans(tensors, tensors, groups)[1], len(tensors), groups))
+
+
+def dmr_clip_norm(tensors: Sequence[torch.Tensor], outs: Sequence[torch.Tensor], norms: torch.Tensor,
+                  workspace: Optional[torch.Tensor], max_norm: float, groups: int = 1, eps: float = 1e-6) -> None:
+    """C-ABI norms and clipping on preallocated device tensors
+    (include/dmr.h): outs may be tensors themselves; norms [groups] float32;
+    workspace of dmr_clip_norm_workspace_size() bytes."""
+    if len(outs) != len(tensors):
+        raise ValueError(f"{len(tensors)} tensors, but {len(outs)} outs")
+    dev, table = _spans(tensors, outs, groups)
+    _check_overlap(tensors, outs)
+    _check(norms, "norms", torch.float32, dev, (groups,))
+    _check(workspace, "workspace", torch.uint8, dev, optional=True)
+    _launch(lib().dmr_clip_norm, dev, table, len(tensors), groups, max_norm, eps, norms.data_ptr(), _address(workspace),
+            0 if workspace is None else workspace.numel())
+
+
+def _check_overlap(tensors, outs) -> None:
+    """An output may be its own tensor; it may not share memory with another, or with another output."""
+    pieces = []
+    for k, (t, o) in enumerate(zip(tensors, outs)):
+        for is_out, v in ((False, t), (True, o)):
+            if v.numel() and not (is_out and v.data_ptr() == t.data_ptr()):
+                pieces.append((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size(), is_out or o.data_ptr() == t.data_ptr()))
+    pieces.sort()
+    end, written = 0, 0     # of all pieces so far, and of those that are written
+    for lo, hi, out in pieces:
+        if lo < (end if out else written):
+            raise ValueError("an output shares memory with another tensor")
+        end = max(end, hi)
+        if out:
+            written = max(written, hi)
+
+
 # ----------------------------------------------------------------------------
 # convenience: allocation + autograd
 # ----------------------------------------------------------------------------
@@ -789,6 +923,77 @@ def grouped_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Ten
     y = torch.empty((R, cout), dtype=dt, device=dev)
     _launch_grouped(x, R, cin, row_offsets, N, weight, bias, cout, code, y, dev)
     return y
+
+
+class _GroupedLayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, row_offsets, weight, bias, eps):
+        _layer_norm_inputs(x, row_offsets, weight)
+        y = torch.empty_like(x)
+        dmr_grouped_layer_norm_fwd(x, row_offsets, weight, bias, y, eps)
+        ctx.eps, ctx.has_bias = eps, bias is not None
+        ctx.save_for_backward(x, row_offsets, weight)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, row_offsets, weight = ctx.saved_tensors
+        need_x, _, need_w, need_b, _ = ctx.needs_input_grad
+        N, C = row_offsets.shape[0] - 1, x.shape[1]
+        gx = torch.empty_like(x) if need_x else None
+        gw, gb = (torch.empty((N, C), dtype=x.dtype, device=x.device) if need else None for need in (need_w, need_b))
+        ws = None
+        if need_w or need_b:
+            ws = torch.empty(dmr_grouped_layer_norm_workspace_size(x.shape[0], N, C, x.dtype), dtype=torch.uint8,
+                             device=x.device)
+        dmr_grouped_layer_norm_bwd(x, row_offsets, weight, g.contiguous(), gx, gw, gb, ws, ctx.eps)
+        return gx, None, gw, gb, None
+
+
+def _wants_grad(*tensors) -> bool:
+    return forward_ad._current_level >= 0 or torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def grouped_layer_norm(x: torch.Tensor, row_offsets: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, eps: float = 1e-5) -> torch.Tensor:
+    """The rows of every group n (a mesh's vertices, an image's pixels) with
+    mean 0 and variance 1, times weight_n, plus bias_n: x [R, C], row_offsets
+    [N + 1] int64, weight and bias [N, C] or None, all of one type (float32,
+    float16 or bfloat16). Differentiable once with respect to x, weight and
+    bias (in reverse mode; second derivatives and forward mode raise)."""
+    if _wants_grad(x, weight, bias):
+        return _GroupedLayerNorm.apply(x, row_offsets, weight, bias, float(eps))
+    y = torch.empty_like(x)
+    dmr_grouped_layer_norm_fwd(x, row_offsets, weight, bias, y, eps)
+    return y
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, groups: Optional[int] = None, eps: float = 1e-6,
+                   out: Optional[Sequence[torch.Tensor]] = None) -> Tuple[List[torch.Tensor], torch.Tensor]:
+    """(grads times min(1, max_norm / (norm + eps)), norms): the norm of all
+    values of all tensors together, norms [1]; or, with `groups`, one norm for
+    each slice of the tensors' first dimension (each mesh's own decoder), norms
+    [groups]. The tensors may be of different types. `out`: where the results
+    go (the same list: in place); new tensors if not given. Not
+    differentiable."""
+    grads = list(grads)
+    count = 1 if groups is None else int(groups)
+    if groups is not None:
+        for g in grads:
+            if g.dim() < 1 or g.shape[0] != count:
+                raise ValueError(f"grads of {count} groups must be [{count}, ...], got {tuple(g.shape)}")
+    outs = [torch.empty_like(g) for g in grads] if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} grads, but {len(outs)} out")
+    dev, table = _spans(grads, outs, count)
+    if out is not None:
+        _check_overlap(grads, outs)
+    size = lib().dmr_clip_norm_workspace_size(table, len(grads), count)
+    norms = torch.empty(count, dtype=torch.float32, device=dev)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _launch(lib().dmr_clip_norm, dev, table, len(grads), count, max_norm, eps, norms.data_ptr(), ws.data_ptr(), size)
+    return outs, norms
 
 
 def orthogonalize(update: torch.Tensor, steps: int = 5, eps: float = 1e-7) -> torch.Tensor:

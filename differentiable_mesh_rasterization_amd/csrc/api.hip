@@ -38,7 +38,8 @@ std::atomic<uint32_t> g_timing_mask{0};
 const char* const kKernelNames[kKernelCount] = {
     "zero_fwd", "face_setup_count", "bin_scan", "bin_fill", "bin_sort", "fine_raster", "zero_grad", "backward_slots",
     "blend_fwd", "blend_bwd", "project_fwd", "project_bwd", "point_setup", "point_raster", "point_bwd",
-    "grouped_linear_fwd", "grouped_linear_bwd", "orthogonalize",
+    "grouped_linear_fwd", "grouped_linear_bwd", "orthogonalize", "grouped_layer_norm_fwd", "grouped_layer_norm_bwd",
+    "clip_norm",
 };
 
 hipEvent_t take_event() {
@@ -585,6 +586,108 @@ dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n
     a.update = update; a.B = B; a.m = m; a.n = n; a.dtype = dtype; a.steps = steps; a.eps = eps; a.out = out;
     a.workspace = static_cast<char*>(workspace); a.stream = stream;
     return launch_orthogonalize(a) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+namespace {
+
+dmr_status check_layer_norm(int64_t R, int32_t C, int64_t N, dmr_dtype dtype) {
+    if (R < 0 || N < 0 || C < 1) return DMR_ERROR_INVALID_VALUE;
+    if (dtype != DMR_FLOAT32 && dtype != DMR_FLOAT16 && dtype != DMR_BFLOAT16) return DMR_ERROR_INVALID_VALUE;
+    if (C > DMR_MAX_LINEAR_WIDTH) return DMR_ERROR_UNSUPPORTED;
+    if (R > INT64_MAX / ((int64_t)DMR_MAX_LINEAR_WIDTH * 64)) return DMR_ERROR_UNSUPPORTED;
+    // the sums over rows take a workgroup for each group and 64 of its values
+    if (N > kMaxWorkItems / 256 / (2 * (int64_t)C / 64 + 1)) return DMR_ERROR_UNSUPPORTED;
+    if (R > 0 && N == 0) return DMR_ERROR_INVALID_VALUE;
+    return DMR_SUCCESS;
+}
+
+}  // namespace
+
+dmr_status dmr_grouped_layer_norm_fwd(const void* x, int64_t R, int32_t features, const int64_t* row_offsets, int64_t N,
+                                      const void* weight, const void* bias, float eps, dmr_dtype dtype, void* y,
+                                      hipStream_t stream) {
+    dmr_status st = check_layer_norm(R, features, N, dtype);
+    if (st != DMR_SUCCESS) return st;
+    if (!isfinite(eps) || !(eps > 0.0f) || (N > 0 && row_offsets == nullptr)) return DMR_ERROR_INVALID_VALUE;
+    if (R == 0) return DMR_SUCCESS;
+    if (!x || !y) return DMR_ERROR_INVALID_VALUE;
+    LayerNormArgs a{};
+    a.x = x; a.R = R; a.C = features; a.off = row_offsets; a.N = N; a.weight = weight; a.bias = bias; a.eps = eps;
+    a.dtype = dtype; a.y = y; a.stream = stream;
+    return launch_layer_norm(a, false) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+size_t dmr_grouped_layer_norm_workspace_size(int64_t R, int64_t N, int32_t features, dmr_dtype dtype) {
+    if (check_layer_norm(R, features, N, dtype) != DMR_SUCCESS) return 0;
+    return align_up(layer_norm_plan(R, features, dtype != DMR_FLOAT32, true).workspace + 256, 256);
+}
+
+dmr_status dmr_grouped_layer_norm_bwd(const void* x, int64_t R, int32_t features, const int64_t* row_offsets, int64_t N,
+                                      const void* weight, float eps, dmr_dtype dtype, const void* grad_y, void* grad_x,
+                                      void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+    dmr_status st = check_layer_norm(R, features, N, dtype);
+    if (st != DMR_SUCCESS) return st;
+    if (!isfinite(eps) || !(eps > 0.0f) || (N > 0 && row_offsets == nullptr)) return DMR_ERROR_INVALID_VALUE;
+    const bool sums = grad_weight || grad_bias;
+    if (R > 0 && (!x || !grad_y)) return DMR_ERROR_INVALID_VALUE;
+    if (N == 0 || !(grad_x || sums) || (R == 0 && !sums)) return DMR_SUCCESS;
+    if (sums) {
+        if (workspace == nullptr || workspace_bytes < dmr_grouped_layer_norm_workspace_size(R, N, features, dtype))
+            return DMR_ERROR_WORKSPACE_TOO_SMALL;
+        if (!ws_aligned(workspace)) return DMR_ERROR_INVALID_VALUE;
+    }
+    LayerNormArgs a{};
+    a.x = x; a.R = R; a.C = features; a.off = row_offsets; a.N = N; a.weight = weight; a.eps = eps; a.dtype = dtype;
+    a.grad_y = grad_y; a.grad_x = grad_x; a.grad_weight = grad_weight; a.grad_bias = grad_bias;
+    a.workspace = static_cast<float*>(workspace); a.stream = stream;
+    return launch_layer_norm(a, true) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+namespace {
+
+dmr_status check_clip(const dmr_tensor_span* tensors, int32_t count, int64_t groups, ClipPlan* plan) {
+    if (count < 0 || groups < 0 || (count > 0 && tensors == nullptr)) return DMR_ERROR_INVALID_VALUE;
+    int64_t all = 0;
+    for (int32_t k = 0; k < count; ++k) {
+        const dmr_dtype t = tensors[k].dtype;
+        if (tensors[k].values < 0 || (t != DMR_FLOAT32 && t != DMR_FLOAT16 && t != DMR_BFLOAT16)) return DMR_ERROR_INVALID_VALUE;
+        if (tensors[k].values > (INT64_MAX / 8 - all) / (groups > 0 ? groups : 1)) return DMR_ERROR_UNSUPPORTED;
+        all += tensors[k].values * groups;
+    }
+    *plan = clip_plan(tensors, count, groups);
+    return plan->fits ? DMR_SUCCESS : DMR_ERROR_UNSUPPORTED;
+}
+
+size_t clip_workspace(const ClipPlan& p, int64_t groups) {
+    return align_up((p.small ? 0 : (size_t)(p.chunks * groups) * sizeof(double)) + 256, 256);
+}
+
+}  // namespace
+
+size_t dmr_clip_norm_workspace_size(const dmr_tensor_span* tensors, int32_t count, int64_t groups) {
+    ClipPlan p{};
+    return check_clip(tensors, count, groups, &p) == DMR_SUCCESS ? clip_workspace(p, groups) : 0;
+}
+
+dmr_status dmr_clip_norm(const dmr_tensor_span* tensors, int32_t count, int64_t groups, float max_norm, float eps,
+                         float* norms, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    ClipPlan p{};
+    const dmr_status st = check_clip(tensors, count, groups, &p);
+    if (st != DMR_SUCCESS) return st;
+    if (!isfinite(max_norm) || !(max_norm >= 0.0f) || !isfinite(eps) || !(eps >= 0.0f)) return DMR_ERROR_INVALID_VALUE;
+    if (groups == 0) return DMR_SUCCESS;
+    if (norms == nullptr) return DMR_ERROR_INVALID_VALUE;
+    for (int32_t k = 0; k < count; ++k)
+        if (tensors[k].values > 0 && (!tensors[k].in || !tensors[k].out)) return DMR_ERROR_INVALID_VALUE;
+    if (!p.small) {
+        if (workspace == nullptr || workspace_bytes < clip_workspace(p, groups)) return DMR_ERROR_WORKSPACE_TOO_SMALL;
+        if (!ws_aligned(workspace)) return DMR_ERROR_INVALID_VALUE;
+    }
+    ClipArgs a{};
+    a.tensors = tensors; a.count = count; a.groups = groups; a.max_norm = max_norm; a.eps = eps; a.norms = norms;
+    a.workspace = static_cast<double*>(workspace); a.stream = stream;
+    return launch_clip(a, p) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
 }
 
 dmr_status dmr_workspace_stats(const void* workspace, dmr_stats* out, hipStream_t stream) {

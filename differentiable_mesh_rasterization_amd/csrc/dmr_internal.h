@@ -348,6 +348,9 @@ enum KernelId : int32_t {
     kKGroupedLinearFwd,
     kKGroupedLinearBwd,
     kKOrthogonalize,
+    kKLayerNormFwd,
+    kKLayerNormBwd,
+    kKClipNorm,
     kKernelCount
 };
 
@@ -473,6 +476,47 @@ struct OrthogonalizeArgs {
 size_t orthogonalize_workspace(int64_t B, int32_t m, int32_t n);   // 0: too large
 int orthogonalize_tile(int64_t B, int32_t m, int32_t n);   // the side of the tiles of X; 0: one workgroup for a matrix
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a);
+
+struct LayerNormArgs {
+    const void* x; int64_t R; int32_t C;
+    const int64_t* off; int64_t N;
+    const void* weight; const void* bias;   // may be null
+    float eps;
+    dmr_dtype dtype;
+    void* y;                                                           // forward
+    const void* grad_y; void* grad_x; void* grad_weight; void* grad_bias;   // backward
+    float* workspace;
+    hipStream_t stream;
+};
+// The lanes of a row (0: a workgroup takes one) and the 16-byte parts that
+// each holds; the rows of a workgroup, the workgroups, the values of their
+// slots and the bytes of the workspace (backward).
+struct LayerNormPlan {
+    int lanes, parts;
+    int64_t per, workgroups, slot_values;
+    size_t workspace;
+};
+LayerNormPlan layer_norm_plan(int64_t R, int32_t C, bool half, bool backward);
+hipError_t launch_layer_norm(const LayerNormArgs& a, bool backward);
+
+// Tensors that one launch of the clipping takes (the table is an argument of
+// the kernel: no copy to the device).
+constexpr int kClipTensors = 64;
+struct ClipArgs {
+    const dmr_tensor_span* tensors; int32_t count;
+    int64_t groups;
+    float max_norm, eps;
+    float* norms; double* workspace;
+    hipStream_t stream;
+};
+// small: a workgroup for each group does everything. Otherwise values of a
+// chunk, and the chunks of a group. fits: a launch holds it.
+struct ClipPlan {
+    bool small, fits;
+    int64_t length, chunks;
+};
+ClipPlan clip_plan(const dmr_tensor_span* tensors, int32_t count, int64_t groups);
+hipError_t launch_clip(const ClipArgs& a, const ClipPlan& p);
 
 // Timing hooks (api.hip).
 void timing_begin(KernelId id, hipStream_t s);

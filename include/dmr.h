@@ -9,8 +9,10 @@
  * (rasterize_points_fwd / rasterize_points_bwd); the upstream projection
  * from world space (dmr_project_fwd / dmr_project_bwd); linear layers with
  * one weight per mesh (dmr_grouped_linear_fwd / dmr_grouped_linear_bwd) and
- * the orthogonalised update of such weights (dmr_orthogonalize); status
- * strings and optional per-kernel timing.
+ * the orthogonalised update of such weights (dmr_orthogonalize); layer norms
+ * of packed rows (dmr_grouped_layer_norm_fwd / dmr_grouped_layer_norm_bwd) and
+ * norms and clipping of gradients (dmr_clip_norm); status strings and optional
+ * per-kernel timing.
  *
  * The main operation is the face-selection stage of the two-stage rasterizer of
  * "Accelerating 3D Deep Learning with PyTorch3D": for every pixel, select the
@@ -420,6 +422,83 @@ dmr_status dmr_orthogonalize(const void* update, int64_t B, int32_t m, int32_t n
 int32_t dmr_orthogonalize_tile(int64_t B, int32_t m, int32_t n);
 /* Workspace of dmr_orthogonalize in bytes; 0 on invalid arguments. */
 size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dtype dtype);
+
+/*
+ * Layer norms of a packed batch, one scale and shift per group: what stands
+ * between the layers above in a deeper decoder. For the rows r of group n,
+ * with m and v the mean and variance (of the values, not one fewer) of the
+ * row's values,
+ *     y_r = gamma_n (x_r - m) / sqrt(v + eps) + beta_n.
+ *
+ *   x, y       [R, features]; y is overwritten.
+ *   row_offsets [N+1] int64, as for dmr_grouped_linear_fwd; rows that other
+ *              offsets give to no group are left as they are.
+ *   weight (gamma), bias (beta) [N, features], each may be NULL (ones, zeros).
+ *   dtype      of all of them. Statistics and sums are float32; the mean is
+ *              corrected by the deviations' own mean, so that rows far from
+ *              zero keep their digits. Each result is rounded once.
+ *   eps        finite and > 0.
+ * A row depends on no other; one with an infinity or NaN gives NaN
+ * throughout. Deviations whose squares' sum passes float32's range give an
+ * infinite variance (y_r = beta_n).
+ * Errors: negative sizes, features below 1, missing pointers, an unknown
+ * dtype, eps not > 0 and finite, or N == 0 with R > 0:
+ * DMR_ERROR_INVALID_VALUE; features above DMR_MAX_LINEAR_WIDTH or more groups
+ * than a launch can hold: DMR_ERROR_UNSUPPORTED. R == 0 launches nothing.
+ */
+dmr_status dmr_grouped_layer_norm_fwd(const void* x, int64_t R, int32_t features, const int64_t* row_offsets, int64_t N,
+                                      const void* weight, const void* bias, float eps, dmr_dtype dtype, void* y,
+                                      hipStream_t stream);
+
+/* Backward of dmr_grouped_layer_norm_fwd for the same inputs, from grad_y
+ * [R, features]; each result is overwritten and may be NULL. With h_r the
+ * normalised row, s_r = 1 / sqrt(v + eps) and q = gamma_n grad_y_r:
+ *     grad_x_r = s_r (q - mean q - h_r mean(q h_r)),
+ *     grad_weight_n = sum_r grad_y_r h_r,  grad_bias_n = sum_r grad_y_r
+ * (zero for an empty group). Sums over rows are added in a fixed order:
+ * results are the same on every run. workspace: 16-byte aligned, of
+ * dmr_grouped_layer_norm_workspace_size() bytes; not used without grad_weight
+ * and grad_bias. */
+dmr_status dmr_grouped_layer_norm_bwd(const void* x, int64_t R, int32_t features, const int64_t* row_offsets, int64_t N,
+                                      const void* weight, float eps, dmr_dtype dtype, const void* grad_y, void* grad_x,
+                                      void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream);
+/* Workspace of dmr_grouped_layer_norm_bwd in bytes; 0 on invalid arguments. */
+size_t dmr_grouped_layer_norm_workspace_size(int64_t R, int64_t N, int32_t features, dmr_dtype dtype);
+
+/*
+ * Norms of gradients over many tensors, and clipping: what keeps one bad
+ * image from moving a decoder far. Every tensor is [groups, values], and group
+ * g (a mesh whose decoder has a slice of every tensor; or all at once with
+ * groups = 1) has the norm
+ *     n_g = sqrt(sum of v^2 over the values v of its slices of all tensors),
+ *     out = v min(1, max_norm / (n_g + eps)).
+ *
+ *   tensors    `count` of them, on the host, read during the call; each of a
+ *              type of its own. out may be in itself; otherwise no output may
+ *              overlap another tensor.
+ *   max_norm, eps  finite and >= 0.
+ *   norms      [groups], overwritten.
+ *   workspace  16-byte aligned, of dmr_clip_norm_workspace_size() bytes.
+ * Squares are added in float64, in a fixed order; no value's square passes its
+ * range. A factor of 1 leaves the values as they are; one of an infinite norm
+ * is 0 (which makes infinities NaN), one of a NaN norm NaN. Other groups are
+ * not touched by it.
+ * Errors: negative sizes, missing pointers, an unknown dtype, max_norm or eps
+ * not finite or below 0: DMR_ERROR_INVALID_VALUE; more values or groups than a
+ * launch can hold: DMR_ERROR_UNSUPPORTED. groups == 0 launches nothing.
+ */
+typedef struct dmr_tensor_span {
+    const void* in;
+    void* out;
+    int64_t values;   /* of one group */
+    dmr_dtype dtype;
+    int32_t reserved;
+} dmr_tensor_span;
+dmr_status dmr_clip_norm(const dmr_tensor_span* tensors, int32_t count, int64_t groups, float max_norm, float eps,
+                         float* norms, void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* Workspace of dmr_clip_norm in bytes; 0 on invalid arguments. */
+size_t dmr_clip_norm_workspace_size(const dmr_tensor_span* tensors, int32_t count, int64_t groups);
 
 /* What the last forward call on `workspace` recorded. Copies the workspace
  * header to the host and synchronises `stream`. */
