@@ -14,10 +14,11 @@ libdmr.so is missing, every call raises.
     dmr_grouped_linear_fwd / _bwd                 linear layers, one weight per mesh (or other group)
     dmr_orthogonalize                             orthogonalised updates of their weights
     dmr_grouped_layer_norm_fwd / _bwd             layer norms, one scale and shift per mesh
+    dmr_grouped_gated_linear_fwd / _bwd           gated layers, one pair of weights per mesh
     dmr_clip_norm                                 norms of gradients over many tensors, and clipping
     rasterize_meshes, project_meshes,
     rasterize_points, grouped_linear,
-    grouped_layer_norm                            autograd-aware conveniences
+    grouped_layer_norm, grouped_gated_linear      autograd-aware conveniences
     orthogonalize, clip_grad_norm                 dmr_orthogonalize and dmr_clip_norm with their buffers allocated
 """
 
@@ -51,12 +52,14 @@ EXPORTED = [
     "rasterize_meshes_fwd_noalloc", "dmr_grouped_linear_fwd", "dmr_grouped_linear_bwd", "dmr_grouped_linear_workspace_size",
     "dmr_grouped_linear_plan", "dmr_orthogonalize", "dmr_orthogonalize_workspace_size", "dmr_orthogonalize_tile",
     "dmr_grouped_layer_norm_fwd", "dmr_grouped_layer_norm_bwd", "dmr_grouped_layer_norm_workspace_size",
-    "dmr_clip_norm", "dmr_clip_norm_workspace_size",
+    "dmr_clip_norm", "dmr_clip_norm_workspace_size", "dmr_grouped_gated_linear_fwd", "dmr_grouped_gated_linear_bwd",
+    "dmr_grouped_gated_linear_workspace_size",
 ]
 DMR_NOALLOC_SCRATCH_BYTES = 128 << 20
 DMR_MAX_LINEAR_WIDTH = 1 << 20
 DMR_MAX_ORTHOGONALIZE_STEPS = 64
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # dmr_dtype
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "sigmoid": 3}         # dmr_activation
 
 
 class DmrError(RuntimeError):
@@ -164,6 +167,12 @@ def lib(path: Optional[str] = None):
     L.dmr_grouped_layer_norm_bwd.argtypes = [P, I64, I32, P, I64, P, F32, INT, P, P, P, P, P, SZ, P]
     L.dmr_grouped_layer_norm_workspace_size.restype = SZ
     L.dmr_grouped_layer_norm_workspace_size.argtypes = [I64, I64, I32, INT]
+    L.dmr_grouped_gated_linear_fwd.restype = INT
+    L.dmr_grouped_gated_linear_fwd.argtypes = [P, I64, I32, P, I64, P, P, I32, INT, INT, P, P]
+    L.dmr_grouped_gated_linear_bwd.restype = INT
+    L.dmr_grouped_gated_linear_bwd.argtypes = [P, I64, I32, P, I64, P, P, I32, INT, INT, P, P, P, P, P, SZ, P]
+    L.dmr_grouped_gated_linear_workspace_size.restype = SZ
+    L.dmr_grouped_gated_linear_workspace_size.argtypes = [I64, I64, I32, I32, INT]
     L.dmr_clip_norm.restype = INT
     L.dmr_clip_norm.argtypes = [P, I32, I64, F32, F32, P, P, SZ, P]
     L.dmr_clip_norm_workspace_size.restype = SZ
@@ -642,6 +651,62 @@ def dmr_grouped_layer_norm_bwd(x: torch.Tensor, row_offsets: torch.Tensor, weigh
             0 if workspace is None else workspace.numel())
 
 
+def _gated_inputs(x, row_offsets, weight, bias, activation):
+    dev, dt = x.device, x.dtype
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    if x.dim() != 2 or weight.dim() != 4:
+        raise ValueError("x must be [R, in_features] and weight [N, 2, out_features, in_features]")
+    R, C = x.shape
+    N, _, F, _ = weight.shape
+    if not (x.is_contiguous() and _alike(weight, dt, dev, (N, 2, F, C)) and _alike(row_offsets, torch.int64, dev, (N + 1,))
+            and (bias is None or _alike(bias, dt, dev, (N, 2, F)))):
+        _check(x, "x", dt, dev)
+        _check(row_offsets, "row_offsets", torch.int64, dev, (N + 1,))
+        _check(weight, "weight", dt, dev, (N, 2, F, C))
+        _check(bias, "bias", dt, dev, (N, 2, F), optional=True)
+    return dev, dt, R, C, N, F, act, _dtype(x, "x")
+
+
+def dmr_grouped_gated_linear_fwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor,
+                                 bias: Optional[torch.Tensor], y: torch.Tensor, activation: str = "silu") -> None:
+    """C-ABI gated layer with one pair of weights per group of rows, on
+    preallocated device tensors (include/dmr.h): y [R, out] from x [R, in],
+    row_offsets [N + 1] int64, weight [N, 2, out, in] and bias [N, 2, out] or
+    None; activation one of ACTIVATIONS."""
+    dev, dt, R, C, N, F, act, code = _gated_inputs(x, row_offsets, weight, bias, activation)
+    if not _alike(y, dt, dev, (R, F)):
+        _check(y, "y", dt, dev, (R, F))
+    _launch(lib().dmr_grouped_gated_linear_fwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, weight.data_ptr(),
+            _address(bias), F, act, code, y.data_ptr())
+
+
+def dmr_grouped_gated_linear_workspace_size(R: int, N: int, in_features: int, out_features: int, dtype: torch.dtype) -> int:
+    return int(lib().dmr_grouped_gated_linear_workspace_size(R, N, in_features, out_features, DTYPES.get(dtype, -1)))
+
+
+def dmr_grouped_gated_linear_bwd(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor,
+                                 bias: Optional[torch.Tensor], grad_y: torch.Tensor, grad_x: Optional[torch.Tensor],
+                                 grad_weight: Optional[torch.Tensor], grad_bias: Optional[torch.Tensor],
+                                 workspace: torch.Tensor, activation: str = "silu") -> None:
+    """C-ABI backward of the gated layer (include/dmr.h); each of the three
+    gradients may be None. workspace of
+    dmr_grouped_gated_linear_workspace_size() bytes."""
+    dev, dt, R, C, N, F, act, code = _gated_inputs(x, row_offsets, weight, bias, activation)
+    if not (_alike(grad_y, dt, dev, (R, F)) and (grad_x is None or _alike(grad_x, dt, dev, (R, C)))
+            and (grad_weight is None or _alike(grad_weight, dt, dev, (N, 2, F, C)))
+            and (grad_bias is None or _alike(grad_bias, dt, dev, (N, 2, F)))):
+        _check(grad_y, "grad_y", dt, dev, (R, F))
+        _check(grad_x, "grad_x", dt, dev, (R, C), optional=True)
+        _check(grad_weight, "grad_weight", dt, dev, (N, 2, F, C), optional=True)
+        _check(grad_bias, "grad_bias", dt, dev, (N, 2, F), optional=True)
+    _check(workspace, "workspace", torch.uint8, dev)
+    _launch(lib().dmr_grouped_gated_linear_bwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, weight.data_ptr(),
+            _address(bias), F, act, code, grad_y.data_ptr(), _address(grad_x), _address(grad_weight), _address(grad_bias),
+            workspace.data_ptr(), workspace.numel())
+
+
 def _spans(tensors, outs, groups) -> Tuple[torch.device, bytes]:
     """The device of `tensors` and the library's table of them."""
     if len(tensors) == 0:
@@ -967,6 +1032,50 @@ def grouped_layer_norm(x: torch.Tensor, row_offsets: torch.Tensor, weight: Optio
     y = torch.empty_like(x)
     dmr_grouped_layer_norm_fwd(x, row_offsets, weight, bias, y, eps)
     return y
+
+
+class _GroupedGatedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, row_offsets, weight, bias, activation):
+        y = _gated(x, row_offsets, weight, bias, activation)
+        ctx.activation = activation
+        ctx.save_for_backward(x, row_offsets, weight, bias)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, row_offsets, weight, bias = ctx.saved_tensors
+        need_x, _, need_w, need_b, _ = ctx.needs_input_grad
+        N, _, F, C = weight.shape
+        gx, gw, gb = (torch.empty_like(t) if need else None for t, need in ((x, need_x), (weight, need_w), (bias, need_b)))
+        ws = torch.empty(dmr_grouped_gated_linear_workspace_size(x.shape[0], N, C, F, x.dtype), dtype=torch.uint8,
+                         device=x.device)
+        dmr_grouped_gated_linear_bwd(x, row_offsets, weight, bias, g.contiguous(), gx, gw, gb, ws, ctx.activation)
+        return gx, None, gw, gb, None
+
+
+def _gated(x, row_offsets, weight, bias, activation):
+    dev, dt, R, C, N, F, act, code = _gated_inputs(x, row_offsets, weight, bias, activation)
+    y = torch.empty((R, F), dtype=dt, device=dev)
+    _launch(lib().dmr_grouped_gated_linear_fwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, weight.data_ptr(),
+            _address(bias), F, act, code, y.data_ptr())
+    return y
+
+
+def grouped_gated_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: torch.Tensor,
+                         bias: Optional[torch.Tensor] = None, activation: str = "silu") -> torch.Tensor:
+    """y_r = act(A_n x_r + a_n) * (U_n x_r + u_n) for the rows r of every
+    group n (a mesh's vertices, an image's pixels), both products in one
+    kernel: x [R, in], row_offsets [N + 1] int64, weight [N, 2, out, in] (A and
+    U), bias [N, 2, out] (a and u) or None, all of one type (float32, float16
+    or bfloat16); activation "silu", "gelu", "gelu_tanh" or "sigmoid".
+    Differentiable once with respect to x, weight and bias (in reverse mode;
+    second derivatives and forward mode raise); the backward pass keeps only
+    the inputs and computes both products again."""
+    if _wants_grad(x, weight, bias):
+        return _GroupedGatedLinear.apply(x, row_offsets, weight, bias, activation)
+    return _gated(x, row_offsets, weight, bias, activation)
 
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, groups: Optional[int] = None, eps: float = 1e-6,

@@ -39,7 +39,7 @@ const char* const kKernelNames[kKernelCount] = {
     "zero_fwd", "face_setup_count", "bin_scan", "bin_fill", "bin_sort", "fine_raster", "zero_grad", "backward_slots",
     "blend_fwd", "blend_bwd", "project_fwd", "project_bwd", "point_setup", "point_raster", "point_bwd",
     "grouped_linear_fwd", "grouped_linear_bwd", "orthogonalize", "grouped_layer_norm_fwd", "grouped_layer_norm_bwd",
-    "clip_norm",
+    "clip_norm", "grouped_gated_linear_fwd", "grouped_gated_linear_bwd",
 };
 
 hipEvent_t take_event() {
@@ -642,6 +642,59 @@ dmr_status dmr_grouped_layer_norm_bwd(const void* x, int64_t R, int32_t features
     a.grad_y = grad_y; a.grad_x = grad_x; a.grad_weight = grad_weight; a.grad_bias = grad_bias;
     a.workspace = static_cast<float*>(workspace); a.stream = stream;
     return launch_layer_norm(a, true) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+namespace {
+
+// Also as a linear layer of 2 F outputs, which the backward pass is.
+dmr_status check_gated(int64_t R, int32_t C, int64_t N, int32_t F, int32_t act, dmr_dtype dtype, const int64_t* off) {
+    if (F < 1 || act < DMR_SILU || act > DMR_SIGMOID) return DMR_ERROR_INVALID_VALUE;
+    if (F > DMR_MAX_LINEAR_WIDTH / 2) return DMR_ERROR_UNSUPPORTED;
+    return check_grouped(R, C, N, 2 * F, dtype, off);
+}
+
+}  // namespace
+
+dmr_status dmr_grouped_gated_linear_fwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                        const void* weight, const void* bias, int32_t out_features, dmr_activation activation,
+                                        dmr_dtype dtype, void* y, hipStream_t stream) {
+    const dmr_status st = check_gated(R, in_features, N, out_features, activation, dtype, row_offsets);
+    if (st != DMR_SUCCESS) return st;
+    if (R == 0) return DMR_SUCCESS;
+    if (!x || !weight || !y) return DMR_ERROR_INVALID_VALUE;
+    GatedArgs a{};
+    a.x = x; a.R = R; a.C = in_features; a.off = row_offsets; a.N = N; a.weight = weight; a.bias = bias; a.F = out_features;
+    a.act = activation; a.dtype = dtype; a.y = y; a.stream = stream;
+    return launch_gated(a, false) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
+}
+
+size_t dmr_grouped_gated_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features,
+                                               dmr_dtype dtype) {
+    static const int64_t none = 0;
+    if (check_gated(R, in_features, N, out_features, DMR_SILU, dtype, &none) != DMR_SUCCESS) return 0;
+    const size_t sums = dmr_grouped_linear_workspace_size(R, N, in_features, 2 * out_features, dtype);
+    return sums == 0 ? 0 : gated_rows_bytes(R, out_features, dtype) + sums;
+}
+
+dmr_status dmr_grouped_gated_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                        const void* weight, const void* bias, int32_t out_features, dmr_activation activation,
+                                        dmr_dtype dtype, const void* grad_y, void* grad_x, void* grad_weight, void* grad_bias,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const dmr_status st = check_gated(R, in_features, N, out_features, activation, dtype, row_offsets);
+    if (st != DMR_SUCCESS) return st;
+    const bool sums = grad_weight || grad_bias;
+    if (R > 0 && (!x || !weight || !grad_y)) return DMR_ERROR_INVALID_VALUE;
+    if (N == 0 || !(grad_x || sums) || (R == 0 && !sums)) return DMR_SUCCESS;
+    if (!grouped_sums_fit(R, N, in_features, 2 * out_features, dtype != DMR_FLOAT32)) return DMR_ERROR_UNSUPPORTED;
+    if (workspace == nullptr ||
+        workspace_bytes < dmr_grouped_gated_linear_workspace_size(R, N, in_features, out_features, dtype))
+        return DMR_ERROR_WORKSPACE_TOO_SMALL;
+    if (!ws_aligned(workspace)) return DMR_ERROR_INVALID_VALUE;
+    GatedArgs a{};
+    a.x = x; a.R = R; a.C = in_features; a.off = row_offsets; a.N = N; a.weight = weight; a.bias = bias; a.F = out_features;
+    a.act = activation; a.dtype = dtype; a.grad_y = grad_y; a.grad_x = grad_x; a.grad_weight = grad_weight;
+    a.grad_bias = grad_bias; a.workspace = static_cast<char*>(workspace); a.stream = stream;
+    return launch_gated(a, true) == hipSuccess ? DMR_SUCCESS : DMR_ERROR_HIP;
 }
 
 namespace {

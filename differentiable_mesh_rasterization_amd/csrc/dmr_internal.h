@@ -351,6 +351,8 @@ enum KernelId : int32_t {
     kKLayerNormFwd,
     kKLayerNormBwd,
     kKClipNorm,
+    kKGatedLinearFwd,
+    kKGatedLinearBwd,
     kKernelCount
 };
 
@@ -498,6 +500,25 @@ struct LayerNormPlan {
 };
 LayerNormPlan layer_norm_plan(int64_t R, int32_t C, bool half, bool backward);
 hipError_t launch_layer_norm(const LayerNormArgs& a, bool backward);
+
+struct GatedArgs {
+    const void* x; int64_t R; int32_t C;
+    const int64_t* off; int64_t N;
+    const void* weight; const void* bias; int32_t F;   // [N, 2, F, C], [N, 2, F] or null
+    int32_t act;                                       // dmr_activation
+    dmr_dtype dtype;
+    void* y;                                                           // forward
+    const void* grad_y; void* grad_x; void* grad_weight; void* grad_bias;   // backward
+    char* workspace;
+    hipStream_t stream;
+};
+// The columns of each of the two products' tiles, and their rows.
+RowsTile gated_tile(int64_t R, int64_t N, int32_t F, bool half, bool vec);
+// [da du] of all rows, which the workspace begins with.
+inline size_t gated_rows_bytes(int64_t R, int32_t F, dmr_dtype dtype) {
+    return align_up((size_t)R * 2 * F * (dtype == DMR_FLOAT32 ? 4 : 2), 256);
+}
+hipError_t launch_gated(const GatedArgs& a, bool backward);
 
 // Tensors that one launch of the clipping takes (the table is an argument of
 // the kernel: no copy to the device).

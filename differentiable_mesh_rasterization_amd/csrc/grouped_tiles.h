@@ -1,0 +1,232 @@
+// What the layers of packed batches share: the tiles of rows that any split
+// into groups makes, found on the device, and the stores of their results.
+#pragma once
+
+#include "dmr_internal.h"
+#include "mfma_tile.h"
+
+namespace dmr {
+namespace {
+
+// Consecutive tiles that a die is given at a time: what its 32 compute units
+// work on together.
+constexpr int kRun = 32;
+
+// A run of rows of one group.
+struct RowTile {
+    int64_t group, first;   // group < 0: no such tile
+    int rows;
+};
+
+// Bounds of group n, held inside [0, R] whatever the offsets say.
+__device__ __forceinline__ void group_bounds(const int64_t* __restrict__ off, int64_t N, int64_t R, int64_t n,
+                                             int64_t& lo, int64_t& hi) {
+    lo = hi = 0;
+    if (n < N) {
+        lo = off[n];
+        hi = off[n + 1];
+        lo = lo < 0 ? 0 : lo > R ? R : lo;
+        hi = hi < lo ? lo : hi > R ? R : hi;
+    }
+}
+
+template <class I>
+__device__ __forceinline__ I wave_inclusive_sum(I v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const I u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// Workgroup b's place in the order of the tiles. Consecutive workgroups go to
+// the 8 dies in turn; this gives each die runs of RUN consecutive tiles (what
+// its 32 compute units work on at a time), which share rows and weights in
+// its L2, and deals the runs out in turn, so that no die is left with the
+// long groups or with the places past the last tile. The grid is a multiple
+// of 8 RUN.
+template <int RUN>
+__device__ __forceinline__ int64_t tile_of_workgroup(uint32_t b) {
+    const uint32_t die = b & 7, i = b >> 3;
+    return (int64_t)((i / RUN * 8 + die) * RUN + i % RUN);
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Row tile t of all groups' tiles of `per` rows in order. Every wave does
+// the same work. (Tile counts fit in 32 bits: a launch holds no more.)
+__device__ __forceinline__ RowTile find_row_tile(const int64_t* __restrict__ off, int64_t N, int64_t R, int per, int t) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int64_t base = 0; base < N; base += 64) {
+        int64_t lo, hi;
+        group_bounds(off, N, R, base + lane, lo, hi);
+        const int tiles = (int)((hi - lo + per - 1) / per);
+        const int upto = before + wave_inclusive_sum(tiles, lane);
+        const uint64_t hit = __ballot(upto > t);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            const int64_t first = lo + (int64_t)(t - (upto - tiles)) * per;
+            const int64_t left = hi - first;
+            RowTile r;
+            r.group = base + src;
+            r.first = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)first, src) |
+                                (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)((uint64_t)first >> 32), src) << 32);
+            r.rows = __builtin_amdgcn_readlane((int)(left < per ? left : per), src);
+            return r;
+        }
+        before = __builtin_amdgcn_readlane(upto, 63);
+    }
+    return {-1, 0, 0};
+}
+
+// Stores four consecutive n of row m.
+template <class T>
+__device__ __forceinline__ void store4(T* __restrict__ row, int n, int N, f32x4 v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < N) row[n + i] = (T)v[i];
+}
+
+// 16 bytes of a row: 8 16-bit or 4 float32 values.
+template <class T>
+__device__ __forceinline__ u32x4 packed(f32x4 lo, f32x4 hi) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(u32x4, lo);
+    } else {
+        alignas(16) T v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = (T)lo[i];
+            v[4 + i] = (T)hi[i];
+        }
+        return *reinterpret_cast<const u32x4*>(v);
+    }
+}
+
+// Writes a workgroup's tile: rows [0, rows) of `out` (leading dimension ld),
+// columns [n0, N), plus bias[n] if given. `wide`: `out` is 16-byte aligned and
+// ld a multiple of 16 bytes.
+template <class T, class Tile>
+__device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, int64_t ld, int rows, int n0, int N,
+                                           const T* __restrict__ bias, bool wide, int tid) {
+    constexpr int STEP = Tile::PAIRED ? 2 : 1;              // blocks of n in a lane's 16 bytes
+    constexpr bool CHUNKS = Tile::PAIRED || sizeof(T) == 4;   // a lane holds 16 bytes of a row
+    f32x4 add[Tile::NT];
+#pragma unroll
+    for (int a = 0; a < Tile::NT; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = n0 + Tile::n_of(tid, a) + i;   // past the end: any value, not stored
+            add[a][i] = bias ? (float)bias[at < N ? at : N - 1] : 0.0f;
+        }
+    if (CHUNKS && wide) {
+        // 32-bit offsets from the tile's corner; stores past the buffer's
+        // range are dropped
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(out + n0, 0, kBufferRange, 0x00020000);
+        const uint32_t line = (uint32_t)(ld * sizeof(T));
+        const int left = N - n0;
+#pragma unroll
+        for (int b = 0; b < Tile::MT; ++b) {
+            const int m = Tile::m_of(tid, b);
+#pragma unroll
+            for (int a = 0; a < Tile::NT; a += 2 * STEP) {
+                const u32x4 c0 = packed<T>(t.acc[a][b] + add[a], t.acc[a + STEP - 1][b] + add[a + STEP - 1]);
+                const int na = Tile::n_of(tid, a);
+                if constexpr (Tile::NT % (2 * STEP) == 0) {
+                    const u32x4 c1 = packed<T>(t.acc[a + STEP][b] + add[a + STEP],
+                                               t.acc[a + 2 * STEP - 1][b] + add[a + 2 * STEP - 1]);
+                    const int nb = Tile::n_of(tid, a + STEP);
+                    store_row_pairs(c0, c1, tid, [&](bool odd, int chunk, u32x4 v) {
+                        const int row = (m & ~1) | (odd ? 1 : 0), n = chunk ? nb : na;
+                        const uint32_t off = (uint32_t)row * line + (uint32_t)n * (uint32_t)sizeof(T);
+                        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, row < rows && n < left ? off : kNowhere, 0, 0);
+                    });
+                } else {
+                    const uint32_t off = (uint32_t)m * line + (uint32_t)na * (uint32_t)sizeof(T);
+                    __builtin_amdgcn_raw_buffer_store_b128(c0, rsrc, m < rows && na < left ? off : kNowhere, 0, 0);
+                }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int a = 0; a < Tile::NT; a += STEP) {
+        const int n = n0 + Tile::n_of(tid, a);
+#pragma unroll
+        for (int b = 0; b < Tile::MT; ++b) {
+            const int m = Tile::m_of(tid, b);
+            if (m >= rows) continue;
+            T* row = out + (int64_t)m * ld;
+            if (CHUNKS && n + 4 * STEP <= N) {
+                const u32x4 v = packed<T>(t.acc[a][b] + add[a], t.acc[a + STEP - 1][b] + add[a + STEP - 1]);
+                __builtin_memcpy(row + n, &v, 16);   // at whatever alignment it has
+            } else {
+#pragma unroll
+                for (int s = 0; s < STEP; ++s) store4<T>(row, n + 4 * s, N, t.acc[a + s][b] + add[a + s]);
+            }
+        }
+    }
+}
+
+// Products of the rows of `rows_in` (k_in wide) with weights(tile, column) over
+// a workgroup's tiles of rows, each handed to store(product, tile, column).
+template <class T, class Tile, bool VEC, class Weights, class Store>
+__device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32_t blocks, const T* __restrict__ rows_in,
+                                               int64_t R, int k_in, const int64_t* __restrict__ off, int64_t N,
+                                               int64_t tiles, int n_tiles, uint32_t places, Weights&& weights,
+                                               Store&& store) {
+    const int tid = threadIdx.x;
+    const auto find = [&](uint32_t place) {
+        const int64_t id = tile_of_workgroup<kRun>(place);
+        if (id >= tiles) return RowTile{-1, 0, 0};
+        return find_row_tile(off, N, R, Tile::BM, (int)(id / n_tiles));
+    };
+    const auto column = [&](uint32_t place) { return (int)(tile_of_workgroup<kRun>(place) % n_tiles) * Tile::COLUMNS; };
+    const auto rows_of = [&](const RowTile& at) {
+        return typename Tile::Source{rows_in + at.first * (int64_t)k_in, k_in, at.rows};
+    };
+    // A workgroup that takes several tiles finds the next one while a tile is
+    // multiplied and issues its first loads before it stores.
+    uint32_t place = block;
+    RowTile at = find(place);
+    int n0 = column(place);
+    if (at.group >= 0) Tile::template begin<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
+    while (at.group >= 0) {
+        place += blocks;
+        const RowTile next = place < places ? find(place) : RowTile{-1, 0, 0};
+        const int next_n0 = column(place);
+        Tile t;
+        t.template finish<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
+        if (next.group >= 0) Tile::template begin<VEC>(lds, weights(next, next_n0), rows_of(next), k_in, tid);
+        store(t, at, n0);
+        at = next;
+        n0 = next_n0;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The most row tiles of `per` rows that R rows in N groups can make.
+inline int64_t most_row_tiles(int64_t R, int64_t N, int per) { return R / per + (N < R ? N : R); }
+
+// Workgroups for `tiles` tiles; 0 if a launch cannot hold them.
+template <int RUN>
+inline unsigned run_grid(int64_t tiles) {
+    const int64_t grid = (tiles + 8 * RUN - 1) / (8 * RUN) * (8 * RUN);
+    return grid > INT32_MAX ? 0u : (unsigned)grid;
+}
+
+}  // namespace
+}  // namespace dmr

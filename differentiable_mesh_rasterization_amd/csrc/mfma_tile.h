@@ -247,21 +247,29 @@ __device__ __forceinline__ void step_barrier() {
 // The tile product of one workgroup: WN x WM waves, each NT x MT blocks of
 // 16 x 16. Of 16-bit types, neighbouring blocks of n are paired so that a lane
 // holds eight consecutive n. SUMS: sum over k of Q[m][k] as well.
-template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int S, bool SUMS = false>
+// PLANES: P is that many matrices, the same COLUMNS = BN / PLANES of n of each:
+// a lane holds the same n of them in blocks PN apart.
+template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int S, bool SUMS = false, int PLANES = 1>
 struct TileProduct {
-    static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64;
-    static constexpr int NT = BN / WN / 16, MT = BM / WM / 16;
+    static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64, COLUMNS = BN / PLANES;
+    static constexpr int NT = BN / WN / 16, MT = BM / WM / 16, PN = NT / PLANES;
     static constexpr int BK = kStepBytes / (int)sizeof(T);
-    static constexpr bool PAIRED = sizeof(T) == 2 && NT % 2 == 0;
-    using P = OperandTile<T, BN, PK, THREADS, kStepBytes, PAIRED>;
+    static constexpr bool PAIRED = sizeof(T) == 2 && PN % 2 == 0;
+    using P = OperandTile<T, COLUMNS, PK, THREADS, kStepBytes, PAIRED>;
     using Q = OperandTile<T, BM, QK, THREADS>;
-    static constexpr int kStage = P::kBytes + Q::kBytes, kLdsBytes = S * kStage;
-    static_assert(S >= 2 && kLdsBytes <= 160 * 1024, "");
+    static constexpr int kP = PLANES * P::kBytes, kStage = kP + Q::kBytes, kLdsBytes = S * kStage;
+    static_assert(S >= 2 && kLdsBytes <= 160 * 1024 && PN * PLANES == NT, "");
 
     struct Source {   // an operand, at row 0 of the tile and k = 0
         const T* at;
         int64_t ld;
         int rows;   // that exist
+    };
+    struct Planes {   // of the same ld and rows
+        Source plane[PLANES];
+        __device__ __forceinline__ const Source& operator[](int i) const { return plane[i]; }
+        __device__ __forceinline__ Planes(const Source& s) : plane{s} {}
+        __device__ __forceinline__ Planes(const Source& s, const Source& t) : plane{s, t} {}
     };
     struct Fragments {
         u32x4 p[NT], q[MT];
@@ -273,7 +281,8 @@ struct TileProduct {
     // First n of this lane's values of block a, and its row m of block b.
     static __device__ __forceinline__ int n_of(int tid, int a) {
         const int wn = (tid >> 6) % WN, q = (tid & 63) >> 4;
-        return wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 8 * q + 4 * (a & 1) : a * 16 + 4 * q);
+        const int c = a % PN;
+        return wn * PN * 16 + (PAIRED ? (c >> 1) * 32 + 8 * q + 4 * (c & 1) : c * 16 + 4 * q);
     }
     static __device__ __forceinline__ int m_of(int tid, int b) {
         return ((tid >> 6) / WN) * MT * 16 + b * 16 + (tid & 15);
@@ -294,10 +303,13 @@ struct TileProduct {
     static __device__ __forceinline__ void read(Fragments& f, const char* lds_p, const char* lds_q, int kk, int tid) {
         const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
 #pragma unroll
-        for (int a = 0; a < NT; ++a)
+        for (int a = 0; a < NT; ++a) {
+            const char* plane = lds_p + a / PN * P::kBytes;
+            const int c = a % PN;
             if constexpr (PAIRED && !PK) {
-                if (a % 2 == 0) paired_fragments<P>(lds_p, kk, wn * NT * 16 + a * 16, lane, f.p[a], f.p[a + 1]);
-            } else f.p[a] = P::fragment(lds_p, kk, wn * NT * 16 + (PAIRED ? (a >> 1) * 32 + 4 * (a & 1) : a * 16), PAIRED ? 8 : 4, lane);
+                if (c % 2 == 0) paired_fragments<P>(plane, kk, wn * PN * 16 + c * 16, lane, f.p[a], f.p[a + 1]);
+            } else f.p[a] = P::fragment(plane, kk, wn * PN * 16 + (PAIRED ? (c >> 1) * 32 + 4 * (c & 1) : c * 16), PAIRED ? 8 : 4, lane);
+        }
 #pragma unroll
         for (int b = 0; b < MT; ++b) f.q[b] = Q::fragment(lds_q, kk, (wm * MT + b) * 16, 4, lane);
     }
@@ -326,22 +338,23 @@ struct TileProduct {
 
     // Issues the loads of the first steps of a product over k in [0, K).
     template <bool VEC>
-    static __device__ __forceinline__ void begin(char* lds, const Source& p, const Source& q, int K, int tid) {
+    static __device__ __forceinline__ void begin(char* lds, const Planes& p, const Source& q, int K, int tid) {
         const int steps = (K + BK - 1) / BK;
-        const typename P::Offsets po = P::offsets(p.ld, p.rows, tid);
+        const typename P::Offsets po = P::offsets(p[0].ld, p[0].rows, tid);
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
 #pragma unroll
         for (int t = 0; t < S; ++t)
             if (t < steps) {
-                stage<VEC, P>(lds + t * kStage, p, po, t * BK, K, tid);
-                stage<VEC, Q>(lds + t * kStage + P::kBytes, q, qo, t * BK, K, tid);
+#pragma unroll
+                for (int i = 0; i < PLANES; ++i) stage<VEC, P>(lds + t * kStage + i * P::kBytes, p[i], po, t * BK, K, tid);
+                stage<VEC, Q>(lds + t * kStage + kP, q, qo, t * BK, K, tid);
             }
     }
 
     // acc = sum over k in [0, K), begun with the same arguments; the LDS is
     // free for other use afterwards.
     template <bool VEC>
-    __device__ __forceinline__ void finish(char* lds, const Source& p, const Source& q, int K, int tid, bool sums = false) {
+    __device__ __forceinline__ void finish(char* lds, const Planes& p, const Source& q, int K, int tid, bool sums = false) {
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -351,41 +364,44 @@ struct TileProduct {
             for (int b = 0; b < MT; ++b) ones[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (K <= 0) return;
         const int steps = (K + BK - 1) / BK;
-        const typename P::Offsets po = P::offsets(p.ld, p.rows, tid);
+        const typename P::Offsets po = P::offsets(p[0].ld, p[0].rows, tid);
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
         // a wave's loads of a step; they arrive in the order of their issue
-        constexpr int kLoads = VEC ? P::kLoadsLeast + Q::kLoadsLeast : 0;
+        constexpr int kLoads = VEC ? PLANES * P::kLoadsLeast + Q::kLoadsLeast : 0;
         if (S <= steps) step_barrier<(S - 1) * kLoads>();   // step 0 is here
         else step_barrier<0>();
         Fragments first, second;
-        read(first, lds, lds + P::kBytes, 0, tid);
+        read(first, lds, lds + kP, 0, tid);
         int cur = 0;   // this step's stage
         for (int t = 0; t < steps; ++t) {
             char* const here = lds + cur;
-            read(second, here, here + P::kBytes, 1, tid);
+            read(second, here, here + kP, 1, tid);
             multiply(first, sums);
             // step t is read, and the loads of step t + 1 have arrived
             if (t - 1 + S < steps) step_barrier<(S - 2) * kLoads>();
             else step_barrier<0>();
             const bool more = t + S < steps;
-            typename P::Held held_p;
+            typename P::Held held_p[PLANES];
             typename Q::Held held_q;
             if (more) {
                 if constexpr (VEC) {
-                    P::stage(here, p.at, p.ld, po, (t + S) * BK, K, tid);
-                    Q::stage(here + P::kBytes, q.at, q.ld, qo, (t + S) * BK, K, tid);
+#pragma unroll
+                    for (int i = 0; i < PLANES; ++i) P::stage(here + i * P::kBytes, p[i].at, p[i].ld, po, (t + S) * BK, K, tid);
+                    Q::stage(here + kP, q.at, q.ld, qo, (t + S) * BK, K, tid);
                 } else {
-                    P::fetch(held_p, p.at, p.ld, p.rows, (t + S) * BK, K, tid);
+#pragma unroll
+                    for (int i = 0; i < PLANES; ++i) P::fetch(held_p[i], p[i].at, p[i].ld, p[i].rows, (t + S) * BK, K, tid);
                     Q::fetch(held_q, q.at, q.ld, q.rows, (t + S) * BK, K, tid);
                 }
             }
             cur = cur + kStage == kLdsBytes ? 0 : cur + kStage;
-            read(first, lds + cur, lds + cur + P::kBytes, 0, tid);   // past the end: not used
+            read(first, lds + cur, lds + cur + kP, 0, tid);   // past the end: not used
             multiply(second, sums);
             if constexpr (!VEC)
                 if (more) {
-                    P::put(here, held_p, tid);
-                    Q::put(here + P::kBytes, held_q, tid);
+#pragma unroll
+                    for (int i = 0; i < PLANES; ++i) P::put(here + i * P::kBytes, held_p[i], tid);
+                    Q::put(here + kP, held_q, tid);
                 }
         }
         step_barrier<0>();
@@ -401,7 +417,7 @@ struct TileProduct {
     }
 
     template <bool VEC>
-    __device__ __forceinline__ void run(char* lds, const Source& p, const Source& q, int K, int tid, bool sums = false) {
+    __device__ __forceinline__ void run(char* lds, const Planes& p, const Source& q, int K, int tid, bool sums = false) {
         begin<VEC>(lds, p, q, K, tid);
         finish<VEC>(lds, p, q, K, tid, sums);
     }

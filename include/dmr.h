@@ -10,9 +10,10 @@
  * from world space (dmr_project_fwd / dmr_project_bwd); linear layers with
  * one weight per mesh (dmr_grouped_linear_fwd / dmr_grouped_linear_bwd) and
  * the orthogonalised update of such weights (dmr_orthogonalize); layer norms
- * of packed rows (dmr_grouped_layer_norm_fwd / dmr_grouped_layer_norm_bwd) and
- * norms and clipping of gradients (dmr_clip_norm); status strings and optional
- * per-kernel timing.
+ * of packed rows (dmr_grouped_layer_norm_fwd / dmr_grouped_layer_norm_bwd),
+ * gated layers (dmr_grouped_gated_linear_fwd / dmr_grouped_gated_linear_bwd)
+ * and norms and clipping of gradients (dmr_clip_norm); status strings and
+ * optional per-kernel timing.
  *
  * The main operation is the face-selection stage of the two-stage rasterizer of
  * "Accelerating 3D Deep Learning with PyTorch3D": for every pixel, select the
@@ -465,6 +466,56 @@ dmr_status dmr_grouped_layer_norm_bwd(const void* x, int64_t R, int32_t features
                                       hipStream_t stream);
 /* Workspace of dmr_grouped_layer_norm_bwd in bytes; 0 on invalid arguments. */
 size_t dmr_grouped_layer_norm_workspace_size(int64_t R, int64_t N, int32_t features, dmr_dtype dtype);
+
+/*
+ * Gated layers of a packed batch, one pair of weights per group: the wide part
+ * of a deeper decoder's block (a linear layer leads back). For the rows r of
+ * group n, with A_n, U_n the two planes of its weight and a_n, u_n of its bias,
+ *     y_r = act(A_n x_r + a_n) (U_n x_r + u_n)   (value by value).
+ *
+ *   x          [R, in_features]; y [R, out_features], overwritten.
+ *   row_offsets [N+1] int64, as for dmr_grouped_linear_fwd; rows that other
+ *              offsets give to no group are left as they are.
+ *   weight     [N, 2, out_features, in_features]; bias [N, 2, out_features] or
+ *              NULL.
+ *   activation act(a): a / (1 + e^-a) (DMR_SILU), a Phi(a) with the normal
+ *              distribution Phi (DMR_GELU), a / (1 + e^-2z) with z = sqrt(2/pi)
+ *              (a + 0.044715 a^3) (DMR_GELU_TANH), 1 / (1 + e^-a)
+ *              (DMR_SIGMOID).
+ *   dtype      of x, weight, bias, y and all gradients. Sums and activations
+ *              are float32 (float32 products too); y is rounded once.
+ * A row depends on no other row; where a or u is infinite or NaN, y is what
+ * the formula gives in float32 (NaN where it multiplies an infinity by zero).
+ * Errors: as for dmr_grouped_linear_fwd with 2 out_features, and
+ * DMR_ERROR_INVALID_VALUE for an unknown activation. R == 0 launches nothing.
+ */
+typedef enum dmr_activation {
+    DMR_SILU = 0,
+    DMR_GELU = 1,
+    DMR_GELU_TANH = 2,
+    DMR_SIGMOID = 3
+} dmr_activation;
+dmr_status dmr_grouped_gated_linear_fwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                        const void* weight, const void* bias, int32_t out_features, dmr_activation activation,
+                                        dmr_dtype dtype, void* y, hipStream_t stream);
+
+/* Backward of dmr_grouped_gated_linear_fwd for the same inputs, from grad_y
+ * [R, out_features]; each result is overwritten and may be NULL. With a and u
+ * as above (they are computed again), da = g u act'(a) and du = g act(a):
+ *     grad_x_r = A_n^T da_r + U_n^T du_r,
+ *     grad_weight_n = (sum_r da_r x_r^T, sum_r du_r x_r^T),
+ *     grad_bias_n = (sum_r da_r, sum_r du_r)   (zero for an empty group).
+ * da and du are rounded to dtype before these products and sums, which are
+ * float32 and added in a fixed order: results are the same on every run.
+ * workspace: 16-byte aligned, of dmr_grouped_gated_linear_workspace_size()
+ * bytes. */
+dmr_status dmr_grouped_gated_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,
+                                        const void* weight, const void* bias, int32_t out_features, dmr_activation activation,
+                                        dmr_dtype dtype, const void* grad_y, void* grad_x, void* grad_weight, void* grad_bias,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* Workspace of dmr_grouped_gated_linear_bwd in bytes; 0 on invalid arguments. */
+size_t dmr_grouped_gated_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features,
+                                               dmr_dtype dtype);
 
 /*
  * Norms of gradients over many tensors, and clipping: what keeps one bad

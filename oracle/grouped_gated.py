@@ -1,0 +1,132 @@
+"""CPU oracle of the gated layers with one pair of weights per group of a
+packed batch, and their backward pass (binary64 numpy).
+
+TEST INFRASTRUCTURE ONLY: the plain, slow definition the GPU layer is checked
+against; it imports nothing from the GPU package.
+
+For the rows r of group n, weight [N, 2, F, C] = (A, U) and bias [N, 2, F]:
+    a = A_n x_r + a_n,  u = U_n x_r + u_n,  y_r = act(a) u;
+    da = g_r u act'(a),  du = g_r act(a),
+    grad_x_r = A_n^T da + U_n^T du,  grad_weight_n = sum_r (da x_r^T, du x_r^T),
+    grad_bias_n = sum_r (da, du).
+"""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+
+from .grouped_linear import TINY, UNIT, _groups, sum_error_bound
+
+ROUND = 2.0 ** -23
+K = math.sqrt(2.0 / math.pi)
+ACTIVATIONS = ("silu", "gelu", "gelu_tanh", "sigmoid")
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
+
+
+def _logistic(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1.0, e) / (1.0 + e)
+
+
+def activate(a, kind):
+    """(act(a), act'(a), the derivative's part that does not vanish with a)"""
+    a = np.asarray(a, np.float64)
+    if kind == "sigmoid":
+        s = _logistic(a)
+        return s, s * _logistic(-a), s * _logistic(-a)
+    if kind == "gelu":
+        below = 0.5 * (_erfc(-a / math.sqrt(2.0)) if a.size else a)
+        return a * below, below + a * np.exp(-0.5 * a * a) / math.sqrt(2.0 * math.pi), below
+    if kind == "silu":
+        z, dz = a, 1.0
+    elif kind == "gelu_tanh":
+        z, dz = 2 * K * (a + 0.044715 * a ** 3), 2 * K * (1 + 3 * 0.044715 * a * a)
+    else:
+        raise ValueError(kind)
+    s = _logistic(z)
+    return a * s, s + a * s * _logistic(-z) * dz, s
+
+
+def _projections(x, row_offsets, weight, bias):
+    N, _, F, _ = weight.shape
+    both = np.zeros((x.shape[0], 2, F))
+    for n, rows in _groups(row_offsets):
+        both[rows] = np.einsum("rc,pfc->rpf", x[rows], weight[n])
+        if bias is not None:
+            both[rows] += bias[n]
+    return both[:, 0], both[:, 1]
+
+
+def _doubles(*arrays):
+    return tuple(None if v is None else np.asarray(v, np.float64) for v in arrays)
+
+
+def gated_forward(x, row_offsets, weight, bias=None, activation="silu"):
+    x, weight, bias = _doubles(x, weight, bias)
+    a, u = _projections(x, row_offsets, weight, bias)
+    return activate(a, activation)[0] * u
+
+
+def gated_backward(x, row_offsets, weight, bias, grad_y, activation="silu"):
+    """(grad_x, grad_weight, grad_bias) from grad_y [R, F]."""
+    x, weight, bias, g = _doubles(x, weight, bias, grad_y)
+    a, u = _projections(x, row_offsets, weight, bias)
+    act, slope, _ = activate(a, activation)
+    return _products(x, row_offsets, weight, np.stack([g * u * slope, g * act], axis=1))
+
+
+def _products(x, row_offsets, weight, back):
+    gx, gw, gb = np.zeros_like(x), np.zeros_like(weight), np.zeros(weight.shape[:3])
+    for n, rows in _groups(row_offsets):
+        gx[rows] = np.einsum("rpf,pfc->rc", back[rows], weight[n])
+        gw[n] = np.einsum("rpf,rc->pfc", back[rows], x[rows])
+        gb[n] = back[rows].sum(axis=0)
+    return gx, gw, gb
+
+
+def _parts(x, row_offsets, weight, bias, activation):
+    """a, u, act(a), act'(a), and bounds on the error of each.
+
+    a and u are sums of C + 1 products in binary32: (C + 3) u of the sum of
+    absolute values, u = ROUND. act and act' have derivatives of at most 1.13
+    and 1 in magnitude. Their own evaluation is off by 8 roundings, and by
+    those of the exponent: 4 u of its argument, which is at most a^2 + |a| +
+    0.08 |a|^3 (gelu's a^2 / 2, silu's a, gelu_tanh's 1.6 a + 0.08 a^3, with
+    the change of the normal distribution's tail below its density's), each of
+    the value or of the derivative's two terms; below 2^-126 they may vanish."""
+    a, u = _projections(x, row_offsets, weight, bias)
+    mag = _projections(np.abs(x), row_offsets, np.abs(weight), None if bias is None else np.abs(bias))
+    ea, eu = ((x.shape[1] + 3) * ROUND * m for m in mag)
+    act, slope, first = activate(a, activation)
+    own = (8 + 4 * (a * a + 2 * np.abs(a) + 0.08 * np.abs(a) ** 3)) * ROUND
+    gone = 2.0 ** -125 * (1 + np.abs(a))
+    eact = 1.13 * ea + own * np.abs(act) + gone
+    eslope = ea + own * (np.abs(first) + np.abs(slope - first)) + gone
+    return a, u, act, slope, eu, eact, eslope
+
+
+def gated_forward_bound(x, row_offsets, weight, bias, dtype, activation="silu"):
+    x, weight, bias = _doubles(x, weight, bias)
+    _, u, act, _, eu, eact, _ = _parts(x, row_offsets, weight, bias, activation)
+    y = act * u
+    e = np.abs(u) * eact + np.abs(act) * eu + eact * eu + ROUND * np.abs(y)
+    return e + UNIT[dtype] * (np.abs(y) + e) + TINY[dtype]
+
+
+def gated_backward_bound(x, row_offsets, weight, bias, grad_y, dtype, activation="silu"):
+    """[da du] with the errors of its factors and one rounding to the type, then sums as for linear layers."""
+    x, weight, bias, g = _doubles(x, weight, bias, grad_y)
+    _, u, act, slope, eu, eact, eslope = _parts(x, row_offsets, weight, bias, activation)
+    da, du = g * u * slope, g * act
+    ea = np.abs(g) * (np.abs(u) * eslope + np.abs(slope) * eu + eslope * eu) + 2 * ROUND * np.abs(da)
+    ed = np.abs(g) * eact + ROUND * np.abs(du)
+    back, eback = np.stack([da, du], axis=1), np.stack([ea, ed], axis=1)
+    eback = eback + UNIT[dtype] * (np.abs(back) + eback) + TINY[dtype]
+    value = _products(x, row_offsets, weight, back)
+    mag = _products(np.abs(x), row_offsets, np.abs(weight), np.abs(back) + eback)
+    extra = _products(np.abs(x), row_offsets, np.abs(weight), eback)
+    rows = np.diff(np.asarray(row_offsets, np.int64)).astype(np.float64)
+    terms = (2 * weight.shape[2], rows[:, None, None, None], rows[:, None, None])
+    return tuple(sum_error_bound(m, t, v, dtype) + (1 + UNIT[dtype]) * e for m, t, v, e in zip(mag, terms, value, extra))
