@@ -672,8 +672,8 @@ size_t dmr_grouped_gated_linear_workspace_size(int64_t R, int64_t N, int32_t in_
                                                dmr_dtype dtype) {
     static const int64_t none = 0;
     if (check_gated(R, in_features, N, out_features, DMR_SILU, dtype, &none) != DMR_SUCCESS) return 0;
-    const size_t sums = dmr_grouped_linear_workspace_size(R, N, in_features, 2 * out_features, dtype);
-    return sums == 0 ? 0 : gated_rows_bytes(R, out_features, dtype) + sums;
+    if (!grouped_sums_fit(R, N, in_features, 2 * out_features, dtype != DMR_FLOAT32)) return 0;
+    return gated_workspace(R, N, in_features, out_features, dtype);
 }
 
 dmr_status dmr_grouped_gated_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,

@@ -467,6 +467,8 @@ __host__ __device__ __forceinline__ int64_t grouped_piece_values(int32_t cin, in
 }
 hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a);
 hipError_t launch_grouped_linear_backward(const GroupedLinearArgs& a);
+// Adds the pieces of long groups' sums (of the backward pass' arguments).
+hipError_t launch_grouped_add_pieces(const GroupedLinearArgs& a, const GroupedPieces& p);
 
 struct OrthogonalizeArgs {
     const void* update; int64_t B; int32_t m, n;
@@ -518,6 +520,10 @@ RowsTile gated_tile(int64_t R, int64_t N, int32_t F, bool half, bool vec);
 inline size_t gated_rows_bytes(int64_t R, int32_t F, dmr_dtype dtype) {
     return align_up((size_t)R * 2 * F * (dtype == DMR_FLOAT32 ? 4 : 2), 256);
 }
+// Whether one kernel computes the whole backward pass, and how it cuts the rows.
+bool gated_narrow(int32_t C, int32_t F);
+GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half);
+size_t gated_workspace(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype);
 hipError_t launch_gated(const GatedArgs& a, bool backward);
 
 // Tensors that one launch of the clipping takes (the table is an argument of

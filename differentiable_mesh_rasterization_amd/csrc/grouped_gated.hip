@@ -73,16 +73,6 @@ __device__ __forceinline__ void with_activation(int act, F&& f) {
     else f([](float a) { return activate<DMR_SIGMOID>(a); });
 }
 
-// One plane's blocks of a tile, for store_tile.
-template <class Tile>
-struct Plane {
-    static constexpr int NT = Tile::PN, MT = Tile::MT;
-    static constexpr bool PAIRED = Tile::PAIRED;
-    f32x4 acc[NT][MT];
-    static __device__ __forceinline__ int n_of(int tid, int a) { return Tile::n_of(tid, a); }
-    static __device__ __forceinline__ int m_of(int tid, int b) { return Tile::m_of(tid, b); }
-};
-
 // Adds the biases (or nothing) to both planes of a tile.
 template <class T, class Tile>
 __device__ __forceinline__ void add_biases(Tile& t, const T* __restrict__ bias, int F, int n0, int tid) {
@@ -100,22 +90,112 @@ __device__ __forceinline__ void add_biases(Tile& t, const T* __restrict__ bias, 
     }
 }
 
-// Values n .. n + 3 of row m of a [rows, N] array; any value where there is none.
+// Where a lane's values of a tile go: rows [0, rows) of `out` (leading
+// dimension ld), columns [n0, N). `wide`: `out` is 16-byte aligned and ld a
+// multiple of 16 bytes.
 template <class T>
-__device__ __forceinline__ f32x4 load4(const T* __restrict__ row, int n, int N, bool exists) {
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (exists && n + 4 <= N) {
-        T t[4];
-        __builtin_memcpy(t, row + n, sizeof(t));
+struct TileOut {
+    T* out;
+    int64_t ld;
+    int rows, n0, N;
+    bool wide;
+};
+
+// Stores block b of a tile's rows, value(a) the four values of block a < NT: as
+// soon as they are formed, which keeps them out of scratch memory.
+template <class T, class Tile, int NT, class Value>
+__device__ __forceinline__ void store_rows(const TileOut<T>& o, int b, int tid, Value&& value) {
+    constexpr int STEP = Tile::PAIRED ? 2 : 1;              // blocks of n in a lane's 16 bytes
+    constexpr bool CHUNKS = Tile::PAIRED || sizeof(T) == 4;   // a lane holds 16 bytes of a row
+    const int m = Tile::m_of(tid, b);
+    if (CHUNKS && o.wide) {
+        // 32-bit offsets from the tile's corner; stores past the buffer's
+        // range are dropped
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(o.out + o.n0, 0, kBufferRange, 0x00020000);
+        const uint32_t line = (uint32_t)(o.ld * sizeof(T));
+        const int left = o.N - o.n0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)t[i];
-    } else if (exists) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < N) v[i] = (float)row[n + i];
+        for (int a = 0; a < NT; a += 2 * STEP) {
+            const u32x4 c0 = packed<T>(value(a), value(a + STEP - 1));
+            const int na = Tile::n_of(tid, a);
+            if constexpr (NT % (2 * STEP) == 0) {
+                const u32x4 c1 = packed<T>(value(a + STEP), value(a + 2 * STEP - 1));
+                const int nb = Tile::n_of(tid, a + STEP);
+                store_row_pairs(c0, c1, tid, [&](bool odd, int chunk, u32x4 v) {
+                    const int row = (m & ~1) | (odd ? 1 : 0), n = chunk ? nb : na;
+                    const uint32_t off = (uint32_t)row * line + (uint32_t)n * (uint32_t)sizeof(T);
+                    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, row < o.rows && n < left ? off : kNowhere, 0, 0);
+                });
+            } else {
+                const uint32_t off = (uint32_t)m * line + (uint32_t)na * (uint32_t)sizeof(T);
+                __builtin_amdgcn_raw_buffer_store_b128(c0, rsrc, m < o.rows && na < left ? off : kNowhere, 0, 0);
+            }
+        }
+        return;
     }
-    return v;
+    if (m >= o.rows) return;
+    T* row = o.out + (int64_t)m * o.ld;
+#pragma unroll
+    for (int a = 0; a < NT; a += STEP) {
+        const int n = o.n0 + Tile::n_of(tid, a);
+        if (CHUNKS && n + 4 * STEP <= o.N) {
+            const u32x4 v = packed<T>(value(a), value(a + STEP - 1));
+            __builtin_memcpy(row + n, &v, 16);   // at whatever alignment it has
+        } else {
+#pragma unroll
+            for (int s = 0; s < STEP; ++s) store4<T>(row, n + 4 * s, o.N, value(a + s));
+        }
+    }
 }
+
+// A lane's values of grad_y in a tile, 16 bytes of a row at a time where a
+// lane's columns are that many; zero where there are none.
+template <class T, class Tile>
+struct Upstream {
+    static constexpr bool CHUNKS = Tile::PAIRED || sizeof(T) == 4;
+    static constexpr int STEP = Tile::PAIRED ? 2 : 1;   // blocks of n in one piece
+    static constexpr int BYTES = STEP * 4 * (int)sizeof(T);
+    uint32_t raw[Tile::MT][Tile::PN / STEP][BYTES / 4];
+
+    // o: of grad_y
+    __device__ __forceinline__ void load(const TileOut<const T>& o, int tid) {
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(o.out + o.n0), 0, kBufferRange, 0x00020000);
+        const uint32_t line = (uint32_t)(o.ld * sizeof(T));
+#pragma unroll
+        for (int b = 0; b < Tile::MT; ++b) {
+            const int m = Tile::m_of(tid, b);
+#pragma unroll
+            for (int a = 0; a < Tile::PN / STEP; ++a) {
+                const int n = Tile::n_of(tid, a * STEP), left = o.N - o.n0 - n;
+                if (CHUNKS && o.wide) {
+                    const uint32_t off = m < o.rows && left > 0 ? (uint32_t)m * line + (uint32_t)n * (uint32_t)sizeof(T) : kNowhere;
+                    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0);
+                    __builtin_memcpy(raw[b][a], &v, BYTES);
+                } else {
+                    const T* at = o.out + (int64_t)m * o.ld + o.n0 + n;
+                    T v[4 * STEP];
+#pragma unroll
+                    for (int i = 0; i < 4 * STEP; ++i) v[i] = (T)0.0f;
+                    if (m < o.rows && left >= 4 * STEP) {
+                        __builtin_memcpy(v, at, BYTES);
+                    } else if (m < o.rows) {
+#pragma unroll
+                        for (int i = 0; i < 4 * STEP; ++i)
+                            if (i < left) v[i] = at[i];
+                    }
+                    __builtin_memcpy(raw[b][a], v, BYTES);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float value(int b, int a, int i) const {
+        T v[4 * STEP];
+        __builtin_memcpy(v, raw[b][a / STEP], BYTES);
+        return (float)v[a % STEP * 4 + i];
+    }
+};
+struct Nothing {};
 
 // GRAD: writes [da du] of the rows to `out` [R, 2 F] from grad_y [R, F];
 // otherwise y to `out` [R, F].
@@ -123,8 +203,9 @@ template <class T, class Tile, bool VEC, bool GRAD>
 __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restrict__ x, int64_t R, int C,
                                                                const int64_t* __restrict__ off, int64_t N,
                                                                const T* __restrict__ weight, const T* __restrict__ bias, int F,
-                                                               int act, const T* __restrict__ grad_y, T* __restrict__ out,
-                                                               bool wide, int64_t tiles, int n_tiles, uint32_t places) {
+                                                               int act, const T* __restrict__ grad_y, bool wide_g,
+                                                               T* __restrict__ out, bool wide, int64_t tiles, int n_tiles,
+                                                               uint32_t places) {
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
     const int tid = threadIdx.x;
     walk_row_tiles<T, Tile, VEC>(
@@ -134,42 +215,349 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
             return typename Tile::Planes(typename Tile::Source{w, C, F - n0},
                                          typename Tile::Source{w + (int64_t)F * C, C, F - n0});
         },
-        [&](Tile& t, const RowTile& at, int n0) {
+        [&](const RowTile& at, int n0) {
+            if constexpr (GRAD) {
+                Upstream<T, Tile> g;
+                g.load({grad_y + at.first * (int64_t)F, F, at.rows, n0, F, wide_g}, tid);
+                return g;
+            } else {
+                return Nothing{};
+            }
+        },
+        [&](Tile& t, const RowTile& at, int n0, const auto& g) {
             add_biases<T, Tile>(t, bias ? bias + at.group * 2 * F : nullptr, F, n0, tid);
-            Plane<Tile> first, second;
+            constexpr int WIDTHS = GRAD ? 2 : 1;
+            const TileOut<T> first = {out + at.first * (int64_t)F * WIDTHS, (int64_t)F * WIDTHS, at.rows, n0, F, wide};
+            TileOut<T> second = first;
+            second.out += F;
             with_activation(act, [&](auto&& activation) {
 #pragma unroll
                 for (int b = 0; b < Tile::MT; ++b) {
-                    const int m = Tile::m_of(tid, b);
 #pragma unroll
-                    for (int a = 0; a < Tile::PN; ++a) {
-                        f32x4 g;
-                        if constexpr (GRAD)
-                            g = load4<T>(grad_y + (at.first + m) * F, n0 + Tile::n_of(tid, a), F, m < at.rows);
+                    for (int a = 0; a < Tile::PN; ++a)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const Act v = activation(t.acc[a][b][i]);
-                            const float u = t.acc[a + Tile::PN][b][i];
                             if constexpr (GRAD) {
-                                first.acc[a][b][i] = g[i] * u * v.slope;
-                                second.acc[a][b][i] = g[i] * v.value;
+                                const float up = g.value(b, a, i);
+                                t.acc[a][b][i] = up * t.acc[a + Tile::PN][b][i] * v.slope;
+                                t.acc[a + Tile::PN][b][i] = up * v.value;
                             } else {
-                                first.acc[a][b][i] = v.value * u;
+                                t.acc[a][b][i] = v.value * t.acc[a + Tile::PN][b][i];
                             }
                         }
-                    }
+                    store_rows<T, Tile, Tile::PN>(first, b, tid, [&](int a) { return t.acc[a][b]; });
+                    if constexpr (GRAD)
+                        store_rows<T, Tile, Tile::PN>(second, b, tid, [&](int a) { return t.acc[a + Tile::PN][b]; });
                 }
             });
-            constexpr int WIDTHS = GRAD ? 2 : 1;
-            T* rows = out + at.first * (int64_t)F * WIDTHS;
-            store_tile<T>(first, rows, (int64_t)F * WIDTHS, at.rows, n0, F, (const T*)nullptr, wide, tid);
-            if constexpr (GRAD)
-                store_tile<T>(second, rows + F, (int64_t)F * WIDTHS, at.rows, n0, F, (const T*)nullptr, wide, tid);
         });
 }
 
+// ---------------------------------------------------------------------------
+// narrow layers: the whole backward pass in one kernel
+// ---------------------------------------------------------------------------
+// With C <= 64 and F <= 128 a workgroup holds both planes of its group's
+// weight in LDS and the gradient of the weight in its accumulators, and takes
+// a piece of the group's rows, 64 MT rows at a time. Each wave has 16 MT of
+// them: it computes a and u, and da and du from them, which are in its
+// accumulators just as the product with the weight takes its operand (row
+// lane & 15, eight consecutive f of 16-bit types or four of float32), so that
+// grad_x follows without a move. For the sum over rows, [da du] and x go to
+// LDS and each wave takes a quarter of the weight's rows. x, grad_y and grad_x
+// pass memory once: 3 C + F values a row where the general form, with [da du]
+// in memory, moves 4 C + 7 F.
+//
+// What bounds it: memory (16-bit) and the float32 products (float32).
+template <class T, int FP_, int MT_>
+struct Narrow {
+    static constexpr int FP = FP_, MT = MT_, CP = 64, THREADS = 256, BM = 64 * MT;
+    static constexpr bool HALF = sizeof(T) == 2;
+    static constexpr int E = 16 / (int)sizeof(T);     // values of 16 bytes
+    static constexpr int XS = CP / (4 * E);           // 64-byte slices of x's row, and of
+    static constexpr int PS = FP / (4 * E);           // a plane's
+    static constexpr int PB = FP / 16, CB = CP / 16;  // blocks of 16
+    static constexpr int WB = 2 * FP / 64;            // blocks of a wave's share of the weight's rows
+    using W = OperandTile<T, FP, true, THREADS, CP * (int)sizeof(T)>;
+    using D = OperandTile<T, 2 * FP, false, THREADS>;
+    using X = OperandTile<T, CP, false, THREADS>;
+    static constexpr int kW = 2 * W::kBytes, kD = BM * 2 * FP * (int)sizeof(T), kX = BM * CP * (int)sizeof(T);
+    static constexpr int kLdsBytes = kW + kD + kX;
+    static_assert(kLdsBytes <= 160 * 1024, "");
+
+    // Blocks of a plane, and of grad_x's columns, are paired in 16 bits so
+    // that a lane holds eight consecutive values.
+    static __device__ __forceinline__ int first_of(int block) { return HALF ? (block >> 1) * 32 + 4 * (block & 1) : block * 16; }
+    static constexpr int STRIDE = HALF ? 8 : 4;
+    // A lane's first column of slice s of a row.
+    static __device__ __forceinline__ int column(int s, int lane) { return s * 4 * E + (lane >> 4) * E; }
+
+    // 16 bytes of line `line` of an image of W, D or X.
+    template <class Image>
+    static __device__ __forceinline__ char* chunk(char* lds, int line, int chunk, int line_bytes) {
+        return lds + line * line_bytes + ((chunk ^ Image::swizzle(line)) << 4);
+    }
+
+    // The fragment of the weight's transpose: columns c = first + STRIDE a + i,
+    // slice s of a plane's f.
+    static __device__ __forceinline__ u32x4 transposed(const char* plane, int s, int first, int lane) {
+        constexpr int line_bytes = CP * (int)sizeof(T);
+        const int q = lane >> 4, r = lane & 15;
+        if constexpr (HALF) {
+            s16x4 half[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int f = s * 32 + 8 * q + 4 * h + (r >> 2), c = first + STRIDE * (r & 3);
+                const int at = f * line_bytes + (((c >> 3) ^ W::swizzle(f)) << 4) + (c & 7) * 2;
+                half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DMR_LDS s16x4*)(plane + at));
+            }
+            return __builtin_bit_cast(u32x4, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int c = first + STRIDE * (r >> 2) + (r & 3);
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int f = s * 16 + 4 * q + j;
+                v[j] = *reinterpret_cast<const uint32_t*>(plane + f * line_bytes + (((c >> 2) ^ W::swizzle(f)) << 4) + (c & 3) * 4);
+            }
+            return v;
+        }
+    }
+};
+
+// 16 bytes of a row of `width` values, from value `at` on; zero where there
+// are none. VEC: rows are whole 16 bytes, aligned.
+template <class T, bool VEC>
+__device__ __forceinline__ u32x4 row_chunk(const T* __restrict__ row, int at, int width, bool exists) {
+    constexpr int E = 16 / (int)sizeof(T);
+    u32x4 raw = {0, 0, 0, 0};
+    const int left = exists ? width - at : 0;
+    if (VEC) {
+        if (left > 0) raw = *reinterpret_cast<const u32x4*>(row + at);
+    } else if (left >= E) {
+        __builtin_memcpy(&raw, row + at, 16);
+    } else if (left > 0) {
+        T v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = e < left ? row[at + e] : (T)0.0f;
+        __builtin_memcpy(&raw, v, 16);
+    }
+    return raw;
+}
+
+template <class T>
+__device__ __forceinline__ float value_of(u32x4 raw, int i) {
+    T v[16 / sizeof(T)];
+    __builtin_memcpy(v, &raw, 16);
+    return (float)v[i];
+}
+
+template <class T, class L, bool VEC>
+__global__ __launch_bounds__(L::THREADS) void gated_narrow_grads(
+    const T* __restrict__ x, int64_t R, int C, const int64_t* __restrict__ off, int64_t N, const T* __restrict__ weight,
+    const T* __restrict__ bias, int F, int act, const T* __restrict__ g, T* __restrict__ grad_x, bool wide_x, int per,
+    T* __restrict__ grad_weight, T* __restrict__ grad_bias, float* __restrict__ slots, int64_t slot_count) {
+    constexpr int MT = L::MT, E = L::E, PB = L::PB, CB = L::CB;
+    __shared__ alignas(16) char lds[L::kLdsBytes];
+    char *const lds_w = lds, *const lds_d = lds + L::kW, *const lds_x = lds_d + L::kD;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
+    const Piece piece = find_piece(off, N, R, per, (int)blockIdx.x);
+    if (piece.group < 0 || piece.slot >= slot_count) return;
+    const T* w = weight + piece.group * 2 * F * (int64_t)C;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        typename L::W::Held held;
+        L::W::fetch(held, w + p * (int64_t)F * C, C, F, 0, C, tid);
+        L::W::put(lds_w + p * L::W::kBytes, held, tid);
+    }
+    // the biases of this lane's values
+    f32x4 add[2][PB];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int a = 0; a < PB; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int f = L::first_of(a) + L::STRIDE * q + i;
+                add[p][a][i] = bias && f < F ? (float)bias[(piece.group * 2 + p) * F + f] : 0.0f;
+            }
+    f32x4 sum[L::WB][CB], ones[L::WB];
+#pragma unroll
+    for (int b = 0; b < L::WB; ++b) {
+        ones[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < CB; ++c) sum[b][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    u32x4 xs[MT][L::XS], gs[MT][L::PS];
+    const auto load = [&](int from) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int row = from + (wave * MT + m) * 16 + r;
+            const bool exists = row < piece.rows;
+            const T *xr = x + (piece.first + row) * (int64_t)C, *gr = g + (piece.first + row) * (int64_t)F;
+#pragma unroll
+            for (int s = 0; s < L::XS; ++s) xs[m][s] = row_chunk<T, VEC>(xr, L::column(s, lane), C, exists);
+#pragma unroll
+            for (int s = 0; s < L::PS; ++s) gs[m][s] = row_chunk<T, VEC>(gr, L::column(s, lane), F, exists);
+        }
+    };
+    load(0);
+    for (int from = 0; from < piece.rows; from += L::BM) {
+        step_barrier<63>();   // the weight is in LDS; the last rows have been summed
+        f32x4 acc[2][PB][MT];
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int a = 0; a < PB; ++a) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[p][a][m] = add[p][a];
+#pragma unroll
+                for (int s = 0; s < L::XS; ++s) {
+                    const u32x4 wf = L::W::fragment(lds_w + p * L::W::kBytes, s, L::first_of(a), L::STRIDE, lane);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[p][a][m] = mma<T>(wf, xs[m][s], acc[p][a][m]);
+                }
+            }
+        u32x4 back[MT][2][L::PS];
+        with_activation(act, [&](auto&& activation) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int s = 0; s < L::PS; ++s) {
+                    constexpr int B = L::HALF ? 2 : 1;   // blocks of a slice
+                    f32x4 da[B], du[B];
+#pragma unroll
+                    for (int h = 0; h < B; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const Act v = activation(acc[0][s * B + h][m][i]);
+                            const float up = value_of<T>(gs[m][s], 4 * h + i);
+                            da[h][i] = up * acc[1][s * B + h][m][i] * v.slope;
+                            du[h][i] = up * v.value;
+                        }
+                    back[m][0][s] = packed<T>(da[0], da[B - 1]);
+                    back[m][1][s] = packed<T>(du[0], du[B - 1]);
+                }
+        });
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int line = (wave * MT + m) * 16 + r;
+            if (from + line >= piece.rows)   // nothing comes of rows that do not exist
+#pragma unroll
+                for (int s = 0; s < L::PS; ++s) back[m][0][s] = back[m][1][s] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < L::XS; ++s)
+                *reinterpret_cast<u32x4*>(L::template chunk<typename L::X>(lds_x, line, s * 4 + q, L::CP * (int)sizeof(T))) = xs[m][s];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int s = 0; s < L::PS; ++s)
+                    *reinterpret_cast<u32x4*>(L::template chunk<typename L::D>(lds_d, line, (p * L::PS + s) * 4 + q,
+                                                                               2 * L::FP * (int)sizeof(T))) = back[m][p][s];
+        }
+        if (from + L::BM < piece.rows) load(from + L::BM);
+        if (grad_x) {
+            f32x4 out[CB][MT];
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) out[c][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int s = 0; s < L::PS; ++s) {
+                        const u32x4 wf = L::transposed(lds_w + p * L::W::kBytes, s, L::first_of(c), lane);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) out[c][m] = mma<T>(wf, back[m][p][s], out[c][m]);
+                    }
+            }
+            // 64 columns are two pieces of 64 bytes in 16 bits, and four in float32
+            constexpr int STEP = L::HALF ? 2 : 1;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int line = from + (wave * MT + m) * 16;
+                T* rows = grad_x + (piece.first + line) * (int64_t)C;
+#pragma unroll
+                for (int c = 0; c < CB; c += 2 * STEP) {
+                    const u32x4 c0 = packed<T>(out[c][m], out[c + STEP - 1][m]);
+                    const u32x4 c1 = packed<T>(out[c + STEP][m], out[c + 2 * STEP - 1][m]);
+                    const int n0 = c * 16 + q * E, n1 = n0 + 4 * E;
+                    if (wide_x) {
+                        store_row_pairs(c0, c1, lane, [&](bool odd, int second, u32x4 v) {
+                            const int row = (r & ~1) | (odd ? 1 : 0), n = second ? n1 : n0;
+                            if (line + row < piece.rows && n < C) *reinterpret_cast<u32x4*>(rows + row * (int64_t)C + n) = v;
+                        });
+                    } else if (line + r < piece.rows) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < E; ++e)
+                                if ((k ? n1 : n0) + e < C) rows[r * (int64_t)C + (k ? n1 : n0) + e] = (T)value_of<T>(k ? c1 : c0, e);
+                    }
+                }
+            }
+        }
+        step_barrier<63>();   // [da du] and x of all waves are in LDS
+#pragma unroll
+        for (int s = 0; s < L::BM / (4 * E); ++s) {
+            u32x4 xf[CB];
+#pragma unroll
+            for (int c = 0; c < CB; ++c) xf[c] = L::X::fragment(lds_x, s, c * 16, 4, lane);
+#pragma unroll
+            for (int b = 0; b < L::WB; ++b) {
+                const u32x4 df = L::D::fragment(lds_d, s, (wave * L::WB + b) * 16, 4, lane);
+                if constexpr (L::HALF) {
+                    constexpr uint32_t bits = one_bits<T>();
+                    ones[b] = mma<T>(u32x4{bits, bits, bits, bits}, df, ones[b]);
+                } else {
+                    ones[b] += __builtin_bit_cast(f32x4, df);
+                }
+#pragma unroll
+                for (int c = 0; c < CB; ++c) sum[b][c] = mma<T>(xf[c], df, sum[b][c]);
+            }
+        }
+    }
+    // rows f of the weight's gradient, columns c = 16 block + 4 q + i
+    float* slot = piece.slot < 0 ? nullptr : slots + piece.slot * grouped_piece_values(C, 2 * F);
+#pragma unroll
+    for (int b = 0; b < L::WB; ++b) {
+        const int at = (wave * L::WB + b) * 16 + r, p = at / L::FP, f = at % L::FP;
+        float total = ones[b][0];
+        if constexpr (!L::HALF) {
+            total = (ones[b][0] + ones[b][1]) + (ones[b][2] + ones[b][3]);
+            total += __shfl_xor(total, 16, 64);
+            total += __shfl_xor(total, 32, 64);
+        }
+        if (f >= F) continue;
+        const int64_t row = p * (int64_t)F + f;
+        if (grad_weight)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+                const int n = c * 16 + 4 * q;
+                if (slot) store4<float>(slot + row * C, n, C, sum[b][c]);
+                else store4<T>(grad_weight + (piece.group * 2 * F + row) * C, n, C, sum[b][c]);
+            }
+        if (grad_bias && q == 0) {
+            if (slot) slot[2 * (int64_t)F * C + row] = total;
+            else grad_bias[piece.group * 2 * F + row] = (T)total;
+        }
+    }
+}
+
+template <class T, class L>
+hipError_t launch_narrow(const GatedArgs& a, const GroupedPieces& p) {
+    constexpr int each = 16 / (int)sizeof(T);
+    const bool whole = a.C % each == 0, vec = whole && a.F % each == 0 && aligned16(a.x) && aligned16(a.grad_y);
+    const auto kernel = vec ? gated_narrow_grads<T, L, true> : gated_narrow_grads<T, L, false>;
+    kernel<<<(unsigned)(a.R / p.rows + a.N), L::THREADS, 0, a.stream>>>(
+        static_cast<const T*>(a.x), a.R, a.C, a.off, a.N, static_cast<const T*>(a.weight), static_cast<const T*>(a.bias), a.F,
+        a.act, static_cast<const T*>(a.grad_y), static_cast<T*>(a.grad_x), whole && aligned16(a.grad_x), p.rows,
+        static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias), reinterpret_cast<float*>(a.workspace), p.slots);
+    return hipGetLastError();
+}
+
 template <class T, class Tile, bool GRAD>
-hipError_t launch_tile(const GatedArgs& a, T* out, bool vec, bool wide) {
+hipError_t launch_tile(const GatedArgs& a, T* out, bool vec, bool wide_g, bool wide) {
     const int n_tiles = ceil_div(a.F, Tile::COLUMNS);
     const int64_t tiles = most_row_tiles(a.R, a.N, Tile::BM) * n_tiles;
     const unsigned places = run_grid<kRun>(tiles);
@@ -181,10 +569,10 @@ hipError_t launch_tile(const GatedArgs& a, T* out, bool vec, bool wide) {
     const T* g = static_cast<const T*>(a.grad_y);
     if (vec)
         grouped_gated<T, Tile, true, GRAD><<<grid, Tile::THREADS, 0, a.stream>>>(x, a.R, a.C, a.off, a.N, w, bias, a.F, a.act, g,
-                                                                                 out, wide, tiles, n_tiles, places);
+                                                                                 wide_g, out, wide, tiles, n_tiles, places);
     else if constexpr (Tile::BN < 256)   // the largest tiles have no form for unaligned arrays
         grouped_gated<T, Tile, false, GRAD><<<grid, Tile::THREADS, 0, a.stream>>>(x, a.R, a.C, a.off, a.N, w, bias, a.F, a.act, g,
-                                                                                  out, wide, tiles, n_tiles, places);
+                                                                                  wide_g, out, wide, tiles, n_tiles, places);
     return hipGetLastError();
 }
 
@@ -195,29 +583,37 @@ template <class T, bool GRAD>
 hipError_t launch_products(const GatedArgs& a, T* out) {
     constexpr int each = 16 / (int)sizeof(T);
     const bool vec = a.C % each == 0 && aligned16(a.x) && aligned16(a.weight);
-    const bool wide = a.F % each == 0 && aligned16(out);
+    const bool whole = a.F % each == 0, wide = whole && aligned16(out), wide_g = whole && aligned16(a.grad_y);
     const RowsTile t = gated_tile(a.R, a.N, a.F, sizeof(T) == 2, vec);
-    if (t.rows == 16) return launch_tile<T, GatedTile<T, 128, 16, 4, 1, 4>, GRAD>(a, out, vec, wide);
-    if (t.columns == 16) return launch_tile<T, GatedTile<T, 32, 128, 1, 4, 2>, GRAD>(a, out, vec, wide);
+    if (t.rows == 16) return launch_tile<T, GatedTile<T, 128, 16, 4, 1, 4>, GRAD>(a, out, vec, wide_g, wide);
+    if (t.columns == 16) return launch_tile<T, GatedTile<T, 32, 128, 1, 4, 2>, GRAD>(a, out, vec, wide_g, wide);
     if constexpr (sizeof(T) == 2)
-        if (t.columns == 128) return launch_tile<T, GatedTile<T, 256, 256, 2, 4, 2>, GRAD>(a, out, vec, wide);
-    if (t.columns == 32) return launch_tile<T, GatedTile<T, 64, 128, 1, 4, 2>, GRAD>(a, out, vec, wide);
-    return launch_tile<T, GatedTile<T, 128, 128, 2, 4, 2>, GRAD>(a, out, vec, wide);
+        if (t.columns == 128) return launch_tile<T, GatedTile<T, 256, 256, 2, 4, 2>, GRAD>(a, out, vec, wide_g, wide);
+    if (t.columns == 32) return launch_tile<T, GatedTile<T, 64, 128, 1, 4, 2>, GRAD>(a, out, vec, wide_g, wide);
+    return launch_tile<T, GatedTile<T, 128, 128, 2, 4, 2>, GRAD>(a, out, vec, wide_g, wide);
 }
 
 template <class T>
 hipError_t launch_typed(const GatedArgs& a, bool backward) {
     if (!backward) return launch_products<T, false>(a, static_cast<T*>(a.y));
+    GroupedLinearArgs b{};
+    b.x = a.x; b.R = a.R; b.cin = a.C; b.off = a.off; b.N = a.N; b.weight = a.weight; b.cout = 2 * a.F; b.dtype = a.dtype;
+    b.grad_x = a.grad_x; b.grad_weight = a.grad_weight; b.grad_bias = a.grad_bias; b.stream = a.stream;
+    if (gated_narrow(a.C, a.F)) {
+        const GroupedPieces p = gated_pieces(a.R, a.N, a.C, a.F, sizeof(T) == 2);
+        const hipError_t err = a.F <= 64 ? launch_narrow<T, Narrow<T, 64, sizeof(T) == 2 ? 2 : 1>>(a, p)
+                                         : launch_narrow<T, Narrow<T, 128, 1>>(a, p);
+        if (err != hipSuccess || p.slots == 0 || !(a.grad_weight || a.grad_bias)) return err;
+        b.workspace = reinterpret_cast<float*>(a.workspace);
+        return launch_grouped_add_pieces(b, p);
+    }
     if (a.R > 0) {
         const hipError_t err = launch_products<T, true>(a, reinterpret_cast<T*>(a.workspace));
         if (err != hipSuccess) return err;
     }
     // [da du] as the upstream gradient of a linear layer of 2 F outputs
-    GroupedLinearArgs b{};
-    b.x = a.x; b.R = a.R; b.cin = a.C; b.off = a.off; b.N = a.N; b.weight = a.weight; b.cout = 2 * a.F; b.dtype = a.dtype;
-    b.grad_y = a.workspace; b.grad_x = a.grad_x; b.grad_weight = a.grad_weight; b.grad_bias = a.grad_bias;
+    b.grad_y = a.workspace;
     b.workspace = reinterpret_cast<float*>(a.workspace + gated_rows_bytes(a.R, a.F, a.dtype));
-    b.stream = a.stream;
     return launch_grouped_linear_backward(b);
 }
 
@@ -233,6 +629,26 @@ RowsTile gated_tile(int64_t R, int64_t N, int32_t F, bool half, bool vec) {
     if (half && vec && F > 64 && R >= 512 * N && tiles(128, 256) >= 224) return {128, 256};
     if (F <= 32 || tiles(64, 128) < 256) return {32, 128};
     return {64, 128};
+}
+
+bool gated_narrow(int32_t C, int32_t F) { return C <= 64 && F <= 128; }
+
+// Pieces for as many workgroups as the device holds at a time (two on a
+// compute unit, or one), of at least 512 rows.
+GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
+    if (!gated_narrow(C, F)) return grouped_pieces(R, N, C, 2 * F, half);
+    const int64_t want = half || F <= 64 ? 512 : 256;
+    int64_t rows = (R + want - 1) / want;
+    rows = (rows + 127) / 128 * 128;
+    rows = rows < 512 ? 512 : rows > 8192 ? 8192 : rows;
+    if (R <= 1024) rows = 1024;   // short enough to need no second launch
+    return {(int)rows, 64, R > rows ? 2 * (R / rows) : 0};
+}
+
+size_t gated_workspace(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype) {
+    const GroupedPieces p = gated_pieces(R, N, C, F, dtype != DMR_FLOAT32);
+    const size_t sums = align_up((size_t)(p.slots * grouped_piece_values(C, 2 * F)) * sizeof(float) + 256, 256);
+    return sums + (gated_narrow(C, F) ? 0 : gated_rows_bytes(R, F, dtype));
 }
 
 hipError_t launch_gated(const GatedArgs& a, bool backward) {

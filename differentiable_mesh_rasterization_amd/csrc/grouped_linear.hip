@@ -14,10 +14,6 @@
 namespace dmr {
 namespace {
 
-// Of the weight gradient's tiles, whose lengths differ, a die is given shorter
-// runs at a time, so that the dies end together.
-constexpr int kPieceRun = 8;
-
 // y = x W^T + b (WK: the weight's contiguous direction is summed over) or
 // grad_x = g W (!WK), row tile by row tile. `n_out` is the width of `out`,
 // `k_in` that of `rows_in`; the weight of a group is [n_out][k_in] if WK and
@@ -36,7 +32,8 @@ __device__ __forceinline__ void rows_of_workgroup(char* lds, uint32_t block, uin
             const T* w = weight + at.group * (int64_t)n_out * k_in + (WK ? (int64_t)n0 * k_in : (int64_t)n0);
             return typename Tile::Source{w, WK ? k_in : n_out, n_out - n0};
         },
-        [&](Tile& t, const RowTile& at, int n0) {
+        [](const RowTile&, int) { return 0; },
+        [&](Tile& t, const RowTile& at, int n0, int) {
             store_tile<T, Tile>(t, out + at.first * (int64_t)n_out, n_out, at.rows, n0, n_out,
                                 bias ? bias + at.group * (int64_t)n_out : nullptr, wide, tid);
         });
@@ -56,68 +53,6 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_rows(const T* __restric
 // ---------------------------------------------------------------------------
 // gradient of the weights: a product over each group's rows
 // ---------------------------------------------------------------------------
-// A group of more than `per` rows is cut into equal pieces of at most that
-// many. A group of one piece (or none) is written directly; the pieces of
-// longer groups go to the workspace in float32, each to a slot of its own, and
-// are added in order afterwards: no atomics, so the result does not depend on
-// timing.
-
-struct Piece {
-    int64_t group, first;   // group < 0: no such piece
-    int rows;
-    int64_t slot;           // < 0: the group's only piece
-};
-
-// The pieces of a group of `rows` rows, and their length (the last may be
-// shorter), a multiple of 64 rows.
-__device__ __forceinline__ int pieces_of(int64_t rows, int per, int& length) {
-    const int64_t n = rows > per ? (rows + per - 1) / per : 1;
-    length = (int)((rows + n * 64 - 1) / (n * 64) * 64);
-    return rows > per ? (int)((rows + length - 1) / length) : 1;
-}
-
-// Piece t of all groups'. Every wave does the same work. Up to 64 groups, the
-// pieces are taken longest first, so that what the device finishes with is
-// short: lane g compares its group's piece with every other's.
-__device__ __forceinline__ Piece find_piece(const int64_t* __restrict__ off, int64_t N, int64_t R, int per, int t) {
-    const int lane = threadIdx.x & 63;
-    int before = 0, slots_before = 0;
-    for (int64_t base = 0; base < N; base += 64) {
-        int64_t lo, hi;
-        group_bounds(off, N, R, base + lane, lo, hi);
-        int length = 0;
-        const int pieces = base + lane < N ? pieces_of(hi - lo, per, length) : 0;
-        const int slots = pieces > 1 ? pieces : 0;
-        const int slots_upto = slots_before + wave_inclusive_sum(slots, lane);
-        int first_of;   // this group's first piece in the order
-        if (N <= 64) {
-            first_of = 0;
-            for (int g = 0; g < (int)N; ++g) {
-                const int l = __builtin_amdgcn_readlane(length, g), n = __builtin_amdgcn_readlane(pieces, g);
-                if (l > length || (l == length && g < lane)) first_of += n;
-            }
-        } else {
-            first_of = before + wave_inclusive_sum(pieces, lane) - pieces;
-        }
-        const uint64_t hit = __ballot(first_of <= t && t < first_of + pieces);
-        if (hit) {
-            const int src = __builtin_ctzll(hit);
-            const int k = t - first_of;
-            const int64_t first = lo + (int64_t)k * length;
-            const int64_t left = hi - first;
-            Piece r;
-            r.group = base + src;
-            r.first = uniform64(__shfl(first, src, 64));
-            r.rows = __builtin_amdgcn_readlane((int)(left < length ? left : length), src);
-            r.slot = __builtin_amdgcn_readlane(pieces > 1 ? slots_upto - slots + k : -1, src);
-            return r;
-        }
-        before = __builtin_amdgcn_readlane(first_of + pieces, 63);
-        slots_before = __builtin_amdgcn_readlane(slots_upto, 63);
-    }
-    return {-1, 0, 0, -1};
-}
-
 template <class T, class Tile, bool VEC>
 __device__ __forceinline__ void weight_grad_of_workgroup(
     char* lds, uint32_t block, const T* __restrict__ x, const T* __restrict__ g, int64_t R, int cin, int cout,
@@ -403,6 +338,16 @@ int64_t add_blocks(int64_t values) {
 }
 
 template <class T>
+hipError_t add_pieces(const GroupedLinearArgs& a, const GroupedPieces& p) {
+    const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout, blocks = add_blocks(values);
+    const auto add = add_split(values) ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
+    add<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), size,
+                                                        a.workspace, p.slots, (unsigned)blocks, static_cast<T*>(a.grad_weight),
+                                                        static_cast<T*>(a.grad_bias));
+    return hipGetLastError();
+}
+
+template <class T>
 hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
     const T* bias = static_cast<const T*>(a.bias);
     const bool in16 = a.cin % (16 / sizeof(T)) == 0, out16 = a.cout % (16 / sizeof(T)) == 0;   // rows of whole 16 bytes
@@ -438,12 +383,7 @@ hipError_t launch_all(const GroupedLinearArgs& a, bool backward) {
                              : launch_weight_tile<T, TileProduct<T, 128, 128, 2, 2, false, false, 2, true>>(a, p, vec_weights,
                                                                                                            wide_w);
         if (err == hipSuccess && p.slots > 0) {
-            const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout, blocks = add_blocks(values);
-            const auto add = add_split(values) ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
-            add<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(
-                a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), size, a.workspace, p.slots,
-                (unsigned)blocks, static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
-            err = hipGetLastError();
+            err = add_pieces<T>(a, p);
         }
     }
     timing_end(kKGroupedLinearBwd, a.stream);
@@ -528,6 +468,14 @@ bool grouped_sums_fit(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half
     return p.slots == 0 || add_blocks((int64_t)cin * cout + cout) * N <= kMaxWorkItems / 256;
 }
 
+hipError_t launch_grouped_add_pieces(const GroupedLinearArgs& a, const GroupedPieces& p) {
+    switch (a.dtype) {
+        case DMR_FLOAT32: return add_pieces<float>(a, p);
+        case DMR_FLOAT16: return add_pieces<_Float16>(a, p);
+        case DMR_BFLOAT16: return add_pieces<__bf16>(a, p);
+    }
+    return hipErrorInvalidValue;
+}
 hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a) { return launch_typed(a, false); }
 hipError_t launch_grouped_linear_backward(const GroupedLinearArgs& a) { return launch_typed(a, true); }
 

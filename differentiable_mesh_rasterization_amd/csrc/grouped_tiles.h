@@ -175,12 +175,14 @@ __device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, i
 }
 
 // Products of the rows of `rows_in` (k_in wide) with weights(tile, column) over
-// a workgroup's tiles of rows, each handed to store(product, tile, column).
-template <class T, class Tile, bool VEC, class Weights, class Store>
+// a workgroup's tiles of rows, each handed to store(product, tile, column,
+// held), held = load(tile, column): what a store needs from memory, asked for
+// ahead of the next tile's loads.
+template <class T, class Tile, bool VEC, class Weights, class Load, class Store>
 __device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32_t blocks, const T* __restrict__ rows_in,
                                                int64_t R, int k_in, const int64_t* __restrict__ off, int64_t N,
                                                int64_t tiles, int n_tiles, uint32_t places, Weights&& weights,
-                                               Store&& store) {
+                                               Load&& load, Store&& store) {
     const int tid = threadIdx.x;
     const auto find = [&](uint32_t place) {
         const int64_t id = tile_of_workgroup<kRun>(place);
@@ -203,11 +205,81 @@ __device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32
         const int next_n0 = column(place);
         Tile t;
         t.template finish<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
+        const auto held = load(at, n0);
         if (next.group >= 0) Tile::template begin<VEC>(lds, weights(next, next_n0), rows_of(next), k_in, tid);
-        store(t, at, n0);
+        store(t, at, n0, held);
         at = next;
         n0 = next_n0;
     }
+}
+
+// ---------------------------------------------------------------------------
+// sums over a group's rows
+// ---------------------------------------------------------------------------
+// Of the weight gradient's tiles, whose lengths differ, a die is given shorter
+// runs at a time, so that the dies end together.
+constexpr int kPieceRun = 8;
+
+// A group of more than `per` rows is cut into equal pieces of at most that
+// many. A group of one piece (or none) is written directly; the pieces of
+// longer groups go to the workspace in float32, each to a slot of its own, and
+// are added in order afterwards: no atomics, so the result does not depend on
+// timing.
+
+struct Piece {
+    int64_t group, first;   // group < 0: no such piece
+    int rows;
+    int64_t slot;           // < 0: the group's only piece
+};
+
+// The pieces of a group of `rows` rows, and their length (the last may be
+// shorter), a multiple of 64 rows.
+__device__ __forceinline__ int pieces_of(int64_t rows, int per, int& length) {
+    const int64_t n = rows > per ? (rows + per - 1) / per : 1;
+    length = (int)((rows + n * 64 - 1) / (n * 64) * 64);
+    return rows > per ? (int)((rows + length - 1) / length) : 1;
+}
+
+// Piece t of all groups'. Every wave does the same work. Up to 64 groups, the
+// pieces are taken longest first, so that what the device finishes with is
+// short: lane g compares its group's piece with every other's.
+__device__ __forceinline__ Piece find_piece(const int64_t* __restrict__ off, int64_t N, int64_t R, int per, int t) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, slots_before = 0;
+    for (int64_t base = 0; base < N; base += 64) {
+        int64_t lo, hi;
+        group_bounds(off, N, R, base + lane, lo, hi);
+        int length = 0;
+        const int pieces = base + lane < N ? pieces_of(hi - lo, per, length) : 0;
+        const int slots = pieces > 1 ? pieces : 0;
+        const int slots_upto = slots_before + wave_inclusive_sum(slots, lane);
+        int first_of;   // this group's first piece in the order
+        if (N <= 64) {
+            first_of = 0;
+            for (int g = 0; g < (int)N; ++g) {
+                const int l = __builtin_amdgcn_readlane(length, g), n = __builtin_amdgcn_readlane(pieces, g);
+                if (l > length || (l == length && g < lane)) first_of += n;
+            }
+        } else {
+            first_of = before + wave_inclusive_sum(pieces, lane) - pieces;
+        }
+        const uint64_t hit = __ballot(first_of <= t && t < first_of + pieces);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            const int k = t - first_of;
+            const int64_t first = lo + (int64_t)k * length;
+            const int64_t left = hi - first;
+            Piece r;
+            r.group = base + src;
+            r.first = uniform64(__shfl(first, src, 64));
+            r.rows = __builtin_amdgcn_readlane((int)(left < length ? left : length), src);
+            r.slot = __builtin_amdgcn_readlane(pieces > 1 ? slots_upto - slots + k : -1, src);
+            return r;
+        }
+        before = __builtin_amdgcn_readlane(first_of + pieces, 63);
+        slots_before = __builtin_amdgcn_readlane(slots_upto, 63);
+    }
+    return {-1, 0, 0, -1};
 }
 
 // ---------------------------------------------------------------------------
