@@ -21,41 +21,39 @@
 namespace dmr {
 namespace {
 
-// Activation and derivative. 1 / (1 + e^-z) and 1 minus it are formed so that
-// neither loses digits to the other; e^-z passes float32's range harmlessly
-// (1 / inf = 0).
+// Activation and derivative. With the logistic function s of z, e^-z may pass
+// float32's range (1 / inf = 0 then). 1 - s is off by 2^-24 at most, which the
+// derivative a s (1 - s) z' + s is of itself, for a z' is at most as large as
+// the argument's own error makes of it.
 struct Act {
     float value, slope;
 };
 
-__device__ __forceinline__ void logistic(float z, float& s, float& rest) {
-    const float t = __builtin_amdgcn_exp2f(z * -1.44269504f);
-    s = __builtin_amdgcn_rcpf(1.0f + t);
-    rest = z >= 0.0f ? t * s : 1.0f - s;   // t may be infinite below zero
+// s of z = -log2(e) z_scaled.
+__device__ __forceinline__ float logistic2(float z_scaled) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z_scaled));
 }
+constexpr float kLog2e = 1.44269504f;
 
 template <int KIND>
 __device__ __forceinline__ Act activate(float a);
 template <>
 __device__ __forceinline__ Act activate<DMR_SILU>(float a) {
-    float s, rest;
-    logistic(a, s, rest);
-    return {a * s, __builtin_fmaf(a * s, rest, s)};
+    const float s = logistic2(a * -kLog2e), v = a * s;
+    return {v, __builtin_fmaf(v, 1.0f - s, s)};
 }
 template <>
 __device__ __forceinline__ Act activate<DMR_SIGMOID>(float a) {
-    float s, rest;
-    logistic(a, s, rest);
-    return {s, s * rest};
+    const float s = logistic2(a * -kLog2e);
+    return {s, s * (1.0f - s)};
 }
 template <>
 __device__ __forceinline__ Act activate<DMR_GELU_TANH>(float a) {
     // (1 + tanh z) / 2 is the logistic function of 2 z, z = k (a + c a^3)
     constexpr float k2 = 1.59576912f, c = 0.044715f;   // 2 sqrt(2 / pi)
     const float aa = a * a;
-    float s, rest;
-    logistic(k2 * a * __builtin_fmaf(c, aa, 1.0f), s, rest);
-    return {a * s, __builtin_fmaf(a * s * rest, k2 * __builtin_fmaf(3.0f * c, aa, 1.0f), s)};
+    const float s = logistic2(a * __builtin_fmaf(-kLog2e * k2 * c, aa, -kLog2e * k2)), v = a * s;
+    return {v, __builtin_fmaf(v * (1.0f - s), __builtin_fmaf(3.0f * k2 * c, aa, k2), s)};
 }
 template <>
 __device__ __forceinline__ Act activate<DMR_GELU>(float a) {
@@ -269,15 +267,23 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
 // in memory, moves 4 C + 7 F.
 //
 // What bounds it: memory (16-bit) and the float32 products (float32).
-template <class T, int FP_, int MT_>
+//
+// SPLIT: two waves share 16 MT rows, each with half of the columns: of a and u
+// first, of grad_x afterwards, for which they read each other's [da du] from
+// LDS. Where the LDS holds one workgroup, it has eight waves that way.
+template <class T, int FP_, int MT_, bool SPLIT_>
 struct Narrow {
-    static constexpr int FP = FP_, MT = MT_, CP = 64, THREADS = 256, BM = 64 * MT;
+    static constexpr int FP = FP_, MT = MT_, CP = 64, BM = 64 * MT;
+    static constexpr bool SPLIT = SPLIT_;
+    static constexpr int SHARES = SPLIT ? 2 : 1, THREADS = 256 * SHARES;
     static constexpr bool HALF = sizeof(T) == 2;
     static constexpr int E = 16 / (int)sizeof(T);     // values of 16 bytes
     static constexpr int XS = CP / (4 * E);           // 64-byte slices of x's row, and of
     static constexpr int PS = FP / (4 * E);           // a plane's
-    static constexpr int PB = FP / 16, CB = CP / 16;  // blocks of 16
-    static constexpr int WB = 2 * FP / 64;            // blocks of a wave's share of the weight's rows
+    static constexpr int CB = CP / 16;                // blocks of 16 columns
+    // a wave's blocks and slices of a plane's columns, blocks of grad_x's, and
+    // of the weight's rows
+    static constexpr int PB = FP / 16 / SHARES, PW = PS / SHARES, GB = CB / SHARES, WB = 2 * FP / 64 / SHARES;
     using W = OperandTile<T, FP, true, THREADS, CP * (int)sizeof(T)>;
     using D = OperandTile<T, 2 * FP, false, THREADS>;
     using X = OperandTile<T, CP, false, THREADS>;
@@ -325,22 +331,49 @@ struct Narrow {
     }
 };
 
-// 16 bytes of a row of `width` values, from value `at` on; zero where there
-// are none. VEC: rows are whole 16 bytes, aligned.
-template <class T, bool VEC>
-__device__ __forceinline__ u32x4 row_chunk(const T* __restrict__ row, int at, int width, bool exists) {
-    constexpr int E = 16 / (int)sizeof(T);
-    u32x4 raw = {0, 0, 0, 0};
-    const int left = exists ? width - at : 0;
-    if (VEC) {
-        if (left > 0) raw = *reinterpret_cast<const u32x4*>(row + at);
-    } else if (left >= E) {
-        __builtin_memcpy(&raw, row + at, 16);
-    } else if (left > 0) {
-        T v[E];
+// Values n .. n + 3 of N; zero where there are none.
+template <class T>
+__device__ __forceinline__ f32x4 load4(const T* __restrict__ from, int n, int N) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n + 4 <= N) {
+        T t[4];
+        __builtin_memcpy(t, from + n, sizeof(t));
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = e < left ? row[at + e] : (T)0.0f;
-        __builtin_memcpy(&raw, v, 16);
+        for (int i = 0; i < 4; ++i) v[i] = (float)t[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < N) v[i] = (float)from[n + i];
+    }
+    return v;
+}
+
+// 16 bytes of row `row` of a [R, width] array, from value `at` on; zero where
+// there are none. VEC: rows are whole 16 bytes, aligned. Others are read past
+// the row's end where the array goes on, and what is past it is masked: lanes
+// that take different ways would wait for each in turn.
+template <class T, bool VEC>
+__device__ __forceinline__ u32x4 row_chunk(const T* __restrict__ rows, int64_t R, int64_t row, int at, int width, bool exists) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const T* from = rows + row * width + at;
+    const int left = exists ? width - at : 0;
+    u32x4 raw = {0, 0, 0, 0};
+    if (VEC) {
+        if (left > 0) raw = *reinterpret_cast<const u32x4*>(from);
+    } else if (left > 0) {
+        if ((R - row) * width - at >= E) {
+            __builtin_memcpy(&raw, from, 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // of dword j, the bytes that are the row's
+                const int bytes = left * (int)sizeof(T) - 4 * j;
+                raw[j] = bytes >= 4 ? raw[j] : bytes <= 0 ? 0u : raw[j] & 0xFFFFu;
+            }
+        } else {
+            T v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = e < left ? from[e] : (T)0.0f;
+            __builtin_memcpy(&raw, v, 16);
+        }
     }
     return raw;
 }
@@ -353,7 +386,7 @@ __device__ __forceinline__ float value_of(u32x4 raw, int i) {
 }
 
 template <class T, class L, bool VEC>
-__global__ __launch_bounds__(L::THREADS) void gated_narrow_grads(
+__global__ __launch_bounds__(L::THREADS, 2) void gated_narrow_grads(
     const T* __restrict__ x, int64_t R, int C, const int64_t* __restrict__ off, int64_t N, const T* __restrict__ weight,
     const T* __restrict__ bias, int F, int act, const T* __restrict__ g, T* __restrict__ grad_x, bool wide_x, int per,
     T* __restrict__ grad_weight, T* __restrict__ grad_bias, float* __restrict__ slots, int64_t slot_count) {
@@ -361,26 +394,18 @@ __global__ __launch_bounds__(L::THREADS) void gated_narrow_grads(
     __shared__ alignas(16) char lds[L::kLdsBytes];
     char *const lds_w = lds, *const lds_d = lds + L::kW, *const lds_x = lds_d + L::kD;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
+    // its 16 MT rows and its share of their columns
+    const int first_row = wave % 4 * MT * 16, share = L::SPLIT ? wave / 4 : 0;
     const Piece piece = find_piece(off, N, R, per, (int)blockIdx.x);
     if (piece.group < 0 || piece.slot >= slot_count) return;
     const T* w = weight + piece.group * 2 * F * (int64_t)C;
+    const T* bias_n = bias ? bias + piece.group * 2 * F : nullptr;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         typename L::W::Held held;
         L::W::fetch(held, w + p * (int64_t)F * C, C, F, 0, C, tid);
         L::W::put(lds_w + p * L::W::kBytes, held, tid);
     }
-    // the biases of this lane's values
-    f32x4 add[2][PB];
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int a = 0; a < PB; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int f = L::first_of(a) + L::STRIDE * q + i;
-                add[p][a][i] = bias && f < F ? (float)bias[(piece.group * 2 + p) * F + f] : 0.0f;
-            }
     f32x4 sum[L::WB][CB], ones[L::WB];
 #pragma unroll
     for (int b = 0; b < L::WB; ++b) {
@@ -388,42 +413,61 @@ __global__ __launch_bounds__(L::THREADS) void gated_narrow_grads(
 #pragma unroll
         for (int c = 0; c < CB; ++c) sum[b][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    u32x4 xs[MT][L::XS], gs[MT][L::PS];
-    const auto load = [&](int from) {
+    // This lane's parts of its rows, asked for an iteration ahead, as soon as
+    // the last ones are used.
+    u32x4 xs[MT][L::XS], gs[MT][L::PW];
+    const auto load_x = [&](u32x4 (&to)[MT][L::XS], int from) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int row = from + (wave * MT + m) * 16 + r;
-            const bool exists = row < piece.rows;
-            const T *xr = x + (piece.first + row) * (int64_t)C, *gr = g + (piece.first + row) * (int64_t)F;
+            const int row = from + first_row + m * 16 + r;
 #pragma unroll
-            for (int s = 0; s < L::XS; ++s) xs[m][s] = row_chunk<T, VEC>(xr, L::column(s, lane), C, exists);
-#pragma unroll
-            for (int s = 0; s < L::PS; ++s) gs[m][s] = row_chunk<T, VEC>(gr, L::column(s, lane), F, exists);
+            for (int s = 0; s < L::XS; ++s)
+                to[m][s] = row_chunk<T, VEC>(x, R, piece.first + row, L::column(s, lane), C, row < piece.rows);
         }
     };
-    load(0);
+    const auto load_g = [&](u32x4 (&to)[MT][L::PW], int from) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int row = from + first_row + m * 16 + r;
+#pragma unroll
+            for (int s = 0; s < L::PW; ++s)
+                to[m][s] = row_chunk<T, VEC>(g, R, piece.first + row, L::column(share * L::PW + s, lane), F, row < piece.rows);
+        }
+    };
+    load_x(xs, 0);
+    load_g(gs, 0);
     for (int from = 0; from < piece.rows; from += L::BM) {
+        const bool more = from + L::BM < piece.rows;
         step_barrier<63>();   // the weight is in LDS; the last rows have been summed
         f32x4 acc[2][PB][MT];
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int a = 0; a < PB; ++a) {
+                const f32x4 add = load4<T>(bias_n + p * F, L::first_of(share * PB + a) + L::STRIDE * q, bias ? F : 0);   // not held: registers are short
 #pragma unroll
-                for (int m = 0; m < MT; ++m) acc[p][a][m] = add[p][a];
+                for (int m = 0; m < MT; ++m) acc[p][a][m] = add;
 #pragma unroll
                 for (int s = 0; s < L::XS; ++s) {
-                    const u32x4 wf = L::W::fragment(lds_w + p * L::W::kBytes, s, L::first_of(a), L::STRIDE, lane);
+                    const u32x4 wf = L::W::fragment(lds_w + p * L::W::kBytes, s, L::first_of(share * PB + a), L::STRIDE, lane);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) acc[p][a][m] = mma<T>(wf, xs[m][s], acc[p][a][m]);
                 }
             }
-        u32x4 back[MT][2][L::PS];
+        if (share == 0)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int s = 0; s < L::XS; ++s)
+                    *reinterpret_cast<u32x4*>(L::template chunk<typename L::X>(lds_x, first_row + m * 16 + r, s * 4 + q,
+                                                                               L::CP * (int)sizeof(T))) = xs[m][s];
+        if (more) load_x(xs, from + L::BM);
+        u32x4 back[MT][2][L::PW];
         with_activation(act, [&](auto&& activation) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int s = 0; s < L::PS; ++s) {
+                for (int s = 0; s < L::PW; ++s) {
                     constexpr int B = L::HALF ? 2 : 1;   // blocks of a slice
                     f32x4 da[B], du[B];
 #pragma unroll
@@ -441,63 +485,81 @@ __global__ __launch_bounds__(L::THREADS) void gated_narrow_grads(
         });
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int line = (wave * MT + m) * 16 + r;
+            const int line = first_row + m * 16 + r;
             if (from + line >= piece.rows)   // nothing comes of rows that do not exist
 #pragma unroll
-                for (int s = 0; s < L::PS; ++s) back[m][0][s] = back[m][1][s] = u32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < L::XS; ++s)
-                *reinterpret_cast<u32x4*>(L::template chunk<typename L::X>(lds_x, line, s * 4 + q, L::CP * (int)sizeof(T))) = xs[m][s];
+                for (int s = 0; s < L::PW; ++s) back[m][0][s] = back[m][1][s] = u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int s = 0; s < L::PS; ++s)
-                    *reinterpret_cast<u32x4*>(L::template chunk<typename L::D>(lds_d, line, (p * L::PS + s) * 4 + q,
+                for (int s = 0; s < L::PW; ++s)
+                    *reinterpret_cast<u32x4*>(L::template chunk<typename L::D>(lds_d, line, (p * L::PS + share * L::PW + s) * 4 + q,
                                                                                2 * L::FP * (int)sizeof(T))) = back[m][p][s];
         }
-        if (from + L::BM < piece.rows) load(from + L::BM);
-        if (grad_x) {
-            f32x4 out[CB][MT];
+        if (more) load_g(gs, from + L::BM);
+        // grad_x of this wave's rows, back(m, p, s) the operand
+        const auto rows_gradient = [&](auto&& back_of) {
+            if (!grad_x) return;
+            f32x4 out[L::GB][MT];
 #pragma unroll
-            for (int c = 0; c < CB; ++c) {
+            for (int c = 0; c < L::GB; ++c) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) out[c][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int s = 0; s < L::PS; ++s) {
-                        const u32x4 wf = L::transposed(lds_w + p * L::W::kBytes, s, L::first_of(c), lane);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) out[c][m] = mma<T>(wf, back[m][p][s], out[c][m]);
-                    }
             }
-            // 64 columns are two pieces of 64 bytes in 16 bits, and four in float32
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int s = 0; s < L::PS; ++s) {
+                    u32x4 rows[MT];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) rows[m] = back_of(m, p, s);
+#pragma unroll
+                    for (int c = 0; c < L::GB; ++c) {
+                        const u32x4 wf = L::transposed(lds_w + p * L::W::kBytes, s, L::first_of(share * L::GB + c), lane);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) out[c][m] = mma<T>(wf, rows[m], out[c][m]);
+                    }
+                }
             constexpr int STEP = L::HALF ? 2 : 1;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const int line = from + (wave * MT + m) * 16;
+                const int line = from + first_row + m * 16;
                 T* rows = grad_x + (piece.first + line) * (int64_t)C;
-#pragma unroll
-                for (int c = 0; c < CB; c += 2 * STEP) {
-                    const u32x4 c0 = packed<T>(out[c][m], out[c + STEP - 1][m]);
-                    const u32x4 c1 = packed<T>(out[c + STEP][m], out[c + 2 * STEP - 1][m]);
-                    const int n0 = c * 16 + q * E, n1 = n0 + 4 * E;
+                const auto put = [&](int row, int n, u32x4 v) {
+                    if (line + row >= piece.rows) return;
+                    T* to = rows + row * (int64_t)C + n;
                     if (wide_x) {
+                        if (n < C) *reinterpret_cast<u32x4*>(to) = v;
+                    } else if (n + E <= C) {
+                        __builtin_memcpy(to, &v, 16);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (n + e < C) to[e] = (T)value_of<T>(v, e);
+                    }
+                };
+#pragma unroll
+                for (int c = 0; c < L::GB; c += 2 * STEP) {
+                    const u32x4 c0 = packed<T>(out[c][m], out[c + STEP - 1][m]);
+                    const int n0 = (share * L::GB + c) * 16 + q * E;
+                    if constexpr (L::GB >= 2 * STEP) {
+                        const u32x4 c1 = packed<T>(out[c + STEP][m], out[c + 2 * STEP - 1][m]);
                         store_row_pairs(c0, c1, lane, [&](bool odd, int second, u32x4 v) {
-                            const int row = (r & ~1) | (odd ? 1 : 0), n = second ? n1 : n0;
-                            if (line + row < piece.rows && n < C) *reinterpret_cast<u32x4*>(rows + row * (int64_t)C + n) = v;
+                            put((r & ~1) | (odd ? 1 : 0), second ? n0 + 4 * E : n0, v);
                         });
-                    } else if (line + r < piece.rows) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int e = 0; e < E; ++e)
-                                if ((k ? n1 : n0) + e < C) rows[r * (int64_t)C + (k ? n1 : n0) + e] = (T)value_of<T>(k ? c1 : c0, e);
+                    } else {
+                        put(r, n0, c0);
                     }
                 }
             }
-        }
+        };
+        if constexpr (!L::SPLIT) rows_gradient([&](int m, int p, int s) { return back[m][p][s]; });
         step_barrier<63>();   // [da du] and x of all waves are in LDS
+        if constexpr (L::SPLIT)
+            rows_gradient([&](int m, int p, int s) {
+                return *reinterpret_cast<const u32x4*>(L::template chunk<typename L::D>(
+                    lds_d, first_row + m * 16 + r, (p * L::PS + s) * 4 + q, 2 * L::FP * (int)sizeof(T)));
+            });
 #pragma unroll
         for (int s = 0; s < L::BM / (4 * E); ++s) {
             u32x4 xf[CB];
@@ -601,8 +663,8 @@ hipError_t launch_typed(const GatedArgs& a, bool backward) {
     b.grad_x = a.grad_x; b.grad_weight = a.grad_weight; b.grad_bias = a.grad_bias; b.stream = a.stream;
     if (gated_narrow(a.C, a.F)) {
         const GroupedPieces p = gated_pieces(a.R, a.N, a.C, a.F, sizeof(T) == 2);
-        const hipError_t err = a.F <= 64 ? launch_narrow<T, Narrow<T, 64, sizeof(T) == 2 ? 2 : 1>>(a, p)
-                                         : launch_narrow<T, Narrow<T, 128, 1>>(a, p);
+        const hipError_t err = a.F <= 64 ? launch_narrow<T, Narrow<T, 64, sizeof(T) == 2 ? 2 : 1, false>>(a, p)
+                                         : launch_narrow<T, Narrow<T, 128, 1, true>>(a, p);
         if (err != hipSuccess || p.slots == 0 || !(a.grad_weight || a.grad_bias)) return err;
         b.workspace = reinterpret_cast<float*>(a.workspace);
         return launch_grouped_add_pieces(b, p);
@@ -634,14 +696,13 @@ RowsTile gated_tile(int64_t R, int64_t N, int32_t F, bool half, bool vec) {
 bool gated_narrow(int32_t C, int32_t F) { return C <= 64 && F <= 128; }
 
 // Pieces for as many workgroups as the device holds at a time (two on a
-// compute unit, or one), of at least 512 rows.
+// compute unit, or one), of at least 128 rows.
 GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
     if (!gated_narrow(C, F)) return grouped_pieces(R, N, C, 2 * F, half);
     const int64_t want = half || F <= 64 ? 512 : 256;
     int64_t rows = (R + want - 1) / want;
     rows = (rows + 127) / 128 * 128;
-    rows = rows < 512 ? 512 : rows > 8192 ? 8192 : rows;
-    if (R <= 1024) rows = 1024;   // short enough to need no second launch
+    rows = rows < 128 ? 128 : rows > 8192 ? 8192 : rows;
     return {(int)rows, 64, R > rows ? 2 * (R / rows) : 0};
 }
 

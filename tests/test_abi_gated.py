@@ -62,8 +62,12 @@ def test_gated_layer_with_nothing_to_do_is_a_no_op(dmr):
 
 def test_gated_workspace_sizes(dmr):
     size, linear = dmr.dmr_grouped_gated_linear_workspace_size, dmr.dmr_grouped_linear_workspace_size
-    for R, N, cin, cout, dtype, each in ((1000, 3, 64, 40, torch.bfloat16, 2), (50000, 3, 37, 19, torch.float32, 4)):
+    # the gradients of both products for every row, and the sums of a linear layer of twice the outputs
+    for R, N, cin, cout, dtype, each in ((1000, 3, 72, 40, torch.bfloat16, 2), (50000, 3, 37, 129, torch.float32, 4)):
         assert size(R, N, cin, cout, dtype) >= R * 2 * cout * each + linear(R, N, cin, 2 * cout, dtype)
+    # narrow layers: sums of pieces alone, a group of r > 128 rows has at most 2 r / 128
+    assert 0 < size(100, 3, 64, 128, torch.float32) <= 512
+    assert 2 * (2 * 64 * 65) * 4 <= size(1 << 20, 4, 64, 64, torch.bfloat16) < (1 << 20) * 2 * 64 * 2
     assert size(-1, 2, 8, 4, torch.float32) == 0 and size(10, 2, 8, 4, torch.float64) == 0
     assert size(10, 2, 8, 1 << 20, torch.float32) == 0
 
