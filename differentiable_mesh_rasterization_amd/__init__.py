@@ -53,7 +53,7 @@ EXPORTED = [
     "dmr_grouped_linear_plan", "dmr_orthogonalize", "dmr_orthogonalize_workspace_size", "dmr_orthogonalize_tile",
     "dmr_grouped_layer_norm_fwd", "dmr_grouped_layer_norm_bwd", "dmr_grouped_layer_norm_workspace_size",
     "dmr_clip_norm", "dmr_clip_norm_workspace_size", "dmr_grouped_gated_linear_fwd", "dmr_grouped_gated_linear_bwd",
-    "dmr_grouped_gated_linear_workspace_size",
+    "dmr_grouped_gated_linear_workspace_size", "dmr_grouped_gated_linear_plan",
 ]
 DMR_NOALLOC_SCRATCH_BYTES = 128 << 20
 DMR_MAX_LINEAR_WIDTH = 1 << 20
@@ -83,6 +83,10 @@ class dmr_stats(ctypes.Structure):
 class dmr_linear_plan(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in ("y_columns", "y_rows", "grad_x_columns", "grad_x_rows", "grad_weight_side",
                                               "piece_rows", "together")]
+
+
+class dmr_gated_plan(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("columns", "rows", "one_kernel", "piece_rows")]
 
 
 _lib = None
@@ -173,6 +177,8 @@ def lib(path: Optional[str] = None):
     L.dmr_grouped_gated_linear_bwd.argtypes = [P, I64, I32, P, I64, P, P, I32, INT, INT, P, P, P, P, P, SZ, P]
     L.dmr_grouped_gated_linear_workspace_size.restype = SZ
     L.dmr_grouped_gated_linear_workspace_size.argtypes = [I64, I64, I32, I32, INT]
+    L.dmr_grouped_gated_linear_plan.restype = INT
+    L.dmr_grouped_gated_linear_plan.argtypes = [I64, I64, I32, I32, INT, I32, P]
     L.dmr_clip_norm.restype = INT
     L.dmr_clip_norm.argtypes = [P, I32, I64, F32, F32, P, P, SZ, P]
     L.dmr_clip_norm_workspace_size.restype = SZ
@@ -707,19 +713,47 @@ def dmr_grouped_gated_linear_bwd(x: torch.Tensor, row_offsets: torch.Tensor, wei
             workspace.data_ptr(), workspace.numel())
 
 
-def _spans(tensors, outs, groups) -> Tuple[torch.device, bytes]:
-    """The device of `tensors` and the library's table of them."""
-    if len(tensors) == 0:
+def dmr_grouped_gated_linear_plan(R: int, N: int, in_features: int, out_features: int, dtype: torch.dtype,
+                                  aligned: bool = True) -> dict:
+    """What calls of these sizes are computed by (include/dmr.h)."""
+    plan = dmr_gated_plan()
+    rc = lib().dmr_grouped_gated_linear_plan(R, N, in_features, out_features, DTYPES.get(dtype, -1), int(aligned),
+                                             ctypes.byref(plan))
+    if rc != 0:
+        raise DmrError("dmr_grouped_gated_linear_plan", rc)
+    return {f: getattr(plan, f) for f, _ in dmr_gated_plan._fields_}
+
+
+_tensor_address, _tensor_values, _tensor_contiguous, _tensor_device = (
+    torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.get_device)
+
+
+def _spans(tensors, outs, groups, alike=False) -> Tuple[torch.device, bytes]:
+    """The device of `tensors` and the library's table of them. alike: outs
+    were made like tensors."""
+    n = len(tensors)
+    if n == 0:
         raise ValueError("there must be a tensor")
-    dev, table = tensors[0].device, []
-    for t, o in zip(tensors, outs):
-        if not (t.is_contiguous() and t.device == dev and t.numel() % max(groups, 1) == 0):
+    # lists at a time: these calls can be short, and the tensors many
+    dev, values, codes = tensors[0].device, list(map(_tensor_values, tensors)), [DTYPES.get(t.dtype) for t in tensors]
+    if None in codes or not all(map(_tensor_contiguous, tensors)) or len(set(map(_tensor_device, tensors))) > 1:
+        for t in tensors:
+            _dtype(t, "tensors")
             _check(t, "tensors", t.dtype, dev)
-            raise ValueError(f"a tensor of {tuple(t.shape)} cannot be shared by {groups} groups")
-        if o is not t and not _alike(o, t.dtype, dev, t.shape):
-            _check(o, "outs", t.dtype, dev, tuple(t.shape))
-        table += (t.data_ptr(), o.data_ptr(), t.numel() // groups if groups else 0, _dtype(t, "tensors"), 0)
-    return dev, struct.pack("QQqii" * len(tensors), *table)
+    if groups != 1:
+        if groups < 0 or (groups > 0 and any(v % groups for v in values)):
+            raise ValueError(f"tensors of {values} values cannot be shared by {groups} groups")
+        values = [v // groups for v in values] if groups else [0] * n
+    if not alike:
+        for t, o in zip(tensors, outs):
+            if o is not t and not _alike(o, t.dtype, dev, t.shape):
+                _check(o, "outs", t.dtype, dev, tuple(t.shape))
+    table = [0] * (5 * n)
+    table[0::5] = map(_tensor_address, tensors)
+    table[1::5] = map(_tensor_address, outs)
+    table[2::5] = values
+    table[3::5] = codes
+    return dev, struct.pack("QQqii" * n, *table)
 
 
 def dmr_clip_norm_workspace_size(tensors: Sequence[torch.Tensor], groups: int = 1) -> int:
@@ -1092,16 +1126,17 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, groups: Optio
         for g in grads:
             if g.dim() < 1 or g.shape[0] != count:
                 raise ValueError(f"grads of {count} groups must be [{count}, ...], got {tuple(g.shape)}")
-    outs = [torch.empty_like(g) for g in grads] if out is None else list(out)
+    outs = list(map(torch.empty_like, grads)) if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError(f"{len(grads)} grads, but {len(outs)} out")
-    dev, table = _spans(grads, outs, count)
+    dev, table = _spans(grads, outs, count, alike=out is None)
     if out is not None:
         _check_overlap(grads, outs)
-    size = lib().dmr_clip_norm_workspace_size(table, len(grads), count)
+    L = lib()
+    size = L.dmr_clip_norm_workspace_size(table, len(grads), count)
     norms = torch.empty(count, dtype=torch.float32, device=dev)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    _launch(lib().dmr_clip_norm, dev, table, len(grads), count, max_norm, eps, norms.data_ptr(), ws.data_ptr(), size)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 256 else None   # the least: none is used
+    _launch(L.dmr_clip_norm, dev, table, len(grads), count, max_norm, eps, norms.data_ptr(), _address(ws), size)
     return outs, norms
 
 

@@ -595,8 +595,8 @@ dmr_status check_layer_norm(int64_t R, int32_t C, int64_t N, dmr_dtype dtype) {
     if (dtype != DMR_FLOAT32 && dtype != DMR_FLOAT16 && dtype != DMR_BFLOAT16) return DMR_ERROR_INVALID_VALUE;
     if (C > DMR_MAX_LINEAR_WIDTH) return DMR_ERROR_UNSUPPORTED;
     if (R > INT64_MAX / ((int64_t)DMR_MAX_LINEAR_WIDTH * 64)) return DMR_ERROR_UNSUPPORTED;
-    // the sums over rows take a workgroup for each group and 64 of its values
-    if (N > kMaxWorkItems / 256 / (2 * (int64_t)C / 64 + 1)) return DMR_ERROR_UNSUPPORTED;
+    // the sums over rows take a workgroup of 1024 for each group and 64 of its values
+    if (N > kMaxWorkItems / 1024 / (2 * (int64_t)C / 64 + 1)) return DMR_ERROR_UNSUPPORTED;
     if (R > 0 && N == 0) return DMR_ERROR_INVALID_VALUE;
     return DMR_SUCCESS;
 }
@@ -619,7 +619,7 @@ dmr_status dmr_grouped_layer_norm_fwd(const void* x, int64_t R, int32_t features
 
 size_t dmr_grouped_layer_norm_workspace_size(int64_t R, int64_t N, int32_t features, dmr_dtype dtype) {
     if (check_layer_norm(R, features, N, dtype) != DMR_SUCCESS) return 0;
-    return align_up(layer_norm_plan(R, features, dtype != DMR_FLOAT32, true).workspace + 256, 256);
+    return align_up(layer_norm_plan(R, N, features, dtype != DMR_FLOAT32, true).workspace + 256, 256);
 }
 
 dmr_status dmr_grouped_layer_norm_bwd(const void* x, int64_t R, int32_t features, const int64_t* row_offsets, int64_t N,
@@ -674,6 +674,19 @@ size_t dmr_grouped_gated_linear_workspace_size(int64_t R, int64_t N, int32_t in_
     if (check_gated(R, in_features, N, out_features, DMR_SILU, dtype, &none) != DMR_SUCCESS) return 0;
     if (!grouped_sums_fit(R, N, in_features, 2 * out_features, dtype != DMR_FLOAT32)) return 0;
     return gated_workspace(R, N, in_features, out_features, dtype);
+}
+
+dmr_status dmr_grouped_gated_linear_plan(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype,
+                                         int32_t aligned, dmr_gated_plan* out) {
+    static const int64_t none = 0;
+    if (out == nullptr) return DMR_ERROR_INVALID_VALUE;
+    const dmr_status st = check_gated(R, in_features, N, out_features, DMR_SILU, dtype, &none);
+    if (st != DMR_SUCCESS) return st;
+    const bool half = dtype != DMR_FLOAT32;
+    const RowsTile t = gated_tile(R, N, out_features, half, aligned && in_features % (half ? 8 : 4) == 0);
+    const GroupedPieces p = gated_pieces(R, N, in_features, out_features, half);
+    *out = {t.columns, t.rows, gated_narrow(in_features, out_features), p.rows};
+    return DMR_SUCCESS;
 }
 
 dmr_status dmr_grouped_gated_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,

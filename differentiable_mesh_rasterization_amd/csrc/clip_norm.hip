@@ -12,6 +12,8 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // at whatever alignment the values have
+
 constexpr int kThreads = 256;
 
 // What a launch is given: the tensors (values of one group each) and, of
@@ -83,8 +85,9 @@ __device__ __forceinline__ double squares(const T* __restrict__ in, int64_t n) {
     return s;
 }
 
-// out = in c; the two may be the same array.
-template <class T, int THREADS>
+// out = in c; the two may be the same array. STREAM: the stores leave the
+// caches to what is still to be read.
+template <class T, int THREADS, bool STREAM>
 __device__ __forceinline__ void scale(const T* in, T* out, int64_t n, float c) {
     const int64_t whole = n / kVector<T>;
     const auto put = [&](u32x4 raw, int64_t i) {
@@ -92,7 +95,13 @@ __device__ __forceinline__ void scale(const T* in, T* out, int64_t n, float c) {
         __builtin_memcpy(v, &raw, 16);
 #pragma unroll
         for (int e = 0; e < kVector<T>; ++e) v[e] = (T)((float)v[e] * c);
-        __builtin_memcpy(out + i * kVector<T>, v, 16);
+        if constexpr (STREAM) {
+            u32x4_any to;
+            __builtin_memcpy(&to, v, 16);
+            __builtin_nontemporal_store(to, reinterpret_cast<u32x4_any*>(out + i * kVector<T>));
+        } else {
+            __builtin_memcpy(out + i * kVector<T>, v, 16);
+        }
     };
     int64_t i = threadIdx.x;
     for (; i + 3 * THREADS < whole; i += 4 * THREADS) {
@@ -165,6 +174,7 @@ __global__ __launch_bounds__(kThreads) void clip_squares(const Spans s, int64_t 
 
 // Scales every chunk by its group's factor, the last chunks first: they were
 // read last, and what the caches still hold of them is read from there.
+template <bool STREAM>
 __global__ __launch_bounds__(kThreads) void clip_scale(const Spans s, int64_t length, int32_t before, int32_t all,
                                                        const double* __restrict__ partial, float max_norm, float eps,
                                                        float* __restrict__ norms) {
@@ -179,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void clip_scale(const Spans s, int64_t le
     const int64_t at = c.group * t.values + c.first;
     typed(t.dtype, [&](auto zero) {
         typedef decltype(zero) T;
-        scale<T, kThreads>(static_cast<const T*>(t.in) + at, static_cast<T*>(t.out) + at, c.values, by);
+        scale<T, kThreads, STREAM>(static_cast<const T*>(t.in) + at, static_cast<T*>(t.out) + at, c.values, by);
     });
 }
 
@@ -204,8 +214,8 @@ __global__ __launch_bounds__(kSmallThreads) void clip_small(const Spans s, float
         const Span& t = s.at[k];
         typed(t.dtype, [&](auto zero) {
             typedef decltype(zero) T;
-            scale<T, kSmallThreads>(static_cast<const T*>(t.in) + group * t.values,
-                                    static_cast<T*>(t.out) + group * t.values, t.values, by);
+            scale<T, kSmallThreads, false>(static_cast<const T*>(t.in) + group * t.values,
+                                           static_cast<T*>(t.out) + group * t.values, t.values, by);
         });
     }
 }
@@ -214,15 +224,21 @@ __global__ __launch_bounds__(kSmallThreads) void clip_small(const Spans s, float
 
 // Chunks are cut so that about 16 workgroups for each compute unit share all
 // values, and none below 8192 values, which take as long to start as to read.
+// More bytes than half of the last cache level are written past the caches,
+// which then hold more of the input when it is read again (402 MB of bfloat16:
+// 224 us with ordinary stores, 204 so; no difference up to 25 MB). A pass over
+// them reads at 4.4 TB/s, with squares in float32 as in float64.
 ClipPlan clip_plan(const dmr_tensor_span* tensors, int32_t count, int64_t groups) {
     ClipPlan p{};
-    double all = 0.0, slice = 0.0;
+    double all = 0.0, slice = 0.0, bytes = 0.0;
     int32_t used = 0;
     for (int32_t k = 0; k < count; ++k) {
         slice += (double)tensors[k].values;
+        bytes += (double)tensors[k].values * (tensors[k].dtype == DMR_FLOAT32 ? 4.0 : 2.0) * (double)groups;
         used += tensors[k].values > 0;
     }
     all = slice * (double)groups;
+    p.stream = bytes > (double)(1 << 27);
     p.small = used <= kClipTensors && slice <= 65536.0;
     double length = all / 4096.0;
     length = length < 8192.0 ? 8192.0 : length;
@@ -271,8 +287,9 @@ hipError_t launch_clip(const ClipArgs& a, const ClipPlan& p) {
             clip_squares<<<(unsigned)(a.groups * s.chunks), kThreads, 0, a.stream>>>(s, p.length, before, all, a.workspace);
         });
         batches([&](const Spans& s, int32_t before) {
-            clip_scale<<<(unsigned)(a.groups * s.chunks), kThreads, 0, a.stream>>>(s, p.length, before, all, a.workspace,
-                                                                                   a.max_norm, a.eps, a.norms);
+            const auto kernel = p.stream ? clip_scale<true> : clip_scale<false>;
+            kernel<<<(unsigned)(a.groups * s.chunks), kThreads, 0, a.stream>>>(s, p.length, before, all, a.workspace, a.max_norm,
+                                                                               a.eps, a.norms);
         });
     }
     timing_end(kKClipNorm, a.stream);

@@ -500,7 +500,7 @@ struct LayerNormPlan {
     int64_t per, workgroups, slot_values;
     size_t workspace;
 };
-LayerNormPlan layer_norm_plan(int64_t R, int32_t C, bool half, bool backward);
+LayerNormPlan layer_norm_plan(int64_t R, int64_t N, int32_t C, bool half, bool backward);
 hipError_t launch_layer_norm(const LayerNormArgs& a, bool backward);
 
 struct GatedArgs {
@@ -537,9 +537,10 @@ struct ClipArgs {
     hipStream_t stream;
 };
 // small: a workgroup for each group does everything. Otherwise values of a
-// chunk, and the chunks of a group. fits: a launch holds it.
+// chunk, and the chunks of a group. fits: a launch holds it; stream: results
+// pass the caches.
 struct ClipPlan {
-    bool small, fits;
+    bool small, fits, stream;
     int64_t length, chunks;
 };
 ClipPlan clip_plan(const dmr_tensor_span* tensors, int32_t count, int64_t groups);

@@ -14,6 +14,8 @@
 // would take 4 F values of traffic for 4 F C operations, even at C of about
 // 500 in 16 bits, and round them.) [da du] is rounded to the type, which is
 // what the matrix instructions of the two products with it take.
+#include <type_traits>
+
 #include "dmr_internal.h"
 #include "grouped_tiles.h"
 #include "mfma_tile.h"
@@ -69,23 +71,6 @@ __device__ __forceinline__ void with_activation(int act, F&& f) {
     else if (act == DMR_GELU) f([](float a) { return activate<DMR_GELU>(a); });
     else if (act == DMR_GELU_TANH) f([](float a) { return activate<DMR_GELU_TANH>(a); });
     else f([](float a) { return activate<DMR_SIGMOID>(a); });
-}
-
-// Adds the biases (or nothing) to both planes of a tile.
-template <class T, class Tile>
-__device__ __forceinline__ void add_biases(Tile& t, const T* __restrict__ bias, int F, int n0, int tid) {
-    if (!bias) return;
-#pragma unroll
-    for (int a = 0; a < Tile::NT; ++a) {
-        f32x4 add;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = n0 + Tile::n_of(tid, a) + i;   // past the end: any value, not stored
-            add[i] = (float)bias[(a / Tile::PN) * (int64_t)F + (at < F ? at : F - 1)];
-        }
-#pragma unroll
-        for (int b = 0; b < Tile::MT; ++b) t.acc[a][b] += add;
-    }
 }
 
 // Where a lane's values of a tile go: rows [0, rows) of `out` (leading
@@ -193,6 +178,49 @@ struct Upstream {
         return (float)v[a % STEP * 4 + i];
     }
 };
+// The biases of a lane's columns, which the sums begin with, packed as they
+// are in memory.
+template <class T, class Tile>
+struct Biases {
+    static constexpr int WORDS = (int)sizeof(T);   // of four values
+    uint32_t raw[Tile::NT][WORDS];
+    // bias: of the group's first plane, or null
+    __device__ __forceinline__ void load(const T* __restrict__ bias, int F, int n0, int tid) {
+#pragma unroll
+        for (int a = 0; a < Tile::NT; ++a) {
+            const int n = n0 + Tile::n_of(tid, a);
+            const T* plane = bias + (a / Tile::PN) * (int64_t)F;
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) raw[a][w] = 0;
+            if (!bias) continue;
+            if (F >= 4) {
+                // the last four values shifted down, where there are fewer
+                const int at = n < F - 4 ? n : F - 4;
+                __builtin_memcpy(raw[a], plane + at, sizeof(raw[a]));
+                const int by = n - at;
+                if constexpr (WORDS == 2) {
+                    const uint64_t v = (uint64_t)raw[a][1] << 32 | raw[a][0];
+                    const uint64_t s = by < 4 ? v >> (16 * by) : 0;
+                    raw[a][0] = (uint32_t)s;
+                    raw[a][1] = (uint32_t)(s >> 32);
+                } else if (by > 0) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) raw[a][w] = n + w < F ? __builtin_bit_cast(uint32_t, (float)plane[n + w]) : 0;
+                }
+            } else {
+                T v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = n + i < F ? plane[n + i] : (T)0.0f;
+                __builtin_memcpy(raw[a], v, sizeof(v));
+            }
+        }
+    }
+    __device__ __forceinline__ f32x4 operator()(int a) const {
+        T v[4];
+        __builtin_memcpy(v, raw[a], sizeof(v));
+        return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+    }
+};
 struct Nothing {};
 
 // GRAD: writes [da du] of the rows to `out` [R, 2 F] from grad_y [R, F];
@@ -205,8 +233,17 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
                                                                T* __restrict__ out, bool wide, int64_t tiles, int n_tiles,
                                                                uint32_t places) {
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
-    const int tid = threadIdx.x;
-    walk_row_tiles<T, Tile, VEC>(
+    // Of a thread's number, as it is found anew for every tile: what follows from
+    // it would be formed once and kept in scratch memory, for registers are short.
+    const auto thread = [] {
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        return tid;
+    };
+    // the 16-byte stores of a wave's part of a tile
+    constexpr int kStores = Tile::PAIRED ? Tile::MT * Tile::PN / 2 : Tile::MT * Tile::PN;
+    constexpr bool LARGE = sizeof(T) == 2 && Tile::BN == 256;
+    walk_row_tiles<T, Tile, VEC, LARGE ? (GRAD ? 2 : 1) * kStores : 0>(
         lds, blockIdx.x, gridDim.x, x, R, C, off, N, tiles, n_tiles, places,
         [&](const RowTile& at, int n0) {
             const T* w = weight + (at.group * 2 * F + n0) * (int64_t)C;
@@ -214,16 +251,17 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
                                          typename Tile::Source{w + (int64_t)F * C, C, F - n0});
         },
         [&](const RowTile& at, int n0) {
-            if constexpr (GRAD) {
-                Upstream<T, Tile> g;
-                g.load({grad_y + at.first * (int64_t)F, F, at.rows, n0, F, wide_g}, tid);
-                return g;
-            } else {
-                return Nothing{};
-            }
+            Biases<T, Tile> b;
+            b.load(bias && at.group >= 0 ? bias + at.group * 2 * F : nullptr, F, n0, thread());
+            return b;
+        },
+        [&](const RowTile& at, int n0) {
+            typename std::conditional<GRAD, Upstream<T, Tile>, Nothing>::type g;
+            if constexpr (GRAD) g.load({grad_y + at.first * (int64_t)F, F, at.rows, n0, F, wide_g}, thread());
+            return g;
         },
         [&](Tile& t, const RowTile& at, int n0, const auto& g) {
-            add_biases<T, Tile>(t, bias ? bias + at.group * 2 * F : nullptr, F, n0, tid);
+            const int tid = thread();
             constexpr int WIDTHS = GRAD ? 2 : 1;
             const TileOut<T> first = {out + at.first * (int64_t)F * WIDTHS, (int64_t)F * WIDTHS, at.rows, n0, F, wide};
             TileOut<T> second = first;
@@ -232,24 +270,29 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
 #pragma unroll
                 for (int b = 0; b < Tile::MT; ++b) {
 #pragma unroll
-                    for (int a = 0; a < Tile::PN; ++a)
+                    for (int a = 0; a < Tile::PN; ++a) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const Act v = activation(t.acc[a][b][i]);
+                            const float u = t.acc[a + Tile::PN][b][i];
                             if constexpr (GRAD) {
                                 const float up = g.value(b, a, i);
-                                t.acc[a][b][i] = up * t.acc[a + Tile::PN][b][i] * v.slope;
+                                t.acc[a][b][i] = up * u * v.slope;
                                 t.acc[a + Tile::PN][b][i] = up * v.value;
                             } else {
-                                t.acc[a][b][i] = v.value * t.acc[a + Tile::PN][b][i];
+                                t.acc[a][b][i] = v.value * u;
                             }
                         }
+                        __builtin_amdgcn_sched_barrier(0);   // registers are short: block after block
+                    }
                     store_rows<T, Tile, Tile::PN>(first, b, tid, [&](int a) { return t.acc[a][b]; });
                     if constexpr (GRAD)
                         store_rows<T, Tile, Tile::PN>(second, b, tid, [&](int a) { return t.acc[a + Tile::PN][b]; });
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             });
-        });
+        },
+        wide);
 }
 
 // ---------------------------------------------------------------------------

@@ -48,17 +48,31 @@ __device__ __forceinline__ void lane_sums(float (&v)[COUNT]) {
 }
 
 // 16 bytes of a row from value `at` on; values that the row does not have are
-// zero. WHOLE: a row is a whole number of 16 bytes.
+// zero. WHOLE: a row is a whole number of 16 bytes. Others in 16 bits are read
+// past the row's end where the array goes on (`room` values from the row's
+// first), and what is past it is masked: lanes that take different ways would
+// wait for each in turn (400000 rows of 301 in bfloat16 158 us so, 143 masked;
+// 200000 in float32, whose parts are half as long, 120 and 130).
 template <class T, bool WHOLE>
-__device__ __forceinline__ u32x4 load16(const T* __restrict__ row, int at, int C) {
+__device__ __forceinline__ u32x4 load16(const T* __restrict__ row, int at, int C, int64_t room) {
     u32x4 raw = {0, 0, 0, 0};
-    if (at + kVector<T> <= C) {
-        __builtin_memcpy(&raw, row + at, 16);
-    } else if (!WHOLE && at < C) {
-        T v[kVector<T>];
+    if (WHOLE) {
+        if (at < C) __builtin_memcpy(&raw, row + at, 16);
+    } else if (at < C) {
+        if (sizeof(T) == 2 ? at + kVector<T> <= room : at + kVector<T> <= C) {
+            __builtin_memcpy(&raw, row + at, 16);
+            if constexpr (sizeof(T) == 2)
 #pragma unroll
-        for (int e = 0; e < kVector<T>; ++e) v[e] = at + e < C ? row[at + e] : (T)0.0f;
-        __builtin_memcpy(&raw, v, 16);
+                for (int j = 0; j < 4; ++j) {   // of dword j, the values that are the row's
+                    const int values = C - at - 2 * j;
+                    raw[j] = values >= 2 ? raw[j] : values <= 0 ? 0u : raw[j] & 0xFFFFu;
+                }
+        } else {
+            T v[kVector<T>];
+#pragma unroll
+            for (int e = 0; e < kVector<T>; ++e) v[e] = at + e < C ? row[at + e] : (T)0.0f;
+            __builtin_memcpy(&raw, v, 16);
+        }
     }
     return raw;
 }
@@ -119,9 +133,9 @@ struct Row {
 
     static __device__ __forceinline__ int column(int part, int v) { return (part + v * L) * E; }
 
-    __device__ __forceinline__ void load(const T* __restrict__ row, int part, int C) {
+    __device__ __forceinline__ void load(const T* __restrict__ row, int part, int C, int64_t room) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) widen<T>(load16<T, WHOLE>(row, column(part, v), C), x[v]);
+        for (int v = 0; v < V; ++v) widen<T>(load16<T, WHOLE>(row, column(part, v), C, room), x[v]);
     }
 
     __device__ __forceinline__ void normalise(int part, int C, float eps) {
@@ -175,8 +189,8 @@ __global__ __launch_bounds__(kThreads) void norm_rows(const T* __restrict__ x, i
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int at = Row<T, L, V, WHOLE>::column(part, v);
-                if (gamma) widen<T>(load16<T, WHOLE>(gamma + n * C, at, C), ga[v]);
-                if (beta) widen<T>(load16<T, WHOLE>(beta + n * C, at, C), be[v]);
+                if (gamma) widen<T>(load16<T, WHOLE>(gamma + n * C, at, C, (N - n) * C), ga[v]);
+                if (beta) widen<T>(load16<T, WHOLE>(beta + n * C, at, C, (N - n) * C), be[v]);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     if (!gamma) ga[v][e] = 1.0f;
@@ -185,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void norm_rows(const T* __restrict__ x, i
             }
         }
         Row<T, L, V, WHOLE> row;
-        row.load(x + r * C, part, C);
+        row.load(x + r * C, part, C, (R - r) * C);
         row.normalise(part, C, eps);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -273,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void norm_grads(const T* __restrict__ x, 
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int at = Row<T, L, V, WHOLE>::column(part, v);
-            if (gamma) widen<T>(load16<T, WHOLE>(gamma + n * C, at, C), ga[v]);
+            if (gamma) widen<T>(load16<T, WHOLE>(gamma + n * C, at, C, (N - n) * C), ga[v]);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 if (!gamma) ga[v][e] = 1.0f;
@@ -283,9 +297,10 @@ __global__ __launch_bounds__(kThreads) void norm_grads(const T* __restrict__ x, 
         for (int64_t r = from + slot; r < to; r += SLOTS) {
             Row<T, L, V, WHOLE> row;
             float q[V][E];
-            row.load(x + r * C, part, C);
+            row.load(x + r * C, part, C, (R - r) * C);
 #pragma unroll
-            for (int v = 0; v < V; ++v) widen<T>(load16<T, WHOLE>(g + r * C, Row<T, L, V, WHOLE>::column(part, v), C), q[v]);
+            for (int v = 0; v < V; ++v) 
+                widen<T>(load16<T, WHOLE>(g + r * C, Row<T, L, V, WHOLE>::column(part, v), C, (R - r) * C), q[v]);
             row.normalise(part, C, eps);
             float means[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -321,13 +336,14 @@ __global__ __launch_bounds__(kThreads) void norm_grads(const T* __restrict__ x, 
 }
 
 // Adds the slots of the groups that more than one workgroup has rows of (64 of
-// a group's 2 C values a workgroup, its four waves a quarter of the slots
-// each, eight loads in flight a lane), and writes the zeros of empty groups.
+// a group's 2 C values a workgroup, each of its waves every WAVESth slot, eight
+// loads in flight a lane), and writes the zeros of empty groups.
+constexpr int kAddWaves = 16;
 template <class T>
-__global__ __launch_bounds__(kThreads) void norm_add_slots(const int64_t* __restrict__ off, int64_t R, int C, int64_t per,
-                                                           const float* __restrict__ slots, unsigned blocks,
-                                                           T* __restrict__ grad_gamma, T* __restrict__ grad_beta) {
-    __shared__ float part[kThreads / 64][64];
+__global__ __launch_bounds__(kAddWaves * 64) void norm_add_slots(const int64_t* __restrict__ off, int64_t R, int C, int64_t per,
+                                                                 const float* __restrict__ slots, unsigned blocks,
+                                                                 T* __restrict__ grad_gamma, T* __restrict__ grad_beta) {
+    __shared__ float part[kAddWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n = blockIdx.x / blocks;
     const int64_t lo = bound(off, n, R), hi = bound(off, n + 1, R);
@@ -339,19 +355,21 @@ __global__ __launch_bounds__(kThreads) void norm_add_slots(const int64_t* __rest
     if (i < 2 * (int64_t)C) {
         // slot 2 first + 1, then 2 w
         const auto at = [&](int64_t k) { return slots + (k == 0 ? 4 * first + 2 : 4 * (first + k)) * C + i; };
-        for (int64_t k = wave; k < count; k += 32) {
+        for (int64_t k = wave; k < count; k += 8 * kAddWaves) {
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = *at(k + 4 * j < count ? k + 4 * j : k);
+            for (int j = 0; j < 8; ++j) v[j] = *at(k + kAddWaves * j < count ? k + kAddWaves * j : k);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (k + 4 * j < count) s += v[j];
+                if (k + kAddWaves * j < count) s += v[j];
         }
     }
     part[wave][lane] = s;
     __syncthreads();
     if (wave > 0 || i >= 2 * (int64_t)C) return;
-    s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kAddWaves; ++w) s += part[w][lane];
     if (i < C) {
         if (grad_gamma) grad_gamma[n * C + i] = (T)s;
     } else if (grad_beta) {
@@ -391,26 +409,26 @@ __device__ __forceinline__ void workgroup_sums(float (&v)[2], float* lds) {
 
 // Calls f(column, values) for the 16-byte parts of a row.
 template <class T, class F>
-__device__ __forceinline__ void over_row(const T* __restrict__ row, int C, F&& f) {
+__device__ __forceinline__ void over_row(const T* __restrict__ row, int C, int64_t room, F&& f) {
     for (int at = threadIdx.x * kVector<T>; at < C; at += kLongThreads * kVector<T>) {
         float v[kVector<T>];
-        widen<T>(load16<T, false>(row, at, C), v);
+        widen<T>(load16<T, false>(row, at, C, room), v);
         f(at, v);
     }
 }
 
 template <class T>
-__device__ __forceinline__ Stats long_stats(const T* __restrict__ row, int C, float eps, float* lds) {
+__device__ __forceinline__ Stats long_stats(const T* __restrict__ row, int C, int64_t room, float eps, float* lds) {
     const float each = 1.0f / (float)C;
     float sums[2] = {0.0f, 0.0f};
-    over_row<T>(row, C, [&](int, const float* v) {
+    over_row<T>(row, C, room, [&](int, const float* v) {
 #pragma unroll
         for (int e = 0; e < kVector<T>; ++e) sums[0] += v[e];
     });
     workgroup_sums(sums, lds);
     const float mean = sums[0] * each;
     sums[0] = sums[1] = 0.0f;
-    over_row<T>(row, C, [&](int at, const float* v) {
+    over_row<T>(row, C, room, [&](int at, const float* v) {
 #pragma unroll
         for (int e = 0; e < kVector<T>; ++e) {
             const float d = at + e < C ? v[e] - mean : 0.0f;
@@ -433,11 +451,12 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_rows(const T* __restri
         const int64_t n = offsets_upto(off, N, 0, r) - 1;
         if (n < 0 || n >= N) continue;
         const T* row = x + r * C;
-        const Stats s = long_stats<T>(row, C, eps, lds);
-        over_row<T>(row, C, [&](int at, const float* v) {
+        const int64_t room = (R - r) * C;
+        const Stats s = long_stats<T>(row, C, room, eps, lds);
+        over_row<T>(row, C, room, [&](int at, const float* v) {
             float ga[kVector<T>], be[kVector<T>], out[kVector<T>];
-            if (gamma) widen<T>(load16<T, false>(gamma + n * C, at, C), ga);
-            if (beta) widen<T>(load16<T, false>(beta + n * C, at, C), be);
+            if (gamma) widen<T>(load16<T, false>(gamma + n * C, at, C, (N - n) * C), ga);
+            if (beta) widen<T>(load16<T, false>(beta + n * C, at, C, (N - n) * C), be);
 #pragma unroll
             for (int e = 0; e < kVector<T>; ++e) {
                 const float h = (v[e] - s.mean - s.shift) * s.scale;
@@ -460,19 +479,20 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_grad_rows(const T* __r
         const int64_t n = offsets_upto(off, N, 0, r) - 1;
         if (n < 0 || n >= N) continue;
         const T* row = x + r * C;
-        const Stats s = long_stats<T>(row, C, eps, lds);
+        const int64_t room = (R - r) * C;
+        const Stats s = long_stats<T>(row, C, room, eps, lds);
         if (stats && threadIdx.x == 0) stats[r] = s;
         if (!grad_x) continue;
         const auto q_of = [&](int at, float (&q)[kVector<T>]) {
             float ga[kVector<T>];
-            widen<T>(load16<T, false>(g + r * C, at, C), q);
+            widen<T>(load16<T, false>(g + r * C, at, C, (R - r) * C), q);
             if (!gamma) return;
-            widen<T>(load16<T, false>(gamma + n * C, at, C), ga);
+            widen<T>(load16<T, false>(gamma + n * C, at, C, (N - n) * C), ga);
 #pragma unroll
             for (int e = 0; e < kVector<T>; ++e) q[e] *= ga[e];
         };
         float means[2] = {0.0f, 0.0f};
-        over_row<T>(row, C, [&](int at, const float* v) {
+        over_row<T>(row, C, room, [&](int at, const float* v) {
             float q[kVector<T>];
             q_of(at, q);
 #pragma unroll
@@ -484,7 +504,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_grad_rows(const T* __r
         });
         workgroup_sums(means, lds);
         const float mq = means[0] * each, mh = means[1] * each;
-        over_row<T>(row, C, [&](int at, const float* v) {
+        over_row<T>(row, C, room, [&](int at, const float* v) {
             float q[kVector<T>], out[kVector<T>];
             q_of(at, q);
 #pragma unroll
@@ -518,8 +538,8 @@ __global__ __launch_bounds__(kThreads) void norm_long_sums(const T* __restrict__
         for (int64_t r = from; r < to; ++r) {
             const Stats s = stats[r];
             float v[E], q[E];
-            widen<T>(load16<T, false>(x + r * C, at, C), v);
-            widen<T>(load16<T, false>(g + r * C, at, C), q);
+            widen<T>(load16<T, false>(x + r * C, at, C, (R - r) * C), v);
+            widen<T>(load16<T, false>(g + r * C, at, C, (R - r) * C), q);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 sums[0][e] = __builtin_fmaf(q[e], (v[e] - s.mean - s.shift) * s.scale, sums[0][e]);
@@ -569,7 +589,7 @@ template <class T>
 hipError_t launch_forward(const LayerNormArgs& a) {
     const T *x = static_cast<const T*>(a.x), *gamma = static_cast<const T*>(a.weight), *beta = static_cast<const T*>(a.bias);
     T* y = static_cast<T*>(a.y);
-    const LayerNormPlan p = layer_norm_plan(a.R, a.C, sizeof(T) == 2, false);
+    const LayerNormPlan p = layer_norm_plan(a.R, a.N, a.C, sizeof(T) == 2, false);
     if (p.lanes == 0) {
         norm_long_rows<T><<<(unsigned)p.workgroups, kLongThreads, 0, a.stream>>>(x, a.R, a.C, a.off, a.N, gamma, beta, a.eps, y);
         return hipGetLastError();
@@ -586,7 +606,7 @@ template <class T>
 hipError_t launch_backward(const LayerNormArgs& a) {
     const T *x = static_cast<const T*>(a.x), *gamma = static_cast<const T*>(a.weight), *g = static_cast<const T*>(a.grad_y);
     T *gx = static_cast<T*>(a.grad_x), *gw = static_cast<T*>(a.grad_weight), *gb = static_cast<T*>(a.grad_bias);
-    const LayerNormPlan p = layer_norm_plan(a.R, a.C, sizeof(T) == 2, true);
+    const LayerNormPlan p = layer_norm_plan(a.R, a.N, a.C, sizeof(T) == 2, true);
     const bool sums = gw || gb;
     float* slots = a.workspace;
     if (a.R > 0 && p.lanes == 0) {
@@ -609,7 +629,7 @@ hipError_t launch_backward(const LayerNormArgs& a) {
     hipError_t err = hipGetLastError();
     if (err == hipSuccess && sums) {
         const unsigned blocks = (unsigned)((2 * (int64_t)a.C + 63) / 64);
-        norm_add_slots<T><<<blocks * (unsigned)a.N, kThreads, 0, a.stream>>>(a.off, a.R, a.C, p.per, slots, blocks, gw, gb);
+        norm_add_slots<T><<<blocks * (unsigned)a.N, kAddWaves * 64, 0, a.stream>>>(a.off, a.R, a.C, p.per, slots, blocks, gw, gb);
         err = hipGetLastError();
     }
     return err;
@@ -620,8 +640,11 @@ hipError_t launch_backward(const LayerNormArgs& a) {
 // How rows are shared out: the lanes of a row and the 16-byte parts each of
 // them holds (0 lanes: a row takes a workgroup), and the rows of a workgroup.
 // 2048 workgroups of the backward pass fill the device with the eight that a
-// compute unit holds; more would only make more slots.
-LayerNormPlan layer_norm_plan(int64_t R, int32_t C, bool half, bool backward) {
+// compute unit holds; more would only make more slots. But where groups are
+// shorter than the rows that a workgroup works on at a time, it would take
+// them one after another: then a workgroup for each of them, as far as slots
+// allow (64 groups of one row of 64 in float16: 87 us before, 6.6 so).
+LayerNormPlan layer_norm_plan(int64_t R, int64_t N, int32_t C, bool half, bool backward) {
     LayerNormPlan p{};
     const int each = half ? 8 : 4;
     const int64_t parts = ((int64_t)C + each - 1) / each;
@@ -635,7 +658,12 @@ LayerNormPlan layer_norm_plan(int64_t R, int32_t C, bool half, bool backward) {
     } else {
         most = backward ? (most * kThreads + parts - 1) / parts : most;   // strips of columns make the rest
     }
-    const int64_t slots = p.lanes > 0 ? kThreads / p.lanes : 1;
+    int64_t slots = p.lanes > 0 ? kThreads / p.lanes : 1;
+    if (backward && p.lanes > 0 && N > 0 && R / N < slots) {
+        slots = R / N > 1 ? R / N : 1;
+        const int64_t room = ((int64_t)1 << 23) / C;
+        if (room > most) most = room;
+    }
     p.per = (R + most * slots - 1) / (most * slots) * slots;
     p.per = p.per < slots ? slots : p.per;
     p.workgroups = (R + p.per - 1) / p.per;

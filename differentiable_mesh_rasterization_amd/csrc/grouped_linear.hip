@@ -32,6 +32,7 @@ __device__ __forceinline__ void rows_of_workgroup(char* lds, uint32_t block, uin
             const T* w = weight + at.group * (int64_t)n_out * k_in + (WK ? (int64_t)n0 * k_in : (int64_t)n0);
             return typename Tile::Source{w, WK ? k_in : n_out, n_out - n0};
         },
+        [](const RowTile&, int) { return typename Tile::Zero(); },
         [](const RowTile&, int) { return 0; },
         [&](Tile& t, const RowTile& at, int n0, int) {
             store_tile<T, Tile>(t, out + at.first * (int64_t)n_out, n_out, at.rows, n0, n_out,

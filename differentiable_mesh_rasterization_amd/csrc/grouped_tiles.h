@@ -176,14 +176,18 @@ __device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, i
 
 // Products of the rows of `rows_in` (k_in wide) with weights(tile, column) over
 // a workgroup's tiles of rows, each handed to store(product, tile, column,
-// held), held = load(tile, column): what a store needs from memory, asked for
-// ahead of the next tile's loads.
-template <class T, class Tile, bool VEC, class Weights, class Load, class Store>
+// held). Asked for ahead of the next tile's loads: held = load(tile, column),
+// what a store needs from memory, and start(tile, column), what the next
+// tile's sums begin with. YOUNGER: the stores that every wave issues in
+// store() at least, if `stores`; the next tile's first steps do not wait for
+// them.
+template <class T, class Tile, bool VEC, int YOUNGER = 0, class Weights, class Start, class Load, class Store>
 __device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32_t blocks, const T* __restrict__ rows_in,
                                                int64_t R, int k_in, const int64_t* __restrict__ off, int64_t N,
                                                int64_t tiles, int n_tiles, uint32_t places, Weights&& weights,
-                                               Load&& load, Store&& store) {
+                                               Start&& start, Load&& load, Store&& store, bool stores = false) {
     const int tid = threadIdx.x;
+    bool stored = false;
     const auto find = [&](uint32_t place) {
         const int64_t id = tile_of_workgroup<kRun>(place);
         if (id >= tiles) return RowTile{-1, 0, 0};
@@ -198,14 +202,17 @@ __device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32
     uint32_t place = block;
     RowTile at = find(place);
     int n0 = column(place);
+    auto from = start(at, n0);
     if (at.group >= 0) Tile::template begin<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
     while (at.group >= 0) {
         place += blocks;
         const RowTile next = place < places ? find(place) : RowTile{-1, 0, 0};
         const int next_n0 = column(place);
         Tile t;
-        t.template finish<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
+        t.template finish<VEC, YOUNGER>(lds, weights(at, n0), rows_of(at), k_in, tid, false, from, stored);
+        stored = stores;
         const auto held = load(at, n0);
+        from = start(next, next_n0);
         if (next.group >= 0) Tile::template begin<VEC>(lds, weights(next, next_n0), rows_of(next), k_in, tid);
         store(t, at, n0, held);
         at = next;

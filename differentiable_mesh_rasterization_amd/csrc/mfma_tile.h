@@ -351,14 +351,22 @@ struct TileProduct {
             }
     }
 
-    // acc = sum over k in [0, K), begun with the same arguments; the LDS is
-    // free for other use afterwards.
-    template <bool VEC>
-    __device__ __forceinline__ void finish(char* lds, const Planes& p, const Source& q, int K, int tid, bool sums = false) {
+    // What the sums over k begin with: zero, or a value for each block of n.
+    struct Zero {
+        __device__ __forceinline__ f32x4 operator()(int) const { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+    };
+
+    // acc = from(n) + sum over k in [0, K), begun with the same arguments; the
+    // LDS is free for other use afterwards. younger: since begin, each wave has
+    // issued YOUNGER stores or more, which need not be done when the first
+    // steps' loads, which are older, have to be.
+    template <bool VEC, int YOUNGER = 0, class From = Zero>
+    __device__ __forceinline__ void finish(char* lds, const Planes& p, const Source& q, int K, int tid, bool sums = false,
+                                           const From& from = From(), bool younger = false) {
 #pragma unroll
         for (int a = 0; a < NT; ++a)
 #pragma unroll
-            for (int b = 0; b < MT; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int b = 0; b < MT; ++b) acc[a][b] = from(a);
         if constexpr (SUMS)
 #pragma unroll
             for (int b = 0; b < MT; ++b) ones[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -368,7 +376,9 @@ struct TileProduct {
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
         // a wave's loads of a step; they arrive in the order of their issue
         constexpr int kLoads = VEC ? PLANES * P::kLoadsLeast + Q::kLoadsLeast : 0;
-        if (S <= steps) step_barrier<(S - 1) * kLoads>();   // step 0 is here
+        static_assert(YOUNGER == 0 || (S == 2 && VEC && kLoads + YOUNGER < 64), "");
+        if (YOUNGER > 0 && younger && S <= steps) step_barrier<(S - 1) * kLoads + YOUNGER>();
+        else if (S <= steps) step_barrier<(S - 1) * kLoads>();   // step 0 is here
         else step_barrier<0>();
         Fragments first, second;
         read(first, lds, lds + kP, 0, tid);
@@ -378,7 +388,8 @@ struct TileProduct {
             read(second, here, here + kP, 1, tid);
             multiply(first, sums);
             // step t is read, and the loads of step t + 1 have arrived
-            if (t - 1 + S < steps) step_barrier<(S - 2) * kLoads>();
+            if (YOUNGER > 0 && younger && t == 0 && S <= steps) step_barrier<(S - 2) * kLoads + YOUNGER>();
+            else if (t - 1 + S < steps) step_barrier<(S - 2) * kLoads>();
             else step_barrier<0>();
             const bool more = t + S < steps;
             typename P::Held held_p[PLANES];

@@ -517,6 +517,18 @@ dmr_status dmr_grouped_gated_linear_bwd(const void* x, int64_t R, int32_t in_fea
 size_t dmr_grouped_gated_linear_workspace_size(int64_t R, int64_t N, int32_t in_features, int32_t out_features,
                                                dmr_dtype dtype);
 
+/* What calls of these sizes are computed by (for measurement and tests; the
+ * results do not depend on it but for the order of sums): the tile of a and u,
+ * in columns of each and rows; whether one kernel computes the whole backward
+ * pass, and the most rows of one of its pieces (otherwise a and u are computed
+ * again by that tile, and the rest is dmr_grouped_linear_bwd's). aligned: the
+ * arrays start on 16 bytes. */
+typedef struct dmr_gated_plan {
+    int32_t columns, rows, one_kernel, piece_rows;
+} dmr_gated_plan;
+dmr_status dmr_grouped_gated_linear_plan(int64_t R, int64_t N, int32_t in_features, int32_t out_features, dmr_dtype dtype,
+                                         int32_t aligned, dmr_gated_plan* out);
+
 /*
  * Norms of gradients over many tensors, and clipping: what keeps one bad
  * image from moving a decoder far. Every tensor is [groups, values], and group

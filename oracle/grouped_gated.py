@@ -50,10 +50,10 @@ def activate(a, kind):
 
 
 def _projections(x, row_offsets, weight, bias):
-    N, _, F, _ = weight.shape
+    N, _, F, C = weight.shape
     both = np.zeros((x.shape[0], 2, F))
     for n, rows in _groups(row_offsets):
-        both[rows] = np.einsum("rc,pfc->rpf", x[rows], weight[n])
+        both[rows] = (x[rows] @ weight[n].reshape(2 * F, C).T).reshape(rows.stop - rows.start, 2, F)
         if bias is not None:
             both[rows] += bias[n]
     return both[:, 0], both[:, 1]
@@ -80,8 +80,9 @@ def gated_backward(x, row_offsets, weight, bias, grad_y, activation="silu"):
 def _products(x, row_offsets, weight, back):
     gx, gw, gb = np.zeros_like(x), np.zeros_like(weight), np.zeros(weight.shape[:3])
     for n, rows in _groups(row_offsets):
-        gx[rows] = np.einsum("rpf,pfc->rc", back[rows], weight[n])
-        gw[n] = np.einsum("rpf,rc->pfc", back[rows], x[rows])
+        flat = back[rows].reshape(rows.stop - rows.start, 2 * weight.shape[2])
+        gx[rows] = flat @ weight[n].reshape(flat.shape[1], x.shape[1])
+        gw[n] = (flat.T @ x[rows]).reshape(gw[n].shape)
         gb[n] = back[rows].sum(axis=0)
     return gx, gw, gb
 
