@@ -1137,6 +1137,9 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, groups: Optio
     norms = torch.empty(count, dtype=torch.float32, device=dev)
     ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 256 else None   # the least: none is used
     _launch(L.dmr_clip_norm, dev, table, len(grads), count, max_norm, eps, norms.data_ptr(), _address(ws), size)
+    if out is not None:
+        for o in outs:      # what autograd saved of them is not what they hold now
+            torch.autograd.graph.increment_version(o)
     return outs, norms
 
 

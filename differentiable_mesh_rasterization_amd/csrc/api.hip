@@ -672,7 +672,7 @@ size_t dmr_grouped_gated_linear_workspace_size(int64_t R, int64_t N, int32_t in_
                                                dmr_dtype dtype) {
     static const int64_t none = 0;
     if (check_gated(R, in_features, N, out_features, DMR_SILU, dtype, &none) != DMR_SUCCESS) return 0;
-    if (!grouped_sums_fit(R, N, in_features, 2 * out_features, dtype != DMR_FLOAT32)) return 0;
+    if (!gated_fits(R, N, in_features, out_features, dtype != DMR_FLOAT32)) return 0;
     return gated_workspace(R, N, in_features, out_features, dtype);
 }
 
@@ -698,7 +698,7 @@ dmr_status dmr_grouped_gated_linear_bwd(const void* x, int64_t R, int32_t in_fea
     const bool sums = grad_weight || grad_bias;
     if (R > 0 && (!x || !weight || !grad_y)) return DMR_ERROR_INVALID_VALUE;
     if (N == 0 || !(grad_x || sums) || (R == 0 && !sums)) return DMR_SUCCESS;
-    if (!grouped_sums_fit(R, N, in_features, 2 * out_features, dtype != DMR_FLOAT32)) return DMR_ERROR_UNSUPPORTED;
+    if (!gated_fits(R, N, in_features, out_features, dtype != DMR_FLOAT32)) return DMR_ERROR_UNSUPPORTED;
     if (workspace == nullptr ||
         workspace_bytes < dmr_grouped_gated_linear_workspace_size(R, N, in_features, out_features, dtype))
         return DMR_ERROR_WORKSPACE_TOO_SMALL;

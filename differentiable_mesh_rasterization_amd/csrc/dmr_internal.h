@@ -467,7 +467,9 @@ __host__ __device__ __forceinline__ int64_t grouped_piece_values(int32_t cin, in
 }
 hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a);
 hipError_t launch_grouped_linear_backward(const GroupedLinearArgs& a);
-// Adds the pieces of long groups' sums (of the backward pass' arguments).
+// Adds the pieces of long groups' sums (of the backward pass' arguments), and
+// whether a launch holds that.
+bool grouped_add_fits(int64_t N, int32_t cin, int32_t cout);
 hipError_t launch_grouped_add_pieces(const GroupedLinearArgs& a, const GroupedPieces& p);
 
 struct OrthogonalizeArgs {
@@ -523,6 +525,7 @@ inline size_t gated_rows_bytes(int64_t R, int32_t F, dmr_dtype dtype) {
 // Whether one kernel computes the whole backward pass, and how it cuts the rows.
 bool gated_narrow(int32_t C, int32_t F);
 GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half);
+bool gated_fits(int64_t R, int64_t N, int32_t C, int32_t F, bool half);   // whether launches hold the backward pass
 size_t gated_workspace(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype);
 hipError_t launch_gated(const GatedArgs& a, bool backward);
 

@@ -771,6 +771,12 @@ GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half
     return {(int)rows, 64, R > rows ? 2 * (R / rows) : 0};
 }
 
+bool gated_fits(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
+    if (!gated_narrow(C, F)) return grouped_sums_fit(R, N, C, 2 * F, half);
+    const GroupedPieces p = gated_pieces(R, N, C, F, half);
+    return R / p.rows + N <= kMaxWorkItems / 512 && (p.slots == 0 || grouped_add_fits(N, C, 2 * F));
+}
+
 size_t gated_workspace(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype) {
     const GroupedPieces p = gated_pieces(R, N, C, F, dtype != DMR_FLOAT32);
     const size_t sums = align_up((size_t)(p.slots * grouped_piece_values(C, 2 * F)) * sizeof(float) + 256, 256);

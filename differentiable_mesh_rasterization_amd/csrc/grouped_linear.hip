@@ -461,12 +461,16 @@ bool grouped_together(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half
     return (row_tiles + items <= few || narrow) && row_tiles + items <= 1 << 23;
 }
 
+bool grouped_add_fits(int64_t N, int32_t cin, int32_t cout) {
+    return add_blocks((int64_t)cin * cout + cout) * N <= kMaxWorkItems / 256;
+}
+
 bool grouped_sums_fit(int64_t R, int64_t N, int32_t cin, int32_t cout, bool half) {
     const GroupedPieces p = grouped_pieces(R, N, cin, cout, half);
     const int side = grouped_weight_side(p, false);   // of the tiles that are more
     const int64_t items = (R / p.rows + N) * ceil_div(cin, side) * ceil_div(cout, side), round = 8 * kPieceRun;
     if ((items + round - 1) / round * round > kMaxWorkItems / 256) return false;
-    return p.slots == 0 || add_blocks((int64_t)cin * cout + cout) * N <= kMaxWorkItems / 256;
+    return p.slots == 0 || grouped_add_fits(N, cin, cout);
 }
 
 hipError_t launch_grouped_add_pieces(const GroupedLinearArgs& a, const GroupedPieces& p) {

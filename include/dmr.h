@@ -431,7 +431,7 @@ size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dty
  * row's values,
  *     y_r = gamma_n (x_r - m) / sqrt(v + eps) + beta_n.
  *
- *   x, y       [R, features]; y is overwritten.
+ *   x, y       [R, features]; y is overwritten and may not alias an input.
  *   row_offsets [N+1] int64, as for dmr_grouped_linear_fwd; rows that other
  *              offsets give to no group are left as they are.
  *   weight (gamma), bias (beta) [N, features], each may be NULL (ones, zeros).
@@ -440,8 +440,8 @@ size_t dmr_orthogonalize_workspace_size(int64_t B, int32_t m, int32_t n, dmr_dty
  *              zero keep their digits. Each result is rounded once.
  *   eps        finite and > 0.
  * A row depends on no other; one with an infinity or NaN gives NaN
- * throughout. Deviations whose squares' sum passes float32's range give an
- * infinite variance (y_r = beta_n).
+ * throughout, as does one whose sum passes float32's range; deviations whose
+ * squares' sum passes it give an infinite variance (y_r = beta_n).
  * Errors: negative sizes, features below 1, missing pointers, an unknown
  * dtype, eps not > 0 and finite, or N == 0 with R > 0:
  * DMR_ERROR_INVALID_VALUE; features above DMR_MAX_LINEAR_WIDTH or more groups
@@ -473,7 +473,8 @@ size_t dmr_grouped_layer_norm_workspace_size(int64_t R, int64_t N, int32_t featu
  * group n, with A_n, U_n the two planes of its weight and a_n, u_n of its bias,
  *     y_r = act(A_n x_r + a_n) (U_n x_r + u_n)   (value by value).
  *
- *   x          [R, in_features]; y [R, out_features], overwritten.
+ *   x          [R, in_features]; y [R, out_features], overwritten; it may not
+ *              alias an input.
  *   row_offsets [N+1] int64, as for dmr_grouped_linear_fwd; rows that other
  *              offsets give to no group are left as they are.
  *   weight     [N, 2, out_features, in_features]; bias [N, 2, out_features] or

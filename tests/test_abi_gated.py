@@ -72,6 +72,18 @@ def test_gated_workspace_sizes(dmr):
     assert size(10, 2, 8, 1 << 20, torch.float32) == 0
 
 
+# groups whose backward pass takes a workgroup of 512 each; whose pieces are
+# added by several of 256 each; and, of wider layers, as a linear layer's
+@pytest.mark.parametrize("R,N,cin,cout,dtype,fewer", [(100, 1 << 23, 1, 100, torch.float32, (1 << 23) - 8),
+                                                      (1000, 1 << 21, 64, 64, torch.float32, 1 << 18),
+                                                      (1 << 29, 1 << 21, 512, 256, torch.bfloat16, 1 << 17)])
+def test_gated_sums_past_a_launch_are_refused(dmr, R, N, cin, cout, dtype, fewer):
+    size, code = dmr.dmr_grouped_gated_linear_workspace_size, dmr.DTYPES[dtype]
+    assert size(R, N, cin, cout, dtype) == 0 and size(R, fewer, cin, cout, dtype) > 0
+    assert _bwd(dmr, R=R, cin=cin, N=N, cout=cout, dtype=code, ws_bytes=1 << 62) == UNSUPPORTED
+    assert _bwd(dmr, R=R, cin=cin, N=fewer, cout=cout, dtype=code, ws_bytes=16) == WS_SMALL
+
+
 def test_gated_arguments_are_checked_before_the_library(dmr):
     x, off, w = torch.zeros((4, 8)), torch.tensor([0, 1, 4]), torch.zeros((2, 2, 3, 8))
     for kind in ("relu", None, 0):

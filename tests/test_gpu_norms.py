@@ -373,6 +373,16 @@ def test_clip_past_32_bit_offsets(dmr):
     assert out[0, -1] == 3.0 and out[1, 0] == 3.0 and out[1, -1] == 4.0 and out.count_nonzero() == 3
 
 
+def test_clip_in_place_is_seen_by_autograd(dmr):
+    # a saved tensor that clipping in place has changed is not differentiated with
+    w = torch.randn(10, device=DEV, requires_grad=True)
+    v = torch.randn(10, device=DEV)
+    loss = (w * v).sum()
+    dmr.clip_grad_norm([v], 0.1, out=[v])
+    with pytest.raises(RuntimeError):
+        loss.backward()
+
+
 def test_clip_streams_and_refusals(dmr):
     grads = [torch.randn((3, 50000), device=DEV), torch.randn((3, 7), device=DEV)]
     first, n = dmr.clip_grad_norm(grads, 1.0, groups=3)
