@@ -253,7 +253,7 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
     // the 16-byte stores of a wave's part of a tile
     constexpr int kStores = Tile::PAIRED ? Tile::MT * Tile::PN / 2 : Tile::MT * Tile::PN;
     constexpr bool LARGE = sizeof(T) == 2 && Tile::BN == 256;
-    walk_row_tiles<T, Tile, VEC, LARGE ? (GRAD ? 2 : 1) * kStores : 0>(
+    walk_row_tiles<T, Tile, VEC, LARGE ? (GRAD ? 2 : 1) * kStores : 0, LARGE>(
         lds, blockIdx.x, gridDim.x, x, R, C, off, N, tiles, n_tiles, places,
         [&](const RowTile& at, int n0) {
             const T* w = weight + (at.group * 2 * F + n0) * (int64_t)C;
@@ -319,7 +319,11 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
 // pass memory once: 3 C + F values a row where the general form, with [da du]
 // in memory, moves 4 C + 7 F.
 //
-// What bounds it: memory (16-bit) and the float32 products (float32).
+// What bounds it: 2^20 rows of 64 to 64 in bfloat16 take 126 us (memory alone
+// 80; LDS, vector and matrix instructions each a part, in turn more than at a
+// time), 217632 of 64 to 128 in float32 240 (the float32 products 139). Two
+// workgroups of 128 rows at a time on a compute unit are faster than one (172)
+// and than more waves with fewer rows each (64 rows at a time: 143).
 //
 // SPLIT: two waves share 16 MT rows, each with half of the columns: of a and u
 // first, of grad_x afterwards, for which they read each other's [da du] from
@@ -686,7 +690,8 @@ hipError_t launch_narrow(const GatedArgs& a, const GroupedPieces& p) {
 template <class T, class Tile, bool GRAD>
 hipError_t launch_tile(const GatedArgs& a, T* out, bool vec, bool wide_g, bool wide) {
     const int n_tiles = ceil_div(a.F, Tile::COLUMNS);
-    const int64_t tiles = most_row_tiles(a.R, a.N, Tile::BM) * n_tiles;
+    // of rows, whole bands of four
+    const int64_t tiles = (most_row_tiles(a.R, a.N, Tile::BM) + 3) / 4 * 4 * n_tiles;
     const unsigned places = run_grid<kRun>(tiles);
     if (places == 0) return hipErrorInvalidValue;
     // as many workgroups as the device holds at a time (a multiple of 8 kRun)
@@ -748,10 +753,13 @@ hipError_t launch_typed(const GatedArgs& a, bool backward) {
 
 // The tile by the columns of each plane and by how many there are, as for
 // linear layers: the larger, the fewer bytes for a product, but they have to
-// fill 256 compute units.
+// fill 256 compute units, and rather half of them with tiles of 16 rows than
+// fewer with 128. (3204 rows of 664 to 21 in float32: 30 us with 32 x 128, 12.4
+// with 64 x 16; 300 of 1024 to 1000 42 and 26; but 10000 of 512 to 48 in
+// bfloat16, 158 tiles, 8.1 and 10.4.)
 RowsTile gated_tile(int64_t R, int64_t N, int32_t F, bool half, bool vec) {
     const auto tiles = [&](int columns, int rows) { return (R / rows + 1) * ceil_div(F, columns); };
-    if (R <= 16 * N) return {64, 16};
+    if (R <= 16 * N || tiles(32, 128) < 128) return {64, 16};
     if (F <= 16) return {16, 128};
     if (half && vec && F > 64 && R >= 512 * N && tiles(128, 256) >= 224) return {128, 256};
     if (F <= 32 || tiles(64, 128) < 256) return {32, 128};

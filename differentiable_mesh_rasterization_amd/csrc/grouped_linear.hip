@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restr
             }
         }
     };
-    const int64_t begin = (int64_t)(blockIdx.x % blocks) * kAddValues<SPLIT>;
+    int64_t begin = (int64_t)(blockIdx.x % blocks) * kAddValues<SPLIT>;
     if constexpr (SPLIT) {
         const int64_t i = begin + lane * 4;
         if (i < values && wave < mine) part[wave][lane] = sum(i, wave);
@@ -207,30 +207,32 @@ __global__ __launch_bounds__(256) void grouped_add_pieces(const int64_t* __restr
     } else {
         // four vectors a lane, 1024 values apart, all in flight
         const float* from = slots + slot * width;
-        f32x4 s[4];
-        int64_t at[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t i = begin + j * 1024 + tid * 4;
-            at[j] = i < values ? i : 0;   // past the end: not written
-            s[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        for (int k = 0; k < mine; k += 2) {
-            f32x4 v[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[u][j] = *reinterpret_cast<const f32x4*>(from + (k + (k + u < mine ? u : 0)) * width + at[j]);
+        for (; begin < values; begin += (int64_t)blocks * kAddValues<SPLIT>) {
+            f32x4 s[4];
+            int64_t at[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[j] += v[0][j];
-                if (k + 1 < mine) s[j] += v[1][j];
+                const int64_t i = begin + j * 1024 + tid * 4;
+                at[j] = i < values ? i : 0;   // past the end: not written
+                s[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
-        }
+            for (int k = 0; k < mine; k += 2) {
+                f32x4 v[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (begin + j * 1024 + tid * 4 < values) write(at[j], s[j]);
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[u][j] = *reinterpret_cast<const f32x4*>(from + (k + (k + u < mine ? u : 0)) * width + at[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[j] += v[0][j];
+                    if (k + 1 < mine) s[j] += v[1][j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (begin + j * 1024 + tid * 4 < values) write(at[j], s[j]);
+        }
     }
 }
 
@@ -340,7 +342,8 @@ int64_t add_blocks(int64_t values) {
 
 template <class T>
 hipError_t add_pieces(const GroupedLinearArgs& a, const GroupedPieces& p) {
-    const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout, blocks = add_blocks(values);
+    const int64_t size = (int64_t)a.cin * a.cout, values = size + a.cout;
+    const int64_t blocks = !add_split(values) && add_blocks(values) > 256 ? 256 : add_blocks(values);
     const auto add = add_split(values) ? grouped_add_pieces<T, true> : grouped_add_pieces<T, false>;
     add<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(a.off, a.N, a.R, p.rows, values, grouped_piece_values(a.cin, a.cout), size,
                                                         a.workspace, p.slots, (unsigned)blocks, static_cast<T*>(a.grad_weight),

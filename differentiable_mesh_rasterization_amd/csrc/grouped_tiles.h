@@ -180,34 +180,57 @@ __device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, i
 // what a store needs from memory, and start(tile, column), what the next
 // tile's sums begin with. YOUNGER: the stores that every wave issues in
 // store() at least, if `stores`; the next tile's first steps do not wait for
-// them.
-template <class T, class Tile, bool VEC, int YOUNGER = 0, class Weights, class Start, class Load, class Store>
+// them. BANDS: the 32 tiles that a die works on together are four of rows by
+// eight of columns, rather than one of rows and the whole of a wide weight,
+// which its L2 does not hold.
+template <class T, class Tile, bool VEC, int YOUNGER = 0, bool BANDS = false, class Weights, class Start, class Load, class Store>
 __device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32_t blocks, const T* __restrict__ rows_in,
                                                int64_t R, int k_in, const int64_t* __restrict__ off, int64_t N,
                                                int64_t tiles, int n_tiles, uint32_t places, Weights&& weights,
                                                Start&& start, Load&& load, Store&& store, bool stores = false) {
     const int tid = threadIdx.x;
     bool stored = false;
-    const auto find = [&](uint32_t place) {
+    // A place's tile of rows; its tile of columns goes to `c`.
+    const auto find = [&](uint32_t place, int& c) {
         const int64_t id = tile_of_workgroup<kRun>(place);
         if (id >= tiles) return RowTile{-1, 0, 0};
-        return find_row_tile(off, N, R, Tile::BM, (int)(id / n_tiles));
+        if constexpr (BANDS) {
+            const int in_band = (int)(id % (4 * n_tiles)), chunk = in_band / 32, in_chunk = in_band % 32;
+            const int wide = n_tiles - 8 * chunk < 8 ? n_tiles - 8 * chunk : 8;
+            c = 8 * chunk + in_chunk % wide;
+            return find_row_tile(off, N, R, Tile::BM, (int)(id / (4 * n_tiles)) * 4 + in_chunk / wide);
+        } else {
+            c = (int)(id % n_tiles);
+            return find_row_tile(off, N, R, Tile::BM, (int)(id / n_tiles));
+        }
     };
-    const auto column = [&](uint32_t place) { return (int)(tile_of_workgroup<kRun>(place) % n_tiles) * Tile::COLUMNS; };
+    // The first tile that exists from a place on, and its first column. (In the
+    // order of rows none exists after one that does not.)
+    const auto find_from = [&](uint32_t& place, int& n0) {
+        int c = 0;
+        RowTile r = find(place, c);
+        if constexpr (BANDS)
+            while (r.group < 0 && place + blocks < places) {
+                place += blocks;
+                r = find(place, c);
+            }
+        n0 = c * Tile::COLUMNS;
+        return r;
+    };
     const auto rows_of = [&](const RowTile& at) {
         return typename Tile::Source{rows_in + at.first * (int64_t)k_in, k_in, at.rows};
     };
     // A workgroup that takes several tiles finds the next one while a tile is
     // multiplied and issues its first loads before it stores.
     uint32_t place = block;
-    RowTile at = find(place);
-    int n0 = column(place);
+    int n0 = 0;
+    RowTile at = find_from(place, n0);
     auto from = start(at, n0);
     if (at.group >= 0) Tile::template begin<VEC>(lds, weights(at, n0), rows_of(at), k_in, tid);
     while (at.group >= 0) {
         place += blocks;
-        const RowTile next = place < places ? find(place) : RowTile{-1, 0, 0};
-        const int next_n0 = column(place);
+        int next_n0 = 0;
+        const RowTile next = place < places ? find_from(place, next_n0) : RowTile{-1, 0, 0};
         Tile t;
         t.template finish<VEC, YOUNGER>(lds, weights(at, n0), rows_of(at), k_in, tid, false, from, stored);
         stored = stores;

@@ -29,9 +29,10 @@ def dmr():
 # (sizes, cin, cout, types, tile: columns and rows); cin of 200: 3 1/8 steps of
 # k in 16 bits, 6 1/4 in float32
 TILES = [([9, 0, 1, 16], 200, 140, ALL, (64, 16)), ([9, 0, 1, 16], 201, 139, ALL, (64, 16)),
-         ([900, 0, 130], 200, 12, ALL, (16, 128)), ([900, 0, 130], 203, 3, ALL, (16, 128)),
-         ([900, 0, 130], 200, 140, ALL, (32, 128)), ([900, 0, 130], 203, 139, ALL, (32, 128)),
-         ([900, 0, 130], 64, 140, ALL, (32, 128)), ([900, 0, 130], 100, 140, ALL, (32, 128)),
+         ([900, 0, 130], 200, 140, ALL, (64, 16)), ([900, 0, 130], 203, 139, ALL, (64, 16)),
+         ([16300, 0, 130], 200, 12, ALL, (16, 128)), ([16300, 0, 130], 203, 3, ALL, (16, 128)),
+         ([3300, 0, 130], 200, 140, ALL, (32, 128)), ([3300, 0, 130], 203, 139, ALL, (32, 128)),
+         ([3300, 0, 130], 64, 140, ALL, (32, 128)), ([3300, 0, 130], 100, 140, ALL, (32, 128)),
          ([12000, 0, 130, 1], 200, 136, ALL, (64, 128)), ([12000, 0, 130, 1], 203, 139, ALL, (64, 128)),
          # 258 tiles of rows and three of columns for 256 workgroups; steps of k: 4, 1, 2 and 3
          ([65000, 0, 130, 1, 700], 200, 264, HALF, (128, 256)), ([65000, 0, 130, 1, 700], 64, 261, HALF, (128, 256)),
