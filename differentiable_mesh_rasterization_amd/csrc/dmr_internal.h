@@ -526,6 +526,7 @@ inline size_t gated_rows_bytes(int64_t R, int32_t F, dmr_dtype dtype) {
 bool gated_narrow(int32_t C, int32_t F);
 GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half);
 bool gated_fits(int64_t R, int64_t N, int32_t C, int32_t F, bool half);   // whether launches hold the backward pass
+bool gated_short(int64_t R, int64_t N, int32_t C, int32_t F, bool half);   // the weights' gradient row by row
 size_t gated_workspace(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype);
 hipError_t launch_gated(const GatedArgs& a, bool backward);
 

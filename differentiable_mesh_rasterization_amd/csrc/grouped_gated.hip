@@ -687,6 +687,90 @@ hipError_t launch_narrow(const GatedArgs& a, const GroupedPieces& p) {
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// few rows for each of many groups: the gradient of the weights
+// ---------------------------------------------------------------------------
+// The weights of every group are written once, and that is all there is to do:
+// a thread takes 16 bytes of columns of eight of the weight's rows and adds
+// its group's rows one after another. (Matrix instructions would multiply 64
+// rows, of which nearly all are not there.)
+constexpr int kShortRows = 8;   // of the weight, a thread's
+
+template <class T, bool VEC>
+__global__ __launch_bounds__(256) void gated_short_weight_grads(const T* __restrict__ x, int64_t R, int C,
+                                                                const int64_t* __restrict__ off, int64_t N,
+                                                                const T* __restrict__ back, int width, bool wide, unsigned blocks,
+                                                                T* __restrict__ grad_weight, T* __restrict__ grad_bias) {
+    constexpr int E = 16 / (int)sizeof(T), PARTS = kShortRows / E;   // 16 bytes of [da du]: eight or four values
+    const int64_t n = blockIdx.x / blocks;
+    int64_t lo, hi;
+    group_bounds(off, N, R, n, lo, hi);
+    const unsigned chunks = (unsigned)((C + E - 1) / E);
+    const unsigned item = (blockIdx.x % blocks) * 256 + threadIdx.x;
+    const int c = (int)(item % chunks) * E;
+    const int64_t f = (int64_t)(item / chunks) * kShortRows;
+    if (f >= width) return;
+    float sum[kShortRows][E], total[kShortRows];
+#pragma unroll
+    for (int k = 0; k < kShortRows; ++k) {
+        total[k] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[k][e] = 0.0f;
+    }
+    for (int64_t r = lo; r < hi; ++r) {
+        const u32x4 xr = row_chunk<T, VEC>(x, R, r, c, C, true);
+        u32x4 d[PARTS];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) d[p] = row_chunk<T, VEC>(back, R, r, (int)f + p * E, width, true);
+#pragma unroll
+        for (int k = 0; k < kShortRows; ++k) {
+            const float v = value_of<T>(d[k / E], k % E);
+            total[k] += v;
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[k][e] = __builtin_fmaf(v, value_of<T>(xr, e), sum[k][e]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kShortRows; ++k) {
+        if (f + k >= width) break;
+        if (grad_weight) {
+            alignas(16) T out[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[e] = (T)sum[k][e];
+            T* to = grad_weight + (n * width + f + k) * C + c;
+            if (wide) {
+                *reinterpret_cast<u32x4*>(to) = *reinterpret_cast<const u32x4*>(out);
+            } else if (c + E <= C) {
+                __builtin_memcpy(to, out, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (c + e < C) to[e] = out[e];
+            }
+        }
+        if (grad_bias && c == 0) grad_bias[n * width + f + k] = (T)total[k];
+    }
+}
+
+// Workgroups of a group.
+int64_t short_blocks(int32_t C, int32_t F, int each) {
+    const int64_t items = (int64_t)ceil_div(C, each) * ceil_div(2 * F, kShortRows);
+    return (items + 255) / 256;
+}
+
+template <class T>
+hipError_t launch_short(const GatedArgs& a) {
+    constexpr int each = 16 / (int)sizeof(T);
+    const int64_t blocks = short_blocks(a.C, a.F, each);
+    const bool whole = a.C % each == 0, vec = whole && 2 * a.F % each == 0 && aligned16(a.x);
+    const auto kernel = vec ? gated_short_weight_grads<T, true> : gated_short_weight_grads<T, false>;
+    kernel<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(static_cast<const T*>(a.x), a.R, a.C, a.off, a.N,
+                                                           reinterpret_cast<const T*>(a.workspace), 2 * a.F,
+                                                           whole && aligned16(a.grad_weight), (unsigned)blocks,
+                                                           static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
+    return hipGetLastError();
+}
+
 template <class T, class Tile, bool GRAD>
 hipError_t launch_tile(const GatedArgs& a, T* out, bool vec, bool wide_g, bool wide) {
     const int n_tiles = ceil_div(a.F, Tile::COLUMNS);
@@ -743,6 +827,11 @@ hipError_t launch_typed(const GatedArgs& a, bool backward) {
         const hipError_t err = launch_products<T, true>(a, reinterpret_cast<T*>(a.workspace));
         if (err != hipSuccess) return err;
     }
+    if ((a.grad_weight || a.grad_bias) && gated_short(a.R, a.N, a.C, a.F, sizeof(T) == 2)) {
+        const hipError_t err = launch_short<T>(a);
+        if (err != hipSuccess || !a.grad_x || a.R == 0) return err;
+        b.grad_weight = b.grad_bias = nullptr;
+    }
     // [da du] as the upstream gradient of a linear layer of 2 F outputs
     b.grad_y = a.workspace;
     b.workspace = reinterpret_cast<float*>(a.workspace + gated_rows_bytes(a.R, a.F, a.dtype));
@@ -783,6 +872,16 @@ bool gated_fits(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
     if (!gated_narrow(C, F)) return grouped_sums_fit(R, N, C, 2 * F, half);
     const GroupedPieces p = gated_pieces(R, N, C, F, half);
     return R / p.rows + N <= kMaxWorkItems / 512 && (p.slots == 0 || grouped_add_fits(N, C, 2 * F));
+}
+
+// Whether the weights' gradient is added row by row: where groups have at most
+// four rows on average and the weights are many. (bfloat16, the whole backward
+// pass: 64 groups of one row, 1024 to 1024, 178 us so and 291 otherwise; 256
+// rows in 64 groups, 512 to 512, 43 and 65; but 900 rows 88 and 76, and 200
+// rows in 100 groups, 65 to 100, where one launch does both gradients, 28 and 17.)
+bool gated_short(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
+    return !gated_narrow(C, F) && R <= 4 * N && (double)N * F * C >= (double)(1 << 21) &&
+           short_blocks(C, F, half ? 8 : 4) * N <= kMaxWorkItems / 256;
 }
 
 size_t gated_workspace(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype) {

@@ -76,6 +76,24 @@ def test_gated_backward_in_one_kernel(dmr, sizes, cin, cout, dtype):
         _check(got, ref, bound, what)
 
 
+# few rows for each of many groups: the weights' gradient row by row (whole 16
+# bytes and not, empty groups, one long group among them, one gradient alone)
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("sizes,cin,cout", [([1] * 40, 200, 300), ([1, 0, 3, 2] * 12, 201, 307), ([0] * 30 + [90] + [1] * 10, 136, 500),
+                                            ([2, 1] * 16, 3, 30000)])
+def test_gated_backward_of_few_rows(dmr, sizes, cin, cout, dtype):
+    say(f"[gpu] gated, few rows {dtype} {cin}->{cout} groups {len(sizes)}")
+    assert sum(sizes) <= 4 * len(sizes) and len(sizes) * cin * cout >= 1 << 21
+    off, (x, x64), (w, w64), (b, b64), (g, g64) = _inputs(sizes, cin, cout, dtype, cin)
+    offd = torch.from_numpy(off).to(DEV)
+    ref = gated_backward(x64, off, w64, b64, g64)
+    bound = gated_backward_bound(x64, off, w64, b64, g64, dtype)
+    for grads in ((True, True, True), (False, True, False), (False, False, True)):
+        for got, r, e, what in zip(_backward(dmr, x, offd, w, b, g, grads=grads), ref, bound, ("gx", "gw", "gb")):
+            if got is not None:
+                _check(got, r, e, what)
+
+
 def test_gated_plans(dmr):
     plan = dmr.dmr_grouped_gated_linear_plan
     assert plan(1 << 20, 16, 64, 64, torch.bfloat16)["one_kernel"] and not plan(1 << 20, 16, 72, 64, torch.bfloat16)["one_kernel"]
