@@ -203,6 +203,20 @@ def test_gated_autograd(dmr):
             dmr.grouped_gated_linear(dual, offd, w)
 
 
+@pytest.mark.parametrize("act", ACTIVATIONS)
+def test_gated_activations_of_very_large_arguments(dmr, act):
+    # a = 1e25 and -1e25 (whose squares pass float32's range), u = 1
+    x, off = torch.ones((2, 1), device=DEV), torch.tensor([0, 1, 2], device=DEV)
+    w = torch.tensor([[[[1e25]], [[1.0]]], [[[-1e25]], [[1.0]]]], device=DEV)
+    high, slope = (1.0, 0.0) if act == "sigmoid" else (float(w[0, 0, 0, 0]), 1.0)
+    for cout in (1, 130):       # both forms of the backward pass
+        wide = w.expand(2, 2, cout, 1).contiguous()
+        y = dmr.grouped_gated_linear(x, off, wide, None, act)
+        assert (y[0] == high).all() and (y[1] == 0).all()
+        _, gw, _ = _backward(dmr, x, off, wide, None, torch.ones_like(y), act)
+        assert (gw[0, 0] == slope).all() and (gw[0, 1] == high).all() and (gw[1] == 0).all()
+
+
 def test_gated_refusals(dmr):
     x, w = torch.zeros((4, 8), device=DEV), torch.zeros((2, 2, 3, 8), device=DEV)
     off = torch.tensor([0, 1, 4], dtype=torch.int64, device=DEV)
