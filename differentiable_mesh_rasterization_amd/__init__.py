@@ -628,7 +628,7 @@ def dmr_grouped_layer_norm_fwd(x: torch.Tensor, row_offsets: torch.Tensor, weigh
         _check(bias, "bias", dt, dev, (N, C), optional=True)
         _check(y, "y", dt, dev, (R, C))
     _launch(lib().dmr_grouped_layer_norm_fwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, _address(weight),
-            _address(bias), eps, code, y.data_ptr())
+            _address(bias), float(eps), code, y.data_ptr())
 
 
 def dmr_grouped_layer_norm_workspace_size(R: int, N: int, features: int, dtype: torch.dtype) -> int:
@@ -652,8 +652,8 @@ def dmr_grouped_layer_norm_bwd(x: torch.Tensor, row_offsets: torch.Tensor, weigh
         _check(grad_weight, "grad_weight", dt, dev, (N, C), optional=True)
         _check(grad_bias, "grad_bias", dt, dev, (N, C), optional=True)
     _check(workspace, "workspace", torch.uint8, dev, optional=not sums)
-    _launch(lib().dmr_grouped_layer_norm_bwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, _address(weight), eps, code,
-            grad_y.data_ptr(), _address(grad_x), _address(grad_weight), _address(grad_bias), _address(workspace),
+    _launch(lib().dmr_grouped_layer_norm_bwd, dev, x.data_ptr(), R, C, row_offsets.data_ptr(), N, _address(weight), float(eps),
+            code, grad_y.data_ptr(), _address(grad_x), _address(grad_weight), _address(grad_bias), _address(workspace),
             0 if workspace is None else workspace.numel())
 
 
@@ -771,17 +771,18 @@ def dmr_clip_norm(tensors: Sequence[torch.Tensor], outs: Sequence[torch.Tensor],
     _check_overlap(tensors, outs)
     _check(norms, "norms", torch.float32, dev, (groups,))
     _check(workspace, "workspace", torch.uint8, dev, optional=True)
-    _launch(lib().dmr_clip_norm, dev, table, len(tensors), groups, max_norm, eps, norms.data_ptr(), _address(workspace),
-            0 if workspace is None else workspace.numel())
+    _launch(lib().dmr_clip_norm, dev, table, len(tensors), groups, float(max_norm), float(eps), norms.data_ptr(),
+            _address(workspace), 0 if workspace is None else workspace.numel())
 
 
 def _check_overlap(tensors, outs) -> None:
     """An output may be its own tensor; it may not share memory with another, or with another output."""
     pieces = []
-    for k, (t, o) in enumerate(zip(tensors, outs)):
+    for t, o in zip(tensors, outs):
         for is_out, v in ((False, t), (True, o)):
             if v.numel() and not (is_out and v.data_ptr() == t.data_ptr()):
-                pieces.append((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size(), is_out or o.data_ptr() == t.data_ptr()))
+                written = is_out or o.data_ptr() == t.data_ptr()
+                pieces.append((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size(), written))
     pieces.sort()
     end, written = 0, 0     # of all pieces so far, and of those that are written
     for lo, hi, out in pieces:
@@ -1136,7 +1137,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, groups: Optio
     size = L.dmr_clip_norm_workspace_size(table, len(grads), count)
     norms = torch.empty(count, dtype=torch.float32, device=dev)
     ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 256 else None   # the least: none is used
-    _launch(L.dmr_clip_norm, dev, table, len(grads), count, max_norm, eps, norms.data_ptr(), _address(ws), size)
+    _launch(L.dmr_clip_norm, dev, table, len(grads), count, float(max_norm), float(eps), norms.data_ptr(), _address(ws), size)
     if out is not None:
         for o in outs:      # what autograd saved of them is not what they hold now
             torch.autograd.graph.increment_version(o)
