@@ -21,9 +21,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libdmr.so")
 SOURCES = ["api.hip", "raster_fwd.hip", "raster_bwd.hip", "blend.hip", "project.hip", "points.hip",
-           "grouped_linear.hip", "orthogonalize.hip", "grouped_layer_norm.hip", "clip_norm.hip",
+           "grouped_linear.hip", "grouped_linear_pairs.hip", "orthogonalize.hip", "grouped_layer_norm.hip", "clip_norm.hip",
            "grouped_gated.hip"]
-HEADERS = ["dmr_internal.h", "lds_accum.h", "mfma_tile.h", "grouped_tiles.h", os.path.join("..", "..", "include", "dmr.h")]
+HEADERS = ["dmr_internal.h", "lds_accum.h", "mfma_tile.h", "grouped_tiles.h", "grouped_linear.h", os.path.join("..", "..", "include", "dmr.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -443,6 +443,7 @@ struct GroupedLinearArgs {
     const void* grad_y; void* grad_x; void* grad_weight; void* grad_bias;   // backward
     float* workspace;
     hipStream_t stream;
+    const void *x_low, *weight_low, *grad_y_low;   // of pairs
 };
 // How the backward pass cuts long groups' rows: rows of a piece, the side of
 // a tile, and the float32 partial results (slots) that the workspace holds.
@@ -467,6 +468,10 @@ __host__ __device__ __forceinline__ int64_t grouped_piece_values(int32_t cin, in
 }
 hipError_t launch_grouped_linear_forward(const GroupedLinearArgs& a);
 hipError_t launch_grouped_linear_backward(const GroupedLinearArgs& a);
+// From grad_y + grad_y_low, both bfloat16, where dtype is a 16-bit type. In
+// float16 x and weight are such pairs too, or float16 where weight_low is null
+// (R <= 16 N and few tiles only).
+hipError_t launch_grouped_linear_backward_pairs(const GroupedLinearArgs& a);
 // Adds the pieces of long groups' sums (of the backward pass' arguments), and
 // whether a launch holds that.
 bool grouped_add_fits(int64_t N, int32_t cin, int32_t cout);
@@ -518,10 +523,12 @@ struct GatedArgs {
 };
 // The columns of each of the two products' tiles, and their rows.
 RowsTile gated_tile(int64_t R, int64_t N, int32_t F, bool half, bool vec);
-// [da du] of all rows, which the workspace begins with.
-inline size_t gated_rows_bytes(int64_t R, int32_t F, dmr_dtype dtype) {
-    return align_up((size_t)R * 2 * F * (dtype == DMR_FLOAT32 ? 4 : 2), 256);
-}
+// [da du] of all rows, which the workspace begins with: float32, or high and
+// low parts in bfloat16, one array after the other.
+inline size_t gated_rows_bytes(int64_t R, int32_t F) { return align_up((size_t)R * 2 * F * 4, 256); }
+// `values` of float16 as pairs of bfloat16, as the workspace holds x and the
+// weight of wide layers.
+inline size_t gated_pair_bytes(int64_t values) { return align_up((size_t)values * 4, 256); }
 // Whether one kernel computes the whole backward pass, and how it cuts the rows.
 bool gated_narrow(int32_t C, int32_t F);
 GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half);

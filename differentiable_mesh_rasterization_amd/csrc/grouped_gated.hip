@@ -12,8 +12,15 @@
 // are computed again, with da and du instead of y as their result: only x is
 // kept of the forward pass, and act's arguments are float32. (Keeping a and u
 // would take 4 F values of traffic for 4 F C operations, even at C of about
-// 500 in 16 bits, and round them.) [da du] is rounded to the type, which is
-// what the matrix instructions of the two products with it take.
+// 500 in 16 bits, and round them.)
+//
+// In 16-bit layers [da du] is held as pairs of bfloat16, high + low, which keep
+// 16 bits or more of it and float32's range: rounded to the type once, it would
+// bring an error of the size of the results' own rounding into them, and in
+// float16 gradients below 2^-25 would vanish and products of an upstream
+// gradient with u past 65504 become infinite, whatever the sums over them are.
+// The two products with it take two matrix instructions for one that way, or
+// three with float16 operands, which are pairs of bfloat16 themselves.
 #include <type_traits>
 
 #include "dmr_internal.h"
@@ -234,15 +241,21 @@ struct Biases {
 };
 struct Nothing {};
 
-// GRAD: writes [da du] of the rows to `out` [R, 2 F] from grad_y [R, F];
-// otherwise y to `out` [R, F].
+// What [da du] is held in, as one array or two.
+template <class T>
+using Back = typename std::conditional<sizeof(T) == 2, __bf16, float>::type;
+
+// GRAD: writes [da du] of the rows to `out` [R, 2 F] from grad_y [R, F] (and
+// its low parts behind it); otherwise y to `out` [R, F].
 template <class T, class Tile, bool VEC, bool GRAD>
 __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restrict__ x, int64_t R, int C,
                                                                const int64_t* __restrict__ off, int64_t N,
                                                                const T* __restrict__ weight, const T* __restrict__ bias, int F,
                                                                int act, const T* __restrict__ grad_y, bool wide_g,
-                                                               T* __restrict__ out, bool wide, int64_t tiles, int n_tiles,
-                                                               uint32_t places) {
+                                                               typename std::conditional<GRAD, Back<T>, T>::type* __restrict__ out,
+                                                               bool wide, int64_t tiles, int n_tiles, uint32_t places) {
+    typedef typename std::conditional<GRAD, Back<T>, T>::type Out;
+    constexpr bool PAIRS = GRAD && sizeof(T) == 2;
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
     // Of a thread's number, as it is found anew for every tile: what follows from
     // it would be formed once and kept in scratch memory, for registers are short.
@@ -254,12 +267,12 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
     // the 16-byte stores of a wave's part of a tile
     constexpr int kStores = Tile::PAIRED ? Tile::MT * Tile::PN / 2 : Tile::MT * Tile::PN;
     constexpr bool LARGE = sizeof(T) == 2 && Tile::BN == 256;
-    walk_row_tiles<T, Tile, VEC, LARGE ? (GRAD ? 2 : 1) * kStores : 0, LARGE>(
+    walk_row_tiles<T, Tile, VEC, LARGE ? (GRAD ? 4 : 1) * kStores : 0, LARGE>(
         lds, blockIdx.x, gridDim.x, x, R, C, off, N, tiles, n_tiles, places,
         [&](const RowTile& at, int n0) {
             const T* w = weight + (at.group * 2 * F + n0) * (int64_t)C;
-            return typename Tile::Planes(typename Tile::Source{w, C, F - n0},
-                                         typename Tile::Source{w + (int64_t)F * C, C, F - n0});
+            return typename Tile::Planes(typename Tile::PSource{w, C, F - n0, nullptr},
+                                         typename Tile::PSource{w + (int64_t)F * C, C, F - n0, nullptr});
         },
         [&](const RowTile& at, int n0) {
             Biases<T, Tile> b;
@@ -274,9 +287,11 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
         [&](Tile& t, const RowTile& at, int n0, const auto& g) {
             const int tid = thread();
             constexpr int WIDTHS = GRAD ? 2 : 1;
-            const TileOut<T> first = {out + at.first * (int64_t)F * WIDTHS, (int64_t)F * WIDTHS, at.rows, n0, F, wide};
-            TileOut<T> second = first;
+            const TileOut<Out> first = {out + at.first * (int64_t)F * WIDTHS, (int64_t)F * WIDTHS, at.rows, n0, F, wide};
+            TileOut<Out> second = first, first_low = first, second_low = first;
             second.out += F;
+            first_low.out += R * F * WIDTHS;
+            second_low.out += R * F * WIDTHS + F;
             with_activation(act, [&](auto&& activation) {
 #pragma unroll
                 for (int b = 0; b < Tile::MT; ++b) {
@@ -296,9 +311,13 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
                         }
                         __builtin_amdgcn_sched_barrier(0);   // registers are short: block after block
                     }
-                    store_rows<T, Tile, Tile::PN>(first, b, tid, [&](int a) { return t.acc[a][b]; });
+                    store_rows<Out, Tile, Tile::PN>(first, b, tid, [&](int a) { return t.acc[a][b]; });
                     if constexpr (GRAD)
-                        store_rows<T, Tile, Tile::PN>(second, b, tid, [&](int a) { return t.acc[a + Tile::PN][b]; });
+                        store_rows<Out, Tile, Tile::PN>(second, b, tid, [&](int a) { return t.acc[a + Tile::PN][b]; });
+                    if constexpr (PAIRS) {
+                        store_rows<Out, Tile, Tile::PN>(first_low, b, tid, [&](int a) { return low_of(t.acc[a][b]); });
+                        store_rows<Out, Tile, Tile::PN>(second_low, b, tid, [&](int a) { return low_of(t.acc[a + Tile::PN][b]); });
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             });
@@ -311,30 +330,36 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_gated(const T* __restri
 // ---------------------------------------------------------------------------
 // With C <= 64 and F <= 128 a workgroup holds both planes of its group's
 // weight in LDS and the gradient of the weight in its accumulators, and takes
-// a piece of the group's rows, 64 MT rows at a time. Each wave has 16 MT of
-// them: it computes a and u, and da and du from them, which are in its
-// accumulators just as the product with the weight takes its operand (row
-// lane & 15, eight consecutive f of 16-bit types or four of float32), so that
-// grad_x follows without a move. For the sum over rows, [da du] and x go to
-// LDS and each wave takes a quarter of the weight's rows. x, grad_y and grad_x
-// pass memory once: 2 C + F values a row where the general form, with [da du]
-// in memory, moves 3 C + 7 F.
-//
-// What bounds it: 2^20 rows of 64 to 64 in bfloat16 take 126 us (memory alone
-// 80; LDS, vector and matrix instructions each a part, in turn more than at a
-// time), 217632 of 64 to 128 in float32 240 (the float32 products 139). Two
-// workgroups of 128 rows at a time on a compute unit are faster than one (172)
-// and than more waves with fewer rows each (64 rows at a time: 143).
+// a piece of the group's rows, 64 MT rows at a time. 16 MT of them at a time
+// give a and u, and da and du from them, which are in a wave's accumulators
+// just as the product with the weight takes its operand (row lane & 15, eight
+// consecutive f of 16-bit types or four of float32). For the sum over rows,
+// [da du] and x go to LDS and each wave takes an equal part of the weight's
+// rows. x, grad_y and grad_x pass memory once: 2 C + F values a row where the
+// general form, with [da du] in memory, moves 3 C + 7 F.
 //
 // SPLIT: two waves share 16 MT rows, each with half of the columns: of a and u
 // first, of grad_x afterwards, for which they read each other's [da du] from
-// LDS. Where the LDS holds one workgroup, it has eight waves that way.
+// LDS. A workgroup has eight waves that way, and a compute unit one workgroup:
+// the registers (about 200 a lane) hold no second one in 16 bits, nor does the
+// LDS in float32 of more than 64 hidden values. Otherwise a wave has all of its
+// rows' [da du] (float32 of at most 64 hidden values, two workgroups).
+//
+// What bounds it: 2^20 rows of 64 to 64 in bfloat16 take 157 us (memory alone
+// 80; LDS, vector and matrix instructions each a part, in turn more than at a
+// time), in float16 223, 217632 of 64 to 128 in float32 225 (the float32
+// products 139). In bfloat16 of 64 to 64, waves that do not share rows spill
+// (306) or have 16 rows each (194); one part of the pairs in LDS after the
+// other, for two workgroups on a compute unit, 191; 64 rows at a time 193;
+// pieces for 512 workgroups instead of 256, 173.
 template <class T, int FP_, int MT_, bool SPLIT_>
 struct Narrow {
     static constexpr int FP = FP_, MT = MT_, CP = 64, BM = 64 * MT;
     static constexpr bool SPLIT = SPLIT_;
     static constexpr int SHARES = SPLIT ? 2 : 1, THREADS = 256 * SHARES;
     static constexpr bool HALF = sizeof(T) == 2;
+    using B = Back<T>;                                // of [da du], in PARTS
+    static constexpr int PARTS = HALF ? 2 : 1;
     static constexpr int E = 16 / (int)sizeof(T);     // values of 16 bytes
     static constexpr int XS = CP / (4 * E);           // 64-byte slices of x's row, and of
     static constexpr int PS = FP / (4 * E);           // a plane's
@@ -343,11 +368,30 @@ struct Narrow {
     // of the weight's rows
     static constexpr int PB = FP / 16 / SHARES, PW = PS / SHARES, GB = CB / SHARES, WB = 2 * FP / 64 / SHARES;
     using W = OperandTile<T, FP, true, THREADS, CP * (int)sizeof(T)>;
-    using D = OperandTile<T, 2 * FP, false, THREADS>;
-    using X = OperandTile<T, CP, false, THREADS>;
+    using D = OperandTile<B, 2 * FP, false, THREADS>;
+    using X = OperandTile<B, CP, false, THREADS>;
+    // x and the weight are pairs of B themselves: x is held in LDS as such, the
+    // weight's fragments are split as they are read
+    static constexpr bool CROSS = HALF && !__is_same(T, B);
     static constexpr int kW = 2 * W::kBytes, kD = BM * 2 * FP * (int)sizeof(T), kX = BM * CP * (int)sizeof(T);
-    static constexpr int kLdsBytes = kW + kD + kX;
-    static_assert(kLdsBytes <= 160 * 1024, "");
+    static constexpr int kLdsBytes = kW + PARTS * kD + (CROSS ? 2 : 1) * kX;
+    static_assert(kLdsBytes <= 160 * 1024 && (PARTS == 1 || SPLIT), "");
+
+    // out[m] += the product of a fragment of the weight with the parts q[k][m]
+    // of [da du] (low with low is left out).
+    static __device__ __forceinline__ void rows_product(u32x4 p, const u32x4 (&q)[PARTS][MT], f32x4 (&out)[MT]) {
+        u32x4 high = p;
+        if constexpr (CROSS) {
+            high = high_bf16<T>(p);
+            const u32x4 low = low_bf16<T>(p);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) out[m] = mma<B>(low, q[0][m], out[m]);
+        }
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) out[m] = mma<B>(high, q[k][m], out[m]);
+    }
 
     // Blocks of a plane, and of grad_x's columns, are paired in 16 bits so
     // that a lane holds eight consecutive values.
@@ -450,7 +494,7 @@ __global__ __launch_bounds__(L::THREADS, 2) void gated_narrow_grads(
     T* __restrict__ grad_weight, T* __restrict__ grad_bias, float* __restrict__ slots, int64_t slot_count) {
     constexpr int MT = L::MT, E = L::E, PB = L::PB, CB = L::CB;
     __shared__ alignas(16) char lds[L::kLdsBytes];
-    char *const lds_w = lds, *const lds_d = lds + L::kW, *const lds_x = lds_d + L::kD;
+    char *const lds_w = lds, *const lds_d = lds + L::kW, *const lds_x = lds_d + L::PARTS * L::kD;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
     // its 16 MT rows and its share of their columns
     const int first_row = wave % 4 * MT * 16, share = L::SPLIT ? wave / 4 : 0;
@@ -524,50 +568,52 @@ __global__ __launch_bounds__(L::THREADS, 2) void gated_narrow_grads(
                     for (int m = 0; m < MT; ++m) acc[p][a][m] = mma<T>(wf, xs[m][s], acc[p][a][m]);
                 }
             }
-        if (share == 0)
+        if (L::CROSS || share == 0)   // of pairs, each of two waves a part
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int s = 0; s < L::XS; ++s)
-                    *reinterpret_cast<u32x4*>(L::template chunk<typename L::X>(lds_x, first_row + m * 16 + r, s * 4 + q,
-                                                                               L::CP * (int)sizeof(T))) = xs[m][s];
+                for (int s = 0; s < L::XS; ++s) {
+                    u32x4 v = xs[m][s];
+                    if constexpr (L::CROSS) v = share == 0 ? high_bf16<T>(v) : low_bf16<T>(v);
+                    *reinterpret_cast<u32x4*>(L::template chunk<typename L::X>(
+                        lds_x + (L::CROSS ? share * L::kX : 0), first_row + m * 16 + r, s * 4 + q, L::CP * (int)sizeof(T))) = v;
+                }
         if (more) load_x(xs, from + L::BM);
-        u32x4 back[MT][2][L::PW];
+        // where slice s of plane p of this lane's [da du] goes, and all of a row's are
+        const auto place = [&](int k, int m, int p, int s) {
+            return reinterpret_cast<u32x4*>(L::template chunk<typename L::D>(
+                lds_d + k * L::kD, first_row + m * 16 + r, (p * L::PS + s) * 4 + q, 2 * L::FP * (int)sizeof(T)));
+        };
+        u32x4 back[MT][2][L::PW];   // used where these are all of a row's
         with_activation(act, [&](auto&& activation) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m) {
+                const bool exists = from + first_row + m * 16 + r < piece.rows;   // nothing comes of rows that do not
 #pragma unroll
                 for (int s = 0; s < L::PW; ++s) {
                     constexpr int B = L::HALF ? 2 : 1;   // blocks of a slice
-                    f32x4 da[B], du[B];
+                    f32x4 d[2][B];
 #pragma unroll
                     for (int h = 0; h < B; ++h)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const Act v = activation(acc[0][s * B + h][m][i]);
                             const float up = value_of<T>(gs[m][s], 4 * h + i);
-                            da[h][i] = up * acc[1][s * B + h][m][i] * v.slope;
-                            du[h][i] = up * v.value;
+                            d[0][h][i] = exists ? up * acc[1][s * B + h][m][i] * v.slope : 0.0f;
+                            d[1][h][i] = exists ? up * v.value : 0.0f;
                         }
-                    back[m][0][s] = packed<T>(da[0], da[B - 1]);
-                    back[m][1][s] = packed<T>(du[0], du[B - 1]);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        back[m][p][s] = packed<typename L::B>(d[p][0], d[p][B - 1]);
+                        *place(0, m, p, share * L::PW + s) = back[m][p][s];
+                        if constexpr (L::PARTS > 1)
+                            *place(1, m, p, share * L::PW + s) = packed<typename L::B>(low_of(d[p][0]), low_of(d[p][B - 1]));
+                    }
                 }
+            }
         });
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int line = first_row + m * 16 + r;
-            if (from + line >= piece.rows)   // nothing comes of rows that do not exist
-#pragma unroll
-                for (int s = 0; s < L::PW; ++s) back[m][0][s] = back[m][1][s] = u32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int s = 0; s < L::PW; ++s)
-                    *reinterpret_cast<u32x4*>(L::template chunk<typename L::D>(lds_d, line, (p * L::PS + share * L::PW + s) * 4 + q,
-                                                                               2 * L::FP * (int)sizeof(T))) = back[m][p][s];
-        }
         if (more) load_g(gs, from + L::BM);
-        // grad_x of this wave's rows, back(m, p, s) the operand
+        // grad_x of this wave's rows, back_of(part, m, p, s) the operand
         const auto rows_gradient = [&](auto&& back_of) {
             if (!grad_x) return;
             f32x4 out[L::GB][MT];
@@ -580,14 +626,15 @@ __global__ __launch_bounds__(L::THREADS, 2) void gated_narrow_grads(
             for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int s = 0; s < L::PS; ++s) {
-                    u32x4 rows[MT];
+                    u32x4 rows[L::PARTS][MT];
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) rows[m] = back_of(m, p, s);
+                    for (int k = 0; k < L::PARTS; ++k)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) rows[k][m] = back_of(k, m, p, s);
 #pragma unroll
                     for (int c = 0; c < L::GB; ++c) {
                         const u32x4 wf = L::transposed(lds_w + p * L::W::kBytes, s, L::first_of(share * L::GB + c), lane);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) out[c][m] = mma<T>(wf, rows[m], out[c][m]);
+                        L::rows_product(wf, rows, out[c]);
                     }
                 }
             constexpr int STEP = L::HALF ? 2 : 1;
@@ -623,29 +670,35 @@ __global__ __launch_bounds__(L::THREADS, 2) void gated_narrow_grads(
                 }
             }
         };
-        if constexpr (!L::SPLIT) rows_gradient([&](int m, int p, int s) { return back[m][p][s]; });
+        if constexpr (!L::SPLIT) rows_gradient([&](int, int m, int p, int s) { return back[m][p][s]; });
         step_barrier<63>();   // [da du] and x of all waves are in LDS
-        if constexpr (L::SPLIT)
-            rows_gradient([&](int m, int p, int s) {
-                return *reinterpret_cast<const u32x4*>(L::template chunk<typename L::D>(
-                    lds_d, first_row + m * 16 + r, (p * L::PS + s) * 4 + q, 2 * L::FP * (int)sizeof(T)));
-            });
+        if constexpr (L::SPLIT) rows_gradient([&](int k, int m, int p, int s) { return *place(k, m, p, s); });
 #pragma unroll
         for (int s = 0; s < L::BM / (4 * E); ++s) {
-            u32x4 xf[CB];
+            u32x4 xf[CB], xl[CB];
 #pragma unroll
-            for (int c = 0; c < CB; ++c) xf[c] = L::X::fragment(lds_x, s, c * 16, 4, lane);
+            for (int c = 0; c < CB; ++c) {
+                xf[c] = L::X::fragment(lds_x, s, c * 16, 4, lane);
+                if constexpr (L::CROSS) xl[c] = L::X::fragment(lds_x + L::kX, s, c * 16, 4, lane);
+            }
 #pragma unroll
             for (int b = 0; b < L::WB; ++b) {
-                const u32x4 df = L::D::fragment(lds_d, s, (wave * L::WB + b) * 16, 4, lane);
-                if constexpr (L::HALF) {
-                    constexpr uint32_t bits = one_bits<T>();
-                    ones[b] = mma<T>(u32x4{bits, bits, bits, bits}, df, ones[b]);
-                } else {
-                    ones[b] += __builtin_bit_cast(f32x4, df);
-                }
 #pragma unroll
-                for (int c = 0; c < CB; ++c) sum[b][c] = mma<T>(xf[c], df, sum[b][c]);
+                for (int k = 0; k < L::PARTS; ++k) {
+                    const u32x4 df = L::D::fragment(lds_d + k * L::kD, s, (wave * L::WB + b) * 16, 4, lane);
+                    if constexpr (L::HALF) {
+                        constexpr uint32_t bits = one_bits<typename L::B>();
+                        ones[b] = mma<typename L::B>(u32x4{bits, bits, bits, bits}, df, ones[b]);
+                    } else {
+                        ones[b] += __builtin_bit_cast(f32x4, df);
+                    }
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) sum[b][c] = mma<typename L::B>(xf[c], df, sum[b][c]);
+                    if constexpr (L::CROSS)
+                        if (k == 0)
+#pragma unroll
+                            for (int c = 0; c < CB; ++c) sum[b][c] = mma<typename L::B>(xl[c], df, sum[b][c]);
+                }
             }
         }
     }
@@ -700,7 +753,8 @@ constexpr int kShortRows = 8;   // of the weight, a thread's
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void gated_short_weight_grads(const T* __restrict__ x, int64_t R, int C,
                                                                 const int64_t* __restrict__ off, int64_t N,
-                                                                const T* __restrict__ back, int width, bool wide, unsigned blocks,
+                                                                const Back<T>* __restrict__ back, int width, bool wide,
+                                                                unsigned blocks,
                                                                 T* __restrict__ grad_weight, T* __restrict__ grad_bias) {
     constexpr int E = 16 / (int)sizeof(T), PARTS = kShortRows / E;   // 16 bytes of [da du]: eight or four values
     const int64_t n = blockIdx.x / blocks;
@@ -720,12 +774,17 @@ __global__ __launch_bounds__(256) void gated_short_weight_grads(const T* __restr
     }
     for (int64_t r = lo; r < hi; ++r) {
         const u32x4 xr = row_chunk<T, VEC>(x, R, r, c, C, true);
-        u32x4 d[PARTS];
+        constexpr bool PAIRS = sizeof(T) == 2;
+        u32x4 d[PARTS], low[PARTS];
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) d[p] = row_chunk<T, VEC>(back, R, r, (int)f + p * E, width, true);
+        for (int p = 0; p < PARTS; ++p) {
+            d[p] = row_chunk<Back<T>, VEC>(back, R, r, (int)f + p * E, width, true);
+            if constexpr (PAIRS) low[p] = row_chunk<Back<T>, VEC>(back + R * width, R, r, (int)f + p * E, width, true);
+        }
 #pragma unroll
         for (int k = 0; k < kShortRows; ++k) {
-            const float v = value_of<T>(d[k / E], k % E);
+            float v = value_of<Back<T>>(d[k / E], k % E);
+            if constexpr (PAIRS) v += value_of<Back<T>>(low[k / E], k % E);
             total[k] += v;
 #pragma unroll
             for (int e = 0; e < E; ++e) sum[k][e] = __builtin_fmaf(v, value_of<T>(xr, e), sum[k][e]);
@@ -766,14 +825,14 @@ hipError_t launch_short(const GatedArgs& a) {
     const bool whole = a.C % each == 0, vec = whole && 2 * a.F % each == 0 && aligned16(a.x);
     const auto kernel = vec ? gated_short_weight_grads<T, true> : gated_short_weight_grads<T, false>;
     kernel<<<(unsigned)(blocks * a.N), 256, 0, a.stream>>>(static_cast<const T*>(a.x), a.R, a.C, a.off, a.N,
-                                                           reinterpret_cast<const T*>(a.workspace), 2 * a.F,
+                                                           reinterpret_cast<const Back<T>*>(a.workspace), 2 * a.F,
                                                            whole && aligned16(a.grad_weight), (unsigned)blocks,
                                                            static_cast<T*>(a.grad_weight), static_cast<T*>(a.grad_bias));
     return hipGetLastError();
 }
 
-template <class T, class Tile, bool GRAD>
-hipError_t launch_tile(const GatedArgs& a, T* out, bool vec, bool wide_g, bool wide) {
+template <class T, class Tile, bool GRAD, class Out>
+hipError_t launch_tile(const GatedArgs& a, Out* out, bool vec, bool wide_g, bool wide) {
     const int n_tiles = ceil_div(a.F, Tile::COLUMNS);
     // of rows, whole bands of four
     const int64_t tiles = (most_row_tiles(a.R, a.N, Tile::BM) + 3) / 4 * 4 * n_tiles;
@@ -796,8 +855,8 @@ hipError_t launch_tile(const GatedArgs& a, T* out, bool vec, bool wide_g, bool w
 template <class T, int BN, int BM, int WN, int WM, int S>
 using GatedTile = TileProduct<T, BN, BM, WN, WM, true, true, S, false, 2>;
 
-template <class T, bool GRAD>
-hipError_t launch_products(const GatedArgs& a, T* out) {
+template <class T, bool GRAD, class Out>
+hipError_t launch_products(const GatedArgs& a, Out* out) {
     constexpr int each = 16 / (int)sizeof(T);
     const bool vec = a.C % each == 0 && aligned16(a.x) && aligned16(a.weight);
     const bool whole = a.F % each == 0, wide = whole && aligned16(out), wide_g = whole && aligned16(a.grad_y);
@@ -810,6 +869,45 @@ hipError_t launch_products(const GatedArgs& a, T* out) {
     return launch_tile<T, GatedTile<T, 128, 128, 2, 4, 2>, GRAD>(a, out, vec, wide_g, wide);
 }
 
+// ---------------------------------------------------------------------------
+// float16 operands of the products with [da du]
+// ---------------------------------------------------------------------------
+// Splits n values into pairs of bfloat16, exactly: the high parts and, behind
+// them, the low ones. (Splitting fragments as they are read takes more time of
+// the vector units than the products take, but where there are few rows, it
+// saves the weights' way to memory and back.)
+__global__ __launch_bounds__(256) void gated_split(const _Float16* __restrict__ in, int64_t n, __bf16* __restrict__ out) {
+    const int64_t step = (int64_t)gridDim.x * 256 * 8;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += step) {
+        if (i + 8 <= n) {
+            u32x4 raw;
+            __builtin_memcpy(&raw, in + i, 16);
+            const u32x4 high = high_bf16<_Float16>(raw), low = low_bf16<_Float16>(raw);
+            __builtin_memcpy(out + i, &high, 16);
+            __builtin_memcpy(out + n + i, &low, 16);
+        } else {
+            for (int64_t k = i; k < n; ++k) {
+                out[k] = (__bf16)(float)in[k];
+                out[n + k] = (__bf16)low_of((float)in[k]);
+            }
+        }
+    }
+}
+
+const __bf16* launch_split(const void* in, int64_t n, char* to, bool needed, hipStream_t stream) {
+    __bf16* out = reinterpret_cast<__bf16*>(to);
+    const int64_t blocks = (n + 2047) / 2048;
+    if (needed && n > 0)
+        gated_split<<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, stream>>>(static_cast<const _Float16*>(in), n, out);
+    return out;
+}
+
+// Whether x and the weight are split in the workspace: where the products take
+// more than the smallest tiles.
+bool gated_splits(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype) {
+    return dtype == DMR_FLOAT16 && (R > 16 * N || (double)N * ceil_div(C, 64) * ceil_div(2 * F, 64) > (double)(1 << 22));
+}
+
 template <class T>
 hipError_t launch_typed(const GatedArgs& a, bool backward) {
     if (!backward) return launch_products<T, false>(a, static_cast<T*>(a.y));
@@ -818,14 +916,14 @@ hipError_t launch_typed(const GatedArgs& a, bool backward) {
     b.grad_x = a.grad_x; b.grad_weight = a.grad_weight; b.grad_bias = a.grad_bias; b.stream = a.stream;
     if (gated_narrow(a.C, a.F)) {
         const GroupedPieces p = gated_pieces(a.R, a.N, a.C, a.F, sizeof(T) == 2);
-        const hipError_t err = a.F <= 64 ? launch_narrow<T, Narrow<T, 64, sizeof(T) == 2 ? 2 : 1, false>>(a, p)
+        const hipError_t err = a.F <= 64 ? launch_narrow<T, Narrow<T, 64, sizeof(T) == 2 ? 2 : 1, sizeof(T) == 2>>(a, p)
                                          : launch_narrow<T, Narrow<T, 128, 1, true>>(a, p);
         if (err != hipSuccess || p.slots == 0 || !(a.grad_weight || a.grad_bias)) return err;
         b.workspace = reinterpret_cast<float*>(a.workspace);
         return launch_grouped_add_pieces(b, p);
     }
     if (a.R > 0) {
-        const hipError_t err = launch_products<T, true>(a, reinterpret_cast<T*>(a.workspace));
+        const hipError_t err = launch_products<T, true>(a, reinterpret_cast<Back<T>*>(a.workspace));
         if (err != hipSuccess) return err;
     }
     if ((a.grad_weight || a.grad_bias) && gated_short(a.R, a.N, a.C, a.F, sizeof(T) == 2)) {
@@ -835,8 +933,27 @@ hipError_t launch_typed(const GatedArgs& a, bool backward) {
     }
     // [da du] as the upstream gradient of a linear layer of 2 F outputs
     b.grad_y = a.workspace;
-    b.workspace = reinterpret_cast<float*>(a.workspace + gated_rows_bytes(a.R, a.F, a.dtype));
-    return launch_grouped_linear_backward(b);
+    char* rest = a.workspace + gated_rows_bytes(a.R, a.F);
+    if constexpr (sizeof(T) == 4) {
+        b.workspace = reinterpret_cast<float*>(rest);
+        return launch_grouped_linear_backward(b);
+    }
+    b.grad_y_low = reinterpret_cast<const __bf16*>(a.workspace) + a.R * 2 * a.F;
+    if (gated_splits(a.R, a.N, a.C, a.F, a.dtype)) {
+        const int64_t rows = a.R * a.C, weights = a.N * 2 * a.F * a.C;
+        const __bf16* x = launch_split(a.x, rows, rest, b.grad_weight || b.grad_bias, a.stream);
+        rest += gated_pair_bytes(rows);
+        const __bf16* w = launch_split(a.weight, weights, rest, b.grad_x, a.stream);
+        rest += gated_pair_bytes(weights);
+        b.x = x;
+        b.x_low = x + rows;
+        b.weight = w;
+        b.weight_low = w + weights;
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    b.workspace = reinterpret_cast<float*>(rest);
+    return launch_grouped_linear_backward_pairs(b);
 }
 
 }  // namespace
@@ -862,7 +979,7 @@ bool gated_narrow(int32_t C, int32_t F) { return C <= 64 && F <= 128; }
 // compute unit, or one), of at least 128 rows.
 GroupedPieces gated_pieces(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
     if (!gated_narrow(C, F)) return grouped_pieces(R, N, C, 2 * F, half);
-    const int64_t want = F <= 64 ? 512 : 256;
+    const int64_t want = F <= 64 && !half ? 512 : 256;
     int64_t rows = (R + want - 1) / want;
     rows = (rows + 127) / 128 * 128;
     rows = rows < 128 ? 128 : rows > 8192 ? 8192 : rows;
@@ -888,7 +1005,9 @@ bool gated_short(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
 size_t gated_workspace(int64_t R, int64_t N, int32_t C, int32_t F, dmr_dtype dtype) {
     const GroupedPieces p = gated_pieces(R, N, C, F, dtype != DMR_FLOAT32);
     const size_t sums = align_up((size_t)(p.slots * grouped_piece_values(C, 2 * F)) * sizeof(float) + 256, 256);
-    return sums + (gated_narrow(C, F) ? 0 : gated_rows_bytes(R, F, dtype));
+    if (gated_narrow(C, F)) return sums;
+    const size_t pairs = gated_splits(R, N, C, F, dtype) ? gated_pair_bytes(R * C) + gated_pair_bytes(N * 2 * F * C) : 0;
+    return sums + gated_rows_bytes(R, F) + pairs;
 }
 
 hipError_t launch_gated(const GatedArgs& a, bool backward) {

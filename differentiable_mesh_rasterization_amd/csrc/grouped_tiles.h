@@ -182,12 +182,13 @@ __device__ __forceinline__ void store_tile(const Tile& t, T* __restrict__ out, i
 // store() at least, if `stores`; the next tile's first steps do not wait for
 // them. BANDS: the 32 tiles that a die works on together are four of rows by
 // eight of columns, rather than one of rows and the whole of a wide weight,
-// which its L2 does not hold.
+// which its L2 does not hold. rows_low: the rows' low parts, of tiles of pairs.
 template <class T, class Tile, bool VEC, int YOUNGER = 0, bool BANDS = false, class Weights, class Start, class Load, class Store>
 __device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32_t blocks, const T* __restrict__ rows_in,
                                                int64_t R, int k_in, const int64_t* __restrict__ off, int64_t N,
                                                int64_t tiles, int n_tiles, uint32_t places, Weights&& weights,
-                                               Start&& start, Load&& load, Store&& store, bool stores = false) {
+                                               Start&& start, Load&& load, Store&& store, bool stores = false,
+                                               const T* __restrict__ rows_low = nullptr) {
     const int tid = threadIdx.x;
     bool stored = false;
     // A place's tile of rows; its tile of columns goes to `c`.
@@ -218,7 +219,8 @@ __device__ __forceinline__ void walk_row_tiles(char* lds, uint32_t block, uint32
         return r;
     };
     const auto rows_of = [&](const RowTile& at) {
-        return typename Tile::Source{rows_in + at.first * (int64_t)k_in, k_in, at.rows};
+        return typename Tile::Source{rows_in + at.first * (int64_t)k_in, k_in, at.rows,
+                                     rows_low ? rows_low + at.first * (int64_t)k_in : nullptr};
     };
     // A workgroup that takes several tiles finds the next one while a tile is
     // multiplied and issues its first loads before it stores.

@@ -75,6 +75,36 @@ __device__ __forceinline__ f32x4 mma<float>(u32x4 p, u32x4 q, f32x4 c) {
     return c;
 }
 
+// What is left of v beside its high part in bfloat16 (nothing beside one that
+// is not finite).
+__device__ __forceinline__ float low_of(float v) {
+    const float high = (float)(__bf16)v;
+    return __builtin_fabsf(high) < __builtin_inff() ? v - high : 0.0f;
+}
+__device__ __forceinline__ f32x4 low_of(f32x4 v) { return f32x4{low_of(v[0]), low_of(v[1]), low_of(v[2]), low_of(v[3])}; }
+
+// Both parts of a fragment's eight values as bfloat16.
+template <class T>
+__device__ __forceinline__ u32x4 high_bf16(u32x4 raw) {
+    T v[8];
+    __bf16 out[8];
+    __builtin_memcpy(v, &raw, 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = (__bf16)(float)v[i];
+    __builtin_memcpy(&raw, out, 16);
+    return raw;
+}
+template <class T>
+__device__ __forceinline__ u32x4 low_bf16(u32x4 raw) {
+    T v[8];
+    __bf16 out[8];
+    __builtin_memcpy(v, &raw, 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = (__bf16)low_of((float)v[i]);
+    __builtin_memcpy(&raw, out, 16);
+    return raw;
+}
+
 // One operand's staged step: ROWS rows of KB bytes of k (K-major: 128).
 // SPREAD: M-major fragments of 16-bit rows are paired.
 //
@@ -249,30 +279,50 @@ __device__ __forceinline__ void step_barrier() {
 // holds eight consecutive n. SUMS: sum over k of Q[m][k] as well.
 // PLANES: P is that many matrices, the same COLUMNS = BN / PLANES of n of each:
 // a lane holds the same n of them in blocks PN apart.
-template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int S, bool SUMS = false, int PLANES = 1>
+// TERMS of 2 or 3: Q is a pair of matrices, high + low (which hold twice the
+// bits of T's significand), and the sum of the products with each is formed.
+// Three where P is a pair as well: the third is P's low part with Q's high one
+// (low with low is at most 2^-16 of the product). A step takes all parts where
+// the LDS holds two workgroups so (INNER); larger tiles take the terms one after
+// another, as one sum over k of TERMS times the steps. P's type PT may be another
+// than T = bfloat16: its float16 values are pairs of bfloat16 exactly, and those
+// are formed as fragments are multiplied (of INNER tiles). OUT: the results'.
+template <class T, int BN_, int BM_, int WN, int WM, bool PK, bool QK, int S, bool SUMS = false, int PLANES = 1, class PT = T,
+          int TERMS = 1, class OUT = PT>
 struct TileProduct {
     static constexpr int BN = BN_, BM = BM_, THREADS = WN * WM * 64, COLUMNS = BN / PLANES;
     static constexpr int NT = BN / WN / 16, MT = BM / WM / 16, PN = NT / PLANES;
     static constexpr int BK = kStepBytes / (int)sizeof(T);
     static constexpr bool PAIRED = sizeof(T) == 2 && PN % 2 == 0;
-    using P = OperandTile<T, COLUMNS, PK, THREADS, kStepBytes, PAIRED>;
+    using P = OperandTile<PT, COLUMNS, PK, THREADS, kStepBytes, PAIRED>;
     using Q = OperandTile<T, BM, QK, THREADS>;
-    static constexpr int kP = PLANES * P::kBytes, kStage = kP + Q::kBytes, kLdsBytes = S * kStage;
+    using PType = PT;
+    using Out = OUT;
+    static constexpr bool SPLIT = !__is_same(T, PT);
+    static constexpr bool INNER = TERMS > 1 && S * ((TERMS == 3 && !SPLIT ? 2 : 1) * P::kBytes + 2 * Q::kBytes) <= 80 * 1024;
+    static_assert((!SPLIT || (TERMS == 3 && INNER)) && sizeof(T) == sizeof(PT) && (TERMS == 1 || PLANES == 1), "");
+    // matrices of a step
+    static constexpr int PS = INNER && TERMS == 3 && !SPLIT ? 2 : PLANES, QS = INNER ? 2 : 1;
+    static constexpr int kP = PS * P::kBytes, kStage = kP + QS * Q::kBytes, kLdsBytes = S * kStage;
     static_assert(S >= 2 && kLdsBytes <= 160 * 1024 && PN * PLANES == NT, "");
 
-    struct Source {   // an operand, at row 0 of the tile and k = 0
-        const T* at;
+    template <class E>
+    struct Operand {   // at row 0 of the tile and k = 0
+        const E* at;
         int64_t ld;
-        int rows;   // that exist
+        int rows;       // that exist
+        const E* low;   // of a pair
     };
+    using Source = Operand<T>;
+    using PSource = Operand<PT>;
     struct Planes {   // of the same ld and rows
-        Source plane[PLANES];
-        __device__ __forceinline__ const Source& operator[](int i) const { return plane[i]; }
-        __device__ __forceinline__ Planes(const Source& s) : plane{s} {}
-        __device__ __forceinline__ Planes(const Source& s, const Source& t) : plane{s, t} {}
+        PSource plane[PLANES];
+        __device__ __forceinline__ const PSource& operator[](int i) const { return plane[i]; }
+        __device__ __forceinline__ Planes(const PSource& s) : plane{s} {}
+        __device__ __forceinline__ Planes(const PSource& s, const PSource& t) : plane{s, t} {}
     };
     struct Fragments {
-        u32x4 p[NT], q[MT];
+        u32x4 p[NT], q[MT], p_low[PS > PLANES ? NT : 1], q_low[QS > 1 ? MT : 1];
     };
 
     f32x4 acc[NT][MT];
@@ -288,37 +338,78 @@ struct TileProduct {
         return ((tid >> 6) / WN) * MT * 16 + b * 16 + (tid & 15);
     }
 
-    template <bool VEC, class Operand>
-    static __device__ __forceinline__ void stage(char* lds, const Source& s, const typename Operand::Offsets& o, int k0, int K,
-                                                 int tid) {
+    // Of step t, of `each` steps a term: its first k, and whose low part it takes.
+    struct Step {
+        int k0;
+        bool p_low, q_low;
+    };
+    static __device__ __forceinline__ Step step(int t, int each) {
+        if constexpr (TERMS == 1 || INNER) return {t * BK, false, false};
+        const int term = (t >= each ? 1 : 0) + (TERMS > 2 && t >= 2 * each ? 1 : 0);
+        return {(t - term * each) * BK, term == 2, term == 1};
+    }
+    static __device__ __forceinline__ int all_steps(int each) { return TERMS > 1 && !INNER ? TERMS * each : each; }
+    // Matrix i of a step's.
+    static __device__ __forceinline__ const PT* p_of(const Planes& p, int i, const Step& s) {
+        if constexpr (PS > PLANES) return i == 0 ? p[0].at : p[0].low;
+        else return TERMS > 1 && s.p_low ? p[i].low : p[i].at;
+    }
+    static __device__ __forceinline__ const T* q_of(const Source& q, int i, const Step& s) {
+        if constexpr (QS > 1) return i == 0 ? q.at : q.low;
+        else return TERMS > 1 && s.q_low ? q.low : q.at;
+    }
+
+    template <bool VEC, class Tile, class E>
+    static __device__ __forceinline__ void stage(char* lds, const E* at, const Operand<E>& s, const typename Tile::Offsets& o,
+                                                 int k0, int K, int tid) {
         if constexpr (VEC) {
-            Operand::stage(lds, s.at, s.ld, o, k0, K, tid);
+            Tile::stage(lds, at, s.ld, o, k0, K, tid);
         } else {
-            typename Operand::Held h;
-            Operand::fetch(h, s.at, s.ld, s.rows, k0, K, tid);
-            Operand::put(lds, h, tid);
+            typename Tile::Held h;
+            Tile::fetch(h, at, s.ld, s.rows, k0, K, tid);
+            Tile::put(lds, h, tid);
         }
     }
 
-    static __device__ __forceinline__ void read(Fragments& f, const char* lds_p, const char* lds_q, int kk, int tid) {
-        const int lane = tid & 63, wn = (tid >> 6) % WN, wm = (tid >> 6) / WN;
+    static __device__ __forceinline__ void read_p(u32x4 (&p)[NT], const char* lds_p, int kk, int tid) {
+        const int lane = tid & 63, wn = (tid >> 6) % WN;
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
             const char* plane = lds_p + a / PN * P::kBytes;
             const int c = a % PN;
             if constexpr (PAIRED && !PK) {
-                if (c % 2 == 0) paired_fragments<P>(plane, kk, wn * PN * 16 + c * 16, lane, f.p[a], f.p[a + 1]);
-            } else f.p[a] = P::fragment(plane, kk, wn * PN * 16 + (PAIRED ? (c >> 1) * 32 + 4 * (c & 1) : c * 16), PAIRED ? 8 : 4, lane);
+                if (c % 2 == 0) paired_fragments<P>(plane, kk, wn * PN * 16 + c * 16, lane, p[a], p[a + 1]);
+            } else p[a] = P::fragment(plane, kk, wn * PN * 16 + (PAIRED ? (c >> 1) * 32 + 4 * (c & 1) : c * 16), PAIRED ? 8 : 4, lane);
         }
+    }
+    static __device__ __forceinline__ void read_q(u32x4 (&q)[MT], const char* lds_q, int kk, int tid) {
+        const int lane = tid & 63, wm = (tid >> 6) / WN;
 #pragma unroll
-        for (int b = 0; b < MT; ++b) f.q[b] = Q::fragment(lds_q, kk, (wm * MT + b) * 16, 4, lane);
+        for (int b = 0; b < MT; ++b) q[b] = Q::fragment(lds_q, kk, (wm * MT + b) * 16, 4, lane);
+    }
+    static __device__ __forceinline__ void read(Fragments& f, const char* lds_p, const char* lds_q, int kk, int tid) {
+        read_p(f.p, lds_p, kk, tid);
+        if constexpr (PS > PLANES) read_p(f.p_low, lds_p + P::kBytes, kk, tid);
+        read_q(f.q, lds_q, kk, tid);
+        if constexpr (QS > 1) read_q(f.q_low, lds_q + Q::kBytes, kk, tid);
     }
 
     __device__ __forceinline__ void multiply(const Fragments& f, bool sums) {
 #pragma unroll
-        for (int a = 0; a < NT; ++a)
+        for (int a = 0; a < NT; ++a) {
+            const u32x4 p = SPLIT ? high_bf16<PT>(f.p[a]) : f.p[a];
 #pragma unroll
-            for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(f.p[a], f.q[b], acc[a][b]);
+            for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(p, f.q[b], acc[a][b]);
+            if constexpr (INNER) {
+#pragma unroll
+                for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(p, f.q_low[b], acc[a][b]);
+                if constexpr (TERMS == 3) {
+                    const u32x4 low = SPLIT ? low_bf16<PT>(f.p[a]) : f.p_low[PS > PLANES ? a : 0];
+#pragma unroll
+                    for (int b = 0; b < MT; ++b) acc[a][b] = mma<T>(low, f.q[b], acc[a][b]);
+                }
+            }
+        }
         if constexpr (SUMS && sizeof(T) == 4) {
             // on the vector units, which are free beside float32 products (a
             // product with ones is half as long again as a 64 x 64 tile's):
@@ -331,7 +422,10 @@ struct TileProduct {
                 constexpr uint32_t w = one_bits<T>();
                 const u32x4 one = {w, w, w, w};
 #pragma unroll
-                for (int b = 0; b < MT; ++b) ones[b] = mma<T>(one, f.q[b], ones[b]);
+                for (int b = 0; b < MT; ++b) {
+                    ones[b] = mma<T>(one, f.q[b], ones[b]);
+                    if constexpr (QS > 1) ones[b] = mma<T>(one, f.q_low[b], ones[b]);
+                }
             }
         }
     }
@@ -339,15 +433,19 @@ struct TileProduct {
     // Issues the loads of the first steps of a product over k in [0, K).
     template <bool VEC>
     static __device__ __forceinline__ void begin(char* lds, const Planes& p, const Source& q, int K, int tid) {
-        const int steps = (K + BK - 1) / BK;
+        const int each = (K + BK - 1) / BK, steps = all_steps(each);
         const typename P::Offsets po = P::offsets(p[0].ld, p[0].rows, tid);
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
 #pragma unroll
         for (int t = 0; t < S; ++t)
             if (t < steps) {
+                const Step s = step(t, each);
 #pragma unroll
-                for (int i = 0; i < PLANES; ++i) stage<VEC, P>(lds + t * kStage + i * P::kBytes, p[i], po, t * BK, K, tid);
-                stage<VEC, Q>(lds + t * kStage + kP, q, qo, t * BK, K, tid);
+                for (int i = 0; i < PS; ++i)
+                    stage<VEC, P>(lds + t * kStage + i * P::kBytes, p_of(p, i, s), p[i % PLANES], po, s.k0, K, tid);
+#pragma unroll
+                for (int i = 0; i < QS; ++i)
+                    stage<VEC, Q>(lds + t * kStage + kP + i * Q::kBytes, q_of(q, i, s), q, qo, s.k0, K, tid);
             }
     }
 
@@ -371,11 +469,11 @@ struct TileProduct {
 #pragma unroll
             for (int b = 0; b < MT; ++b) ones[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (K <= 0) return;
-        const int steps = (K + BK - 1) / BK;
+        const int each = (K + BK - 1) / BK, steps = all_steps(each);
         const typename P::Offsets po = P::offsets(p[0].ld, p[0].rows, tid);
         const typename Q::Offsets qo = Q::offsets(q.ld, q.rows, tid);
         // a wave's loads of a step; they arrive in the order of their issue
-        constexpr int kLoads = VEC ? PLANES * P::kLoadsLeast + Q::kLoadsLeast : 0;
+        constexpr int kLoads = VEC ? PS * P::kLoadsLeast + QS * Q::kLoadsLeast : 0;
         static_assert(YOUNGER == 0 || (S == 2 && VEC && kLoads + YOUNGER < 64), "");
         if (YOUNGER > 0 && younger && S <= steps) step_barrier<(S - 1) * kLoads + YOUNGER>();
         else if (S <= steps) step_barrier<(S - 1) * kLoads>();   // step 0 is here
@@ -385,34 +483,39 @@ struct TileProduct {
         int cur = 0;   // this step's stage
         for (int t = 0; t < steps; ++t) {
             char* const here = lds + cur;
+            const bool add = sums && !step(t, each).p_low;   // Q's parts are added once
             read(second, here, here + kP, 1, tid);
-            multiply(first, sums);
+            multiply(first, add);
             // step t is read, and the loads of step t + 1 have arrived
             if (YOUNGER > 0 && younger && t == 0 && S <= steps) step_barrier<(S - 2) * kLoads + YOUNGER>();
             else if (t - 1 + S < steps) step_barrier<(S - 2) * kLoads>();
             else step_barrier<0>();
             const bool more = t + S < steps;
-            typename P::Held held_p[PLANES];
-            typename Q::Held held_q;
+            typename P::Held held_p[PS];
+            typename Q::Held held_q[QS];
             if (more) {
+                const Step s = step(t + S, each);
                 if constexpr (VEC) {
 #pragma unroll
-                    for (int i = 0; i < PLANES; ++i) P::stage(here + i * P::kBytes, p[i].at, p[i].ld, po, (t + S) * BK, K, tid);
-                    Q::stage(here + kP, q.at, q.ld, qo, (t + S) * BK, K, tid);
+                    for (int i = 0; i < PS; ++i) P::stage(here + i * P::kBytes, p_of(p, i, s), p[0].ld, po, s.k0, K, tid);
+#pragma unroll
+                    for (int i = 0; i < QS; ++i) Q::stage(here + kP + i * Q::kBytes, q_of(q, i, s), q.ld, qo, s.k0, K, tid);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < PLANES; ++i) P::fetch(held_p[i], p[i].at, p[i].ld, p[i].rows, (t + S) * BK, K, tid);
-                    Q::fetch(held_q, q.at, q.ld, q.rows, (t + S) * BK, K, tid);
+                    for (int i = 0; i < PS; ++i) P::fetch(held_p[i], p_of(p, i, s), p[0].ld, p[0].rows, s.k0, K, tid);
+#pragma unroll
+                    for (int i = 0; i < QS; ++i) Q::fetch(held_q[i], q_of(q, i, s), q.ld, q.rows, s.k0, K, tid);
                 }
             }
             cur = cur + kStage == kLdsBytes ? 0 : cur + kStage;
             read(first, lds + cur, lds + cur + kP, 0, tid);   // past the end: not used
-            multiply(second, sums);
+            multiply(second, add);
             if constexpr (!VEC)
                 if (more) {
 #pragma unroll
-                    for (int i = 0; i < PLANES; ++i) P::put(here + i * P::kBytes, held_p[i], tid);
-                    Q::put(here + kP, held_q, tid);
+                    for (int i = 0; i < PS; ++i) P::put(here + i * P::kBytes, held_p[i], tid);
+#pragma unroll
+                    for (int i = 0; i < QS; ++i) Q::put(here + kP + i * Q::kBytes, held_q[i], tid);
                 }
         }
         step_barrier<0>();

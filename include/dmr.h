@@ -506,8 +506,10 @@ dmr_status dmr_grouped_gated_linear_fwd(const void* x, int64_t R, int32_t in_fea
  *     grad_x_r = A_n^T da_r + U_n^T du_r,
  *     grad_weight_n = (sum_r da_r x_r^T, sum_r du_r x_r^T),
  *     grad_bias_n = (sum_r da_r, sum_r du_r)   (zero for an empty group).
- * da and du are rounded to dtype before these products and sums, which are
- * float32 and added in a fixed order: results are the same on every run.
+ * These sums are float32 and added in a fixed order: results are the same on
+ * every run. da and du have float32's range in every type, and 16 bits of their
+ * significands or more; an infinite one makes infinities or NaN of the sums that
+ * it enters, and of no others.
  * workspace: 16-byte aligned, of dmr_grouped_gated_linear_workspace_size()
  * bytes. */
 dmr_status dmr_grouped_gated_linear_bwd(const void* x, int64_t R, int32_t in_features, const int64_t* row_offsets, int64_t N,

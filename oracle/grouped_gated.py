@@ -116,18 +116,25 @@ def gated_forward_bound(x, row_offsets, weight, bias, dtype, activation="silu"):
     return e + UNIT[dtype] * (np.abs(y) + e) + TINY[dtype]
 
 
+# what [da du] is off by as it enters its products, relatively: a rounding to
+# float32; the rest of a pair of bfloat16 (each part off by half a step, 2^-8 of
+# it, at most); with float16 operands as much again for low times low, which is left out
+HELD = {"float32": UNIT["float32"], "float16": 2.0 ** -15, "bfloat16": 2.0 ** -16}
+PRODUCTS = {"float32": 1, "float16": 3, "bfloat16": 2}     # of a term, each added
+
+
 def gated_backward_bound(x, row_offsets, weight, bias, grad_y, dtype, activation="silu"):
-    """[da du] with the errors of its factors and one rounding to the type, then sums as for linear layers."""
+    """[da du] with the errors of its factors and as it is held, then sums as for linear layers."""
     x, weight, bias, g = _doubles(x, weight, bias, grad_y)
     _, u, act, slope, eu, eact, eslope = _parts(x, row_offsets, weight, bias, activation)
     da, du = g * u * slope, g * act
     ea = np.abs(g) * (np.abs(u) * eslope + np.abs(slope) * eu + eslope * eu) + 2 * ROUND * np.abs(da)
     ed = np.abs(g) * eact + ROUND * np.abs(du)
     back, eback = np.stack([da, du], axis=1), np.stack([ea, ed], axis=1)
-    eback = eback + UNIT[dtype] * (np.abs(back) + eback) + TINY[dtype]
+    eback = eback + HELD[dtype] * (np.abs(back) + eback) + 2.0 ** -126   # no type's range but float32's
     value = _products(x, row_offsets, weight, back)
     mag = _products(np.abs(x), row_offsets, np.abs(weight), np.abs(back) + eback)
     extra = _products(np.abs(x), row_offsets, np.abs(weight), eback)
     rows = np.diff(np.asarray(row_offsets, np.int64)).astype(np.float64)
-    terms = (2 * weight.shape[2], rows[:, None, None, None], rows[:, None, None])
+    terms = tuple(PRODUCTS[dtype] * t for t in (2 * weight.shape[2], rows[:, None, None, None], rows[:, None, None]))
     return tuple(sum_error_bound(m, t, v, dtype) + (1 + UNIT[dtype]) * e for m, t, v, e in zip(mag, terms, value, extra))
