@@ -501,7 +501,7 @@ __global__ __launch_bounds__(L::THREADS, 2) void gated_narrow_grads(
     const Piece piece = find_piece(off, N, R, per, (int)blockIdx.x);
     if (piece.group < 0 || piece.slot >= slot_count) return;
     const T* bias_n = bias ? bias + piece.group * 2 * F : nullptr;
-    {
+    {   // (not for an empty group: without rows the call needs no weight)
         typename L::W::Held held[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -509,7 +509,7 @@ __global__ __launch_bounds__(L::THREADS, 2) void gated_narrow_grads(
             for (int i = 0; i < L::W::kLoads; ++i) {
                 const int c = i * L::THREADS + tid, line = c / L::W::kLine;
                 held[p].chunk[i] = row_chunk<T, VEC>(weight, N * 2 * F, (piece.group * 2 + p) * F + line,
-                                                     ((c % L::W::kLine) ^ L::W::swizzle(line)) * E, C, line < F);
+                                                     ((c % L::W::kLine) ^ L::W::swizzle(line)) * E, C, line < F && piece.rows > 0);
             }
 #pragma unroll
         for (int p = 0; p < 2; ++p) L::W::put(lds_w + p * L::W::kBytes, held[p], tid);
@@ -943,7 +943,7 @@ hipError_t launch_typed(const GatedArgs& a, bool backward) {
         const int64_t rows = a.R * a.C, weights = a.N * 2 * a.F * a.C;
         const __bf16* x = launch_split(a.x, rows, rest, b.grad_weight || b.grad_bias, a.stream);
         rest += gated_pair_bytes(rows);
-        const __bf16* w = launch_split(a.weight, weights, rest, b.grad_x, a.stream);
+        const __bf16* w = launch_split(a.weight, weights, rest, b.grad_x && a.R > 0, a.stream);
         rest += gated_pair_bytes(weights);
         b.x = x;
         b.x_low = x + rows;
