@@ -282,7 +282,12 @@ __global__ __launch_bounds__(kThreads) void norm_grads(const T* __restrict__ x, 
     for (int64_t from = begin; from < end;) {
         // the group of row `from`: the last that begins there or before
         n = offsets_upto(off, N, n, from) - 1;
-        if (n < 0 || n >= N) break;
+        if (n < 0) {   // rows before the first group's
+            n = 0;
+            from = bound(off, 0, R);
+            continue;
+        }
+        if (n >= N) break;
         const int64_t lo = bound(off, n, R), hi = bound(off, n + 1, R);
         const int64_t to = hi < end ? hi : end;
         if (to <= from) break;
@@ -531,7 +536,12 @@ __global__ __launch_bounds__(kThreads) void norm_long_sums(const T* __restrict__
     int64_t n = 0;
     for (int64_t from = begin; from < end;) {
         n = offsets_upto(off, N, n, from) - 1;
-        if (n < 0 || n >= N) break;
+        if (n < 0) {   // rows before the first group's
+            n = 0;
+            from = bound(off, 0, R);
+            continue;
+        }
+        if (n >= N) break;
         const int64_t lo = bound(off, n, R), hi = bound(off, n + 1, R);
         const int64_t to = hi < end ? hi : end;
         if (to <= from) break;
