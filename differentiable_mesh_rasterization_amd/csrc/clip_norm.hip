@@ -120,9 +120,12 @@ __device__ __forceinline__ void scale(const T* in, T* out, int64_t n, float c) {
     if (last < n) out[last] = (T)((float)in[last] * c);
 }
 
-// min(1, max_norm / (norm + eps)); NaN for a norm that is one.
+// min(1, max_norm / (norm + eps)); NaN for a norm that is one, and 1 where
+// there is nothing to scale (zero by zero).
 __device__ __forceinline__ float factor(double norm, float max_norm, float eps) {
-    const double q = (double)max_norm / (norm + (double)eps);
+    const double by = norm + (double)eps;
+    if (by == 0.0) return 1.0f;
+    const double q = (double)max_norm / by;
     return q >= 1.0 ? 1.0f : (float)q;
 }
 

@@ -547,8 +547,9 @@ dmr_status dmr_grouped_gated_linear_plan(int64_t R, int64_t N, int32_t in_featur
  *   norms      [groups], overwritten.
  *   workspace  16-byte aligned, of dmr_clip_norm_workspace_size() bytes.
  * Squares are added in float64, in a fixed order; no value's square passes its
- * range. A factor of 1 leaves the values as they are; one of an infinite norm
- * is 0 (which makes infinities NaN), one of a NaN norm NaN. Other groups are
+ * range. A factor of 1 leaves the values as they are, and n_g + eps of zero
+ * gives that factor whatever max_norm is; the factor of an infinite norm is 0
+ * (which makes infinities NaN), that of a NaN norm NaN. Other groups are
  * not touched by it.
  * Errors: negative sizes, missing pointers, an unknown dtype, max_norm or eps
  * not finite or below 0: DMR_ERROR_INVALID_VALUE; more values or groups than a
