@@ -85,16 +85,24 @@ __device__ __forceinline__ double squares(const T* __restrict__ in, int64_t n) {
     return s;
 }
 
+// A factor, by 2^exponent: float32 has not the digits of those below its
+// normal values, but their products with large values have.
+struct Factor {
+    float c;
+    int exponent;
+    __device__ __forceinline__ float operator*(float v) const { return __builtin_ldexpf(v * c, exponent); }
+};
+
 // out = in c; the two may be the same array. STREAM: the stores leave the
 // caches to what is still to be read.
 template <class T, int THREADS, bool STREAM>
-__device__ __forceinline__ void scale(const T* in, T* out, int64_t n, float c) {
+__device__ __forceinline__ void scale(const T* in, T* out, int64_t n, Factor c) {
     const int64_t whole = n / kVector<T>;
     const auto put = [&](u32x4 raw, int64_t i) {
         T v[kVector<T>];
         __builtin_memcpy(v, &raw, 16);
 #pragma unroll
-        for (int e = 0; e < kVector<T>; ++e) v[e] = (T)((float)v[e] * c);
+        for (int e = 0; e < kVector<T>; ++e) v[e] = (T)(c * (float)v[e]);
         if constexpr (STREAM) {
             u32x4_any to;
             __builtin_memcpy(&to, v, 16);
@@ -117,16 +125,19 @@ __device__ __forceinline__ void scale(const T* in, T* out, int64_t n, float c) {
         put(raw, i);
     }
     const int64_t last = whole * kVector<T> + threadIdx.x;
-    if (last < n) out[last] = (T)((float)in[last] * c);
+    if (last < n) out[last] = (T)(c * (float)in[last]);
 }
 
 // min(1, max_norm / (norm + eps)); NaN for a norm that is one, and 1 where
 // there is nothing to scale (zero by zero).
-__device__ __forceinline__ float factor(double norm, float max_norm, float eps) {
+__device__ __forceinline__ Factor factor(double norm, float max_norm, float eps) {
     const double by = norm + (double)eps;
-    if (by == 0.0) return 1.0f;
-    const double q = (double)max_norm / by;
-    return q >= 1.0 ? 1.0f : (float)q;
+    if (by == 0.0) return {1.0f, 0};
+    double q = (double)max_norm / by;
+    if (q >= 1.0) return {1.0f, 0};
+    int exponent = 0;
+    if (q < 0x1p-126) q = __builtin_frexp(q, &exponent);
+    return {(float)q, exponent};
 }
 
 template <class F>
@@ -187,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void clip_scale(const Spans s, int64_t le
     for (int i = threadIdx.x; i < all; i += kThreads) sum += partial[c.group * all + i];
     const double norm = sqrt(workgroup_sum<kThreads / 64>(sum, part));
     if (before == 0 && c.index == 0 && threadIdx.x == 0) norms[c.group] = (float)norm;
-    const float by = factor(norm, max_norm, eps);
+    const Factor by = factor(norm, max_norm, eps);
     const Span& t = s.at[c.tensor];
     const int64_t at = c.group * t.values + c.first;
     typed(t.dtype, [&](auto zero) {
@@ -212,7 +223,7 @@ __global__ __launch_bounds__(kSmallThreads) void clip_small(const Spans s, float
     }
     const double norm = sqrt(workgroup_sum<kSmallThreads / 64>(sum, part));
     if (threadIdx.x == 0) norms[group] = (float)norm;
-    const float by = factor(norm, max_norm, eps);
+    const Factor by = factor(norm, max_norm, eps);
     for (int k = 0; k < s.count; ++k) {
         const Span& t = s.at[k];
         typed(t.dtype, [&](auto zero) {
