@@ -444,6 +444,7 @@ struct GroupedLinearArgs {
     float* workspace;
     hipStream_t stream;
     const void *x_low, *weight_low, *grad_y_low;   // of pairs
+    int32_t long_only;   // not 0: the sums of groups of more rows than this alone, in one piece each
 };
 // How the backward pass cuts long groups' rows: rows of a piece, the side of
 // a tile, and the float32 partial results (slots) that the workspace holds.

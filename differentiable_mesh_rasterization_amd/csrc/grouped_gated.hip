@@ -750,6 +750,12 @@ hipError_t launch_narrow(const GatedArgs& a, const GroupedPieces& p) {
 // rows, of which nearly all are not there.)
 constexpr int kShortRows = 8;   // of the weight, a thread's
 
+// The rows of a group that are added that way at most. Few rows on average may
+// still be nearly all of one group's: longer groups are left to the linear
+// layer's tiles (131072 rows of one group among 32768, 72 to 32 in bfloat16: 4.6 ms
+// so, 71 by a thread's loop; 64 groups of four rows, 512 to 512: 45.6 and 42.7 us).
+constexpr int kShortMost = 64;
+
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void gated_short_weight_grads(const T* __restrict__ x, int64_t R, int C,
                                                                 const int64_t* __restrict__ off, int64_t N,
@@ -760,6 +766,7 @@ __global__ __launch_bounds__(256) void gated_short_weight_grads(const T* __restr
     const int64_t n = blockIdx.x / blocks;
     int64_t lo, hi;
     group_bounds(off, N, R, n, lo, hi);
+    if (hi - lo > kShortMost) return;
     const unsigned chunks = (unsigned)((C + E - 1) / E);
     const unsigned item = (blockIdx.x % blocks) * 256 + threadIdx.x;
     const int c = (int)(item % chunks) * E;
@@ -928,8 +935,10 @@ hipError_t launch_typed(const GatedArgs& a, bool backward) {
     }
     if ((a.grad_weight || a.grad_bias) && gated_short(a.R, a.N, a.C, a.F, sizeof(T) == 2)) {
         const hipError_t err = launch_short<T>(a);
-        if (err != hipSuccess || !a.grad_x || a.R == 0) return err;
-        b.grad_weight = b.grad_bias = nullptr;
+        if (err != hipSuccess) return err;
+        b.long_only = kShortMost;
+        if (a.R <= kShortMost) b.grad_weight = b.grad_bias = nullptr;   // no group is longer
+        if (a.R == 0 || !(b.grad_x || b.grad_weight || b.grad_bias)) return hipSuccess;
     }
     // [da du] as the upstream gradient of a linear layer of 2 F outputs
     b.grad_y = a.workspace;

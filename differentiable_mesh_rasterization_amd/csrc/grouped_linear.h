@@ -69,12 +69,12 @@ __device__ __forceinline__ void weight_grad_of_workgroup(
     char* lds, uint32_t block, const typename Tile::PType* __restrict__ x, const typename Tile::PType* __restrict__ x_low,
     const T* __restrict__ g, const T* __restrict__ g_low, int64_t R, int cin, int cout, const int64_t* __restrict__ off,
     int64_t N, int per, typename Tile::Out* __restrict__ grad_weight, typename Tile::Out* __restrict__ grad_bias, bool wide,
-    float* __restrict__ slots, int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
+    float* __restrict__ slots, int64_t slot_count, int64_t items, int n_tiles, int m_tiles, int shortest = -1) {
     typedef typename Tile::Out Out;
     const int64_t id = tile_of_workgroup<kPieceRun>(block);
     if (id >= items) return;
     const int tiles = n_tiles * m_tiles;
-    const Piece at = find_piece(off, N, R, per, (int)(id / tiles));
+    const Piece at = shortest < 0 ? find_piece(off, N, R, per, (int)(id / tiles)) : find_long(off, N, R, shortest, id / tiles);
     if (at.group < 0 || at.slot >= slot_count) return;
     const int tile = (int)(id % tiles);
     const int n0 = (tile % n_tiles) * Tile::BN, m0 = (tile / n_tiles) * Tile::BM;
@@ -128,10 +128,10 @@ __global__ __launch_bounds__(Tile::THREADS) void grouped_weight_grad(
     const typename Tile::PType* __restrict__ x, const typename Tile::PType* __restrict__ x_low, const T* __restrict__ g,
     const T* __restrict__ g_low, int64_t R, int cin, int cout, const int64_t* __restrict__ off, int64_t N, int per,
     typename Tile::Out* __restrict__ grad_weight, typename Tile::Out* __restrict__ grad_bias, bool wide,
-    float* __restrict__ slots, int64_t slot_count, int64_t items, int n_tiles, int m_tiles) {
+    float* __restrict__ slots, int64_t slot_count, int64_t items, int n_tiles, int m_tiles, int shortest) {
     __shared__ alignas(16) char lds[Tile::kLdsBytes];
     weight_grad_of_workgroup<T, Tile, VEC>(lds, blockIdx.x, x, x_low, g, g_low, R, cin, cout, off, N, per, grad_weight, grad_bias, wide,
-                                           slots, slot_count, items, n_tiles, m_tiles);
+                                           slots, slot_count, items, n_tiles, m_tiles, shortest);
 }
 
 // Both gradients in one launch: the workgroups of the weight's, whose chains
@@ -312,7 +312,9 @@ hipError_t launch_rows(const GroupedLinearArgs& a, const T* in, int k_in, const 
 template <class T, class Tile>
 hipError_t launch_weight_tile(const GroupedLinearArgs& a, const GroupedPieces& p, bool vec, bool wide) {
     const int n_tiles = ceil_div(a.cin, Tile::BN), m_tiles = ceil_div(a.cout, Tile::BM);
-    const int64_t items = (a.R / p.rows + a.N) * n_tiles * m_tiles;
+    const int64_t pieces = a.long_only ? (a.R + a.long_only) / (a.long_only + 1) : a.R / p.rows + a.N;   // at most
+    const int64_t items = pieces * n_tiles * m_tiles;
+    const int shortest = a.long_only ? a.long_only : -1;
     const unsigned grid = run_grid<kPieceRun>(items);
     if (grid == 0) return hipErrorInvalidValue;
     typedef typename Tile::PType PT;
@@ -322,10 +324,10 @@ hipError_t launch_weight_tile(const GroupedLinearArgs& a, const GroupedPieces& p
     Out *gw = static_cast<Out*>(a.grad_weight), *gb = static_cast<Out*>(a.grad_bias);
     if (vec)
         grouped_weight_grad<T, Tile, true><<<grid, Tile::THREADS, 0, a.stream>>>(
-            x, x_low, g, g_low, a.R, a.cin, a.cout, a.off, a.N, p.rows, gw, gb, wide, a.workspace, p.slots, items, n_tiles, m_tiles);
+            x, x_low, g, g_low, a.R, a.cin, a.cout, a.off, a.N, p.rows, gw, gb, wide, a.workspace, p.slots, items, n_tiles, m_tiles, shortest);
     else if constexpr (Tile::BN < 256)
         grouped_weight_grad<T, Tile, false><<<grid, Tile::THREADS, 0, a.stream>>>(
-            x, x_low, g, g_low, a.R, a.cin, a.cout, a.off, a.N, p.rows, gw, gb, wide, a.workspace, p.slots, items, n_tiles, m_tiles);
+            x, x_low, g, g_low, a.R, a.cin, a.cout, a.off, a.N, p.rows, gw, gb, wide, a.workspace, p.slots, items, n_tiles, m_tiles, shortest);
     return hipGetLastError();
 }
 
@@ -405,8 +407,9 @@ hipError_t launch_backward(const GroupedLinearArgs& a) {
     const bool vec_rows = whole && aligned16(a.weight) && aligned16(a.weight_low);
     const bool vec_weights = whole && aligned16(a.x) && aligned16(a.x_low);
     const bool wide_x = in16 && aligned16(a.grad_x), wide_w = in16 && aligned16(a.grad_weight);
-    const GroupedPieces p = weights ? grouped_pieces(a.R, a.N, a.cin, a.cout, sizeof(T) == 2) : GroupedPieces{};
-    const bool together = weights && launch_together<T, PT, OUT, TERMS>(a, p, vec_rows && vec_weights, wide_x, wide_w, err);
+    GroupedPieces p = weights ? grouped_pieces(a.R, a.N, a.cin, a.cout, sizeof(T) == 2) : GroupedPieces{};
+    if (a.long_only) p = {1 << 30, p.side, 0};
+    const bool together = weights && !a.long_only && launch_together<T, PT, OUT, TERMS>(a, p, vec_rows && vec_weights, wide_x, wide_w, err);
     if (!together && a.grad_x && a.R > 0)
         err = launch_rows<T, PT, OUT, TERMS, false>(a, static_cast<const T*>(a.grad_y), a.cout, (const OUT*)nullptr,
                                                     static_cast<OUT*>(a.grad_x), a.cin, vec_rows, wide_x);

@@ -1,9 +1,13 @@
-"""Calls of the gated layers at the edges of what is allowed, through the C ABI."""
+"""Calls of the gated layers at the edges of what is allowed, through the C ABI.
+
+Tolerances: as in test_gpu_gated.py (oracle/grouped_gated.py)."""
 
 import pytest
 import torch
 
 from gpu_util import DEV, require_gpu, say
+from test_gpu_gated import _backward, _check, _inputs
+from oracle.grouped_gated import gated_backward, gated_backward_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +33,20 @@ def test_gated_backward_without_rows_needs_no_inputs(dmr, N, cin, cout, dtype):
                                                     torch.cuda.current_stream().cuda_stream)
         torch.cuda.synchronize()
         assert rc == 0 and (gw == 0).all() and (gb == 0).all()
+
+
+# few rows on average, nearly all of them one group's: aligned and not, few and many tiles
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("before,size,after,cin,cout", [(900, 3000, 400, 72, 40), (40, 65, 30, 131, 260), (2000, 8300, 1000, 67, 33),
+                                                        (20, 64, 30, 136, 320), (30, 400, 100, 136, 200)])
+def test_gated_backward_of_one_long_group_among_many_short_ones(dmr, before, size, after, cin, cout, dtype):
+    say(f"[gpu] gated, {size} rows of one group among {before + after}, {cin}->{cout} {dtype}")
+    sizes = [0, 1, 0, 2] * (before // 4) + [size] + [1, 0] * (after // 2)
+    assert sum(sizes) <= 4 * len(sizes) and len(sizes) * cin * cout >= 1 << 21
+    off, (x, x64), (w, w64), (b, b64), (g, g64) = _inputs(sizes, cin, cout, dtype, cin)
+    offd = torch.from_numpy(off).to(DEV)
+    ref, bound = gated_backward(x64, off, w64, b64, g64), gated_backward_bound(x64, off, w64, b64, g64, dtype)
+    for grads in ((True, True, True), (False, True, False), (False, False, True), (True, False, False)):
+        for got, r, e, what in zip(_backward(dmr, x, offd, w, b, g, grads=grads), ref, bound, ("gx", "gw", "gb")):
+            if got is not None:
+                _check(got, r, e, what)
