@@ -30,10 +30,13 @@
 namespace dmr {
 namespace {
 
-// Activation and derivative. With the logistic function s of z, e^-z may pass
-// float32's range (1 / inf = 0 then). 1 - s is off by 2^-24, which moves the
-// derivative s + a s (1 - s) z' by a s z' 2^-24: no more than the rounding of
-// a does.
+// Activation and derivative. The exponential's argument is rounded twice, which
+// moves it by |z| 2^-23 relatively: so far are negative tails off. With the
+// logistic function s of z, e^-z may pass float32's range (1 / inf = 0 then).
+// 1 - s is off by 2^-24, which moves the derivative s + a s (1 - s) z' by a s z'
+// 2^-24: no more than the rounding of a does. Sigmoid's derivative has no term
+// beside s (1 - s), which is e s^2 with s and e = e^-|a| of the magnitude: both
+// tails keep their digits (by 1 - s it is 7e-4 off at 10, and zero from 17 on).
 struct Act {
     float value, slope;
 };
@@ -53,8 +56,9 @@ __device__ __forceinline__ Act activate<DMR_SILU>(float a) {
 }
 template <>
 __device__ __forceinline__ Act activate<DMR_SIGMOID>(float a) {
-    const float s = logistic2(a * -kLog2e);
-    return {s, s * (1.0f - s)};
+    const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(a) * -kLog2e);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e), below = e * s;
+    return {a < 0.0f ? below : s, below * s};
 }
 template <>
 __device__ __forceinline__ Act activate<DMR_GELU_TANH>(float a) {

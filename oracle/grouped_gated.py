@@ -87,6 +87,38 @@ def _products(x, row_offsets, weight, back):
     return gx, gw, gb
 
 
+def activation_error(a, kind):
+    """Bounds on the errors of act(a) and act'(a) as they are evaluated in binary32 from a itself.
+
+    u = ROUND is the error of a hardware exponential or reciprocal, and of two
+    correct roundings. An exponential e^-z, z formed with r roundings, is off by
+    2 u and r u / 2 times z, relatively: E. The logistic function s = 1 / (1 +
+    e^-z) by (1 - s) E + 3 u, and nothing where e^-z vanishes beside 1.
+    silu, gelu_tanh (v = a s, v' = s + v (1 - s) z'): r is 2 and 5; 1 - s is off
+    by what s is, and a rounding. sigmoid (s and e s^2 of the magnitude; below
+    zero e s): r is 2. gelu: the tail t Q(t) e^(-a^2 / 2) beyond |a|, with t and
+    Q off by 8 u together and the exponential's argument by 3 roundings; the
+    derivative is a e^(-a^2 / 2) / sqrt(2 pi) + its normal distribution.
+    Exponentials below 2^-126 may vanish."""
+    a = np.asarray(a, np.float64)
+    value, slope, first = activate(a, kind)
+    m, gone = np.abs(a), 2.0 ** -125 * (1 + np.abs(a))
+    if kind == "sigmoid":
+        e, s = (2 + m) * ROUND, _logistic(m)
+        es = (1 - s) * e + 3 * ROUND
+        return np.abs(value) * (np.where(a < 0, e, 0.0) + es + ROUND) + gone, slope * (e + 2 * es + 2 * ROUND) + gone
+    if kind == "gelu":
+        e = (2 + 0.75 * a * a) * ROUND
+        tail = activate(-m, kind)[2] * (e + 10 * ROUND)          # of the distribution below -|a|
+        below = tail + ROUND * first
+        return m * below + ROUND * np.abs(value) + gone, below + np.abs(slope - first) * (e + 2 * ROUND) + ROUND * np.abs(slope) + gone
+    r, z, dz = (2, a, 1.0) if kind == "silu" else (5, 2 * K * (a + 0.044715 * a ** 3), 2 * K * (1 + 3 * 0.044715 * a * a))
+    s, rest = _logistic(z), _logistic(-z)
+    es = np.where(rest < 2.0 ** -25, rest, rest * (2 + 0.5 * r * np.abs(z)) * ROUND + 3 * ROUND)    # relative
+    eslope = s * es + np.abs(value) * dz * (s * es + ROUND * rest + rest * (es + 6 * ROUND)) + ROUND * np.abs(slope)
+    return np.abs(value) * (es + ROUND) + gone, eslope + gone * (1 + dz)    # a vanished s in a s z'
+
+
 def _parts(x, row_offsets, weight, bias, activation):
     """a, u, act(a), act'(a), and bounds on the error of each.
 
