@@ -49,6 +49,19 @@ def activate(a, kind):
     return a * s, s + a * s * _logistic(-z) * dz, s
 
 
+def curvature(a, kind):
+    """act''(a)"""
+    a = np.asarray(a, np.float64)
+    if kind == "gelu":
+        return (2 - a * a) * np.exp(-0.5 * a * a) / math.sqrt(2.0 * math.pi)
+    z, dz, ddz = (2 * K * (a + 0.044715 * a ** 3), 2 * K * (1 + 3 * 0.044715 * a * a), 2 * K * 6 * 0.044715 * a) \
+        if kind == "gelu_tanh" else (a, 1.0, 0.0)
+    s, p = _logistic(z), _logistic(z) * _logistic(-z)
+    if kind == "sigmoid":
+        return p * (1 - 2 * s)
+    return 2 * p * dz + a * p * ((1 - 2 * s) * dz * dz + ddz)
+
+
 def _projections(x, row_offsets, weight, bias):
     N, _, F, C = weight.shape
     both = np.zeros((x.shape[0], 2, F))
@@ -87,7 +100,7 @@ def _products(x, row_offsets, weight, back):
     return gx, gw, gb
 
 
-def activation_error(a, kind):
+def activation_error(a, kind, known=None):
     """Bounds on the errors of act(a) and act'(a) as they are evaluated in binary32 from a itself.
 
     u = ROUND is the error of a hardware exponential or reciprocal, and of two
@@ -101,7 +114,7 @@ def activation_error(a, kind):
     derivative is a e^(-a^2 / 2) / sqrt(2 pi) + its normal distribution.
     Exponentials below 2^-126 may vanish."""
     a = np.asarray(a, np.float64)
-    value, slope, first = activate(a, kind)
+    value, slope, first = known or activate(a, kind)
     m, gone = np.abs(a), 2.0 ** -125 * (1 + np.abs(a))
     if kind == "sigmoid":
         e, s = (2 + m) * ROUND, _logistic(m)
@@ -109,7 +122,7 @@ def activation_error(a, kind):
         return np.abs(value) * (np.where(a < 0, e, 0.0) + es + ROUND) + gone, slope * (e + 2 * es + 2 * ROUND) + gone
     if kind == "gelu":
         e = (2 + 0.75 * a * a) * ROUND
-        tail = activate(-m, kind)[2] * (e + 10 * ROUND)          # of the distribution below -|a|
+        tail = np.minimum(first, 0.5 * np.exp(-0.5 * a * a)) * (e + 10 * ROUND)   # of the distribution below -|a|, or a bound
         below = tail + ROUND * first
         return m * below + ROUND * np.abs(value) + gone, below + np.abs(slope - first) * (e + 2 * ROUND) + ROUND * np.abs(slope) + gone
     r, z, dz = (2, a, 1.0) if kind == "silu" else (5, 2 * K * (a + 0.044715 * a ** 3), 2 * K * (1 + 3 * 0.044715 * a * a))
@@ -123,20 +136,17 @@ def _parts(x, row_offsets, weight, bias, activation):
     """a, u, act(a), act'(a), and bounds on the error of each.
 
     a and u are sums of C + 1 products in binary32: (C + 3) u of the sum of
-    absolute values, u = ROUND. act and act' have derivatives of at most 1.13
-    and 1 in magnitude. Their own evaluation is off by 8 roundings, and by
-    those of the exponent: 4 u of its argument, which is at most a^2 + |a| +
-    0.08 |a|^3 (gelu's a^2 / 2, silu's a, gelu_tanh's 1.6 a + 0.08 a^3, with
-    the change of the normal distribution's tail below its density's), each of
-    the value or of the derivative's two terms; below 2^-126 they may vanish."""
+    absolute values, u = ROUND: e. act moves with a by its derivative there, and
+    1/2 e^2 times the second, which is at most 1 in magnitude; act' by the second,
+    and the third is at most 2. Their own evaluation
+    (activation_error) is at a value of a that is e off: a hundredth more."""
     a, u = _projections(x, row_offsets, weight, bias)
     mag = _projections(np.abs(x), row_offsets, np.abs(weight), None if bias is None else np.abs(bias))
     ea, eu = ((x.shape[1] + 3) * ROUND * m for m in mag)
-    act, slope, first = activate(a, activation)
-    own = (8 + 4 * (a * a + 2 * np.abs(a) + 0.08 * np.abs(a) ** 3)) * ROUND
-    gone = 2.0 ** -125 * (1 + np.abs(a))
-    eact = 1.13 * ea + own * np.abs(act) + gone
-    eslope = ea + own * (np.abs(first) + np.abs(slope - first)) + gone
+    act, slope, _ = known = activate(a, activation)
+    own_act, own_slope = activation_error(a, activation, known)
+    eact = 1.01 * (own_act + np.abs(slope) * ea + 0.5 * ea * ea)
+    eslope = 1.01 * (own_slope + np.abs(curvature(a, activation)) * ea + ea * ea)
     return a, u, act, slope, eu, eact, eslope
 
 
