@@ -1058,8 +1058,8 @@ def grouped_layer_norm(x: torch.Tensor, row_offsets: torch.Tensor, weight: Optio
                        bias: Optional[torch.Tensor] = None, eps: float = 1e-5) -> torch.Tensor:
     """The rows of every group n (a mesh's vertices, an image's pixels) with
     mean 0 and variance 1, times weight_n, plus bias_n: x [R, C], row_offsets
-    [N + 1] int64, weight and bias [N, C] or None, all of one type (float32,
-    float16 or bfloat16). Differentiable once with respect to x, weight and
+    [N + 1] int64 from 0 to R, weight and bias [N, C] or None, all of one type
+    (float32, float16 or bfloat16). Differentiable once with respect to x, weight and
     bias (in reverse mode; second derivatives and forward mode raise)."""
     if _wants_grad(x, weight, bias):
         return _GroupedLayerNorm.apply(x, row_offsets, weight, bias, float(eps))
@@ -1101,8 +1101,8 @@ def grouped_gated_linear(x: torch.Tensor, row_offsets: torch.Tensor, weight: tor
                          bias: Optional[torch.Tensor] = None, activation: str = "silu") -> torch.Tensor:
     """y_r = act(A_n x_r + a_n) * (U_n x_r + u_n) for the rows r of every
     group n (a mesh's vertices, an image's pixels), both products in one
-    kernel: x [R, in], row_offsets [N + 1] int64, weight [N, 2, out, in] (A and
-    U), bias [N, 2, out] (a and u) or None, all of one type (float32, float16
+    kernel: x [R, in], row_offsets [N + 1] int64 from 0 to R, weight [N, 2, out,
+    in] (A and U), bias [N, 2, out] (a and u) or None, all of one type (float32, float16
     or bfloat16); activation "silu", "gelu", "gelu_tanh" or "sigmoid".
     Differentiable once with respect to x, weight and bias (in reverse mode;
     second derivatives and forward mode raise); the backward pass keeps only

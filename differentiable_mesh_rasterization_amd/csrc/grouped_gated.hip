@@ -1008,8 +1008,8 @@ bool gated_fits(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
 
 // Whether the weights' gradient is added row by row: where groups have at most
 // four rows on average and the weights are many. (bfloat16, the whole backward
-// pass: 64 groups of one row, 1024 to 1024, 178 us so and 291 otherwise; 256
-// rows in 64 groups, 512 to 512, 43 and 65; but 900 rows 88 and 76, and 200
+// pass: 64 groups of one row, 1024 to 1024, 176 us so and 295 otherwise; 256
+// rows in 64 groups, 512 to 512, 51 and 70; but 900 rows 90 and 79, and 200
 // rows in 100 groups, 65 to 100, where one launch does both gradients, 28 and 17.)
 bool gated_short(int64_t R, int64_t N, int32_t C, int32_t F, bool half) {
     return !gated_narrow(C, F) && R <= 4 * N && (double)N * F * C >= (double)(1 << 21) &&
