@@ -50,3 +50,34 @@ def test_gated_backward_of_one_long_group_among_many_short_ones(dmr, before, siz
         for got, r, e, what in zip(_backward(dmr, x, offd, w, b, g, grads=grads), ref, bound, ("gx", "gw", "gb")):
             if got is not None:
                 _check(got, r, e, what)
+
+
+# the forms of the backward pass that lay operands out in the workspace, or take more launches than float32's
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("sizes,cin,cout", [([300, 0, 1700], 64, 32), ([300, 0, 1700], 136, 72), ([1, 0, 90, 2] + [1] * 60, 136, 300)])
+def test_gated_16_bit_backward_in_a_graph(dmr, sizes, cin, cout, dtype):
+    say(f"[gpu] gated backward in a graph, {cin}->{cout} {dtype}")
+    R, N = sum(sizes), len(sizes)
+    off = torch.tensor([0, *torch.tensor(sizes).cumsum(0).tolist()], device=DEV)
+    x, w, g = (torch.randn(s, device=DEV).to(dtype) for s in ((R, cin), (N, 2, cout, cin), (R, cout)))
+
+    def work():
+        return _backward(dmr, x, off, w, None, g)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for k in range(4):
+        x.copy_(torch.randn_like(x))
+        w.copy_(torch.randn_like(w))
+        eager = work()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
