@@ -524,8 +524,8 @@ size_t dmr_grouped_gated_linear_workspace_size(int64_t R, int64_t N, int32_t in_
  * results do not depend on it but for the order of sums): the tile of a and u,
  * in columns of each and rows; whether one kernel computes the whole backward
  * pass, and the most rows of one of its pieces (otherwise a and u are computed
- * again by that tile, and the rest is dmr_grouped_linear_bwd's). aligned: the
- * arrays start on 16 bytes. */
+ * again by that tile, and the rest is dmr_grouped_linear_bwd's of twice the
+ * outputs, of pairs in 16-bit types). aligned: the arrays start on 16 bytes. */
 typedef struct dmr_gated_plan {
     int32_t columns, rows, one_kernel, piece_rows;
 } dmr_gated_plan;
